@@ -7,11 +7,15 @@ is missing the import of an entry point raises.
 Entry points (same names as the C ABI): ``kda_project_inputs``, ``kda_decode_step``, ``kda_decode_multi``,
 ``kda_prefill_chunked``,
 ``kda_resume_from_slot``, ``kda_prefill_workspace_bytes``, ``kda_checkpoint_count``,
-``kda_status_string``; the host prefix index ``kda_prefix_*`` through :class:`PrefixIndex`.
+``kda_status_string``; the host prefix index ``kda_prefix_*`` through :class:`PrefixIndex`; latent attention over
+a paged cache (:class:`LatentCache`, :class:`PageTable`): ``kda_latent_append``, ``kda_latent_decode``,
+``kda_latent_prefill`` and the page pool's ``kda_pages_reserve``, ``kda_pages_truncate``, ``kda_pages_fork``,
+``kda_pages_compact``, ``kda_pages_copy``.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -23,6 +27,7 @@ _lib = None
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_WORKSPACE, KDA_ERR_CUDA = 0, 1, 2, 3, 4
 KDA_DEV_BAD_SLOT, KDA_DEV_BAD_SEQLENS, KDA_DEV_BAD_CKPT, KDA_DEV_TIMEOUT = 1, 2, 4, 16
+KDA_DEV_BAD_PAGE, KDA_DEV_NO_PAGES = 8, 32
 
 
 class KdaError(RuntimeError):
@@ -33,6 +38,8 @@ class KdaError(RuntimeError):
 
 
 KDA_STATE_FP32, KDA_STATE_BF16 = 0, 1
+KDA_ELEM_BF16, KDA_ELEM_FP16 = 0, 1
+LATENT_MAX_TOKENS, LATENT_MAX_HEADS = 64, 128  # KDA_LATENT_MAX_* in kda.h
 
 
 class _Pool(ctypes.Structure):
@@ -44,6 +51,19 @@ class _Pool(ctypes.Structure):
 class _Params(ctypes.Structure):
     _fields_ = [("conv_weight", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("l2_eps", ctypes.c_float),
                 ("rms_eps", ctypes.c_float), ("scale", ctypes.c_float), ("conv_silu", ctypes.c_int32)]
+
+
+class _LatentCache(ctypes.Structure):
+    _fields_ = [("rank", ctypes.c_int32), ("rope", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("layers", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("pages", ctypes.c_void_p)]
+
+
+class _PageTable(ctypes.Structure):
+    _fields_ = [("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("refcount", ctypes.c_void_p)]
 
 
 class _PrefixPlan(ctypes.Structure):
@@ -89,6 +109,28 @@ def load_library(path: str | None = None):
     lib.kda_last_error_string.restype = ctypes.c_char_p
     lib.kda_check_slots.argtypes = [i64, i32, vp, vp, i32, vp]
     lib.kda_check_slots.restype = ctypes.c_int
+    pcache, ptable, f32 = ctypes.POINTER(_LatentCache), ctypes.POINTER(_PageTable), ctypes.c_float
+    lib.kda_latent_append.argtypes = [pcache, i32, ptable, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp]
+    lib.kda_latent_append.restype = ctypes.c_int
+    lib.kda_latent_decode_workspace_bytes.argtypes = [pcache, i32, i32, i32]
+    lib.kda_latent_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_latent_decode.argtypes = [pcache, i32, ptable, i32, vp, vp, i64, i32, i32, vp, i64, i64, vp, f32, vp, vp,
+                                      vp, ctypes.c_size_t, vp, vp]
+    lib.kda_latent_decode.restype = ctypes.c_int
+    lib.kda_latent_prefill.argtypes = [i32] * 6 + [vp, vp, i64, i64, i32, i32, vp, i64, i64, vp, i64, i64, vp, i64, vp,
+                                                   i64, i64, f32, vp, vp, vp, vp]
+    lib.kda_latent_prefill.restype = ctypes.c_int
+    lib.kda_pages_workspace_bytes.argtypes = [ptable, i32]
+    lib.kda_pages_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("kda_pages_reserve", "kda_pages_fork"):
+        getattr(lib, name).argtypes = [ptable, pcache, i32, vp, vp, vp, ctypes.c_size_t, vp, vp]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.kda_pages_truncate.argtypes = [ptable, i32, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.kda_pages_truncate.restype = ctypes.c_int
+    lib.kda_pages_compact.argtypes = [ptable, pcache, vp, ctypes.c_size_t, vp, vp]
+    lib.kda_pages_compact.restype = ctypes.c_int
+    lib.kda_pages_copy.argtypes = [pcache, i32, vp, vp, vp, vp]
+    lib.kda_pages_copy.restype = ctypes.c_int
     lib.kda_selftest_wait_timeout.argtypes = [i64, vp, vp]
     lib.kda_selftest_wait_timeout.restype = ctypes.c_int
     lib.kda_prefix_index_create.argtypes = [i32, i32, i32, i64]
@@ -326,6 +368,237 @@ def kda_resume_from_slot(pool: StatePool, src_slot, dst_slot, dev_status, stream
     rc = load_library().kda_resume_from_slot(ctypes.byref(pc), int(src_slot.shape[0]), _ptr(src_slot),
                                              _ptr(dst_slot), _ptr(dev_status), _stream(stream))
     _check(rc, "kda_resume_from_slot")
+
+
+# ------------------------------------------------------------------------------------------ latent attention
+_ELEM = {torch.bfloat16: KDA_ELEM_BF16, torch.float16: KDA_ELEM_FP16}
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(fn):
+    """Runs a latent / page call on the CUDA device of its tensors (current or not), with that device's current
+    stream unless one is given; tensors on different devices, or on the CPU, raise ValueError."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        device = None
+        for x in list(args) + list(kw.values()):
+            for t in ((x.pages,) if isinstance(x, LatentCache) else (x.table, x.lens, x.refcount)
+                      if isinstance(x, PageTable) else (x,)):
+                if isinstance(t, torch.Tensor):
+                    _need(t.is_cuda, f"{fn.__name__}: tensors must be on a CUDA device")
+                    _need(device is None or t.device == device, f"{fn.__name__}: tensors are on different devices")
+                    device = t.device
+        if stream is not None:
+            _need(stream.device == device, f"{fn.__name__}: the stream belongs to another device")
+        with torch.cuda.device(device):
+            return fn(*args, stream=torch.cuda.current_stream() if stream is None else stream, **kw)
+    return call
+
+
+def _int32(t, what: str, n: int | None = None):
+    """A contiguous int32 tensor of n elements (or None), as a pointer."""
+    if t is None:
+        return None
+    _need(t.dtype == torch.int32 and t.dim() == 1 and (n is None or t.shape[0] == n),
+          f"{what} must be an int32 vector" + ("" if n is None else f" of {n} elements"))
+    return _ptr(t)
+
+
+def _rows_of(t, what: str, dtype, shape):
+    """A tensor of that type and shape whose last axis is contiguous: its pointer and its other strides."""
+    _need(isinstance(t, torch.Tensor), f"{what} must be a tensor")
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what} must be {dtype} of shape {tuple(shape)}")
+    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{what}: the last axis must be contiguous")
+    # the stride of an axis of one element is free in torch: give one that holds a row
+    st, least = [], int(t.shape[-1])
+    for k in range(t.dim() - 2, -1, -1):
+        st.append(least if t.shape[k] <= 1 else int(t.stride(k)))
+        least = max(least, st[-1] * int(t.shape[k]))
+    return (ctypes.c_void_p(t.data_ptr()), *reversed(st))
+
+
+def _out(t, what: str, dtype, shape):
+    if t is None:
+        return None
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what} must be {dtype} of shape {tuple(shape)}")
+    return _ptr(t)
+
+
+@dataclass
+class LatentCache:
+    """Paged cache rows c | r of every layer: pages [layers, num_pages, page_size, rank + rope] bf16 or fp16.  The first
+    two axes may be strided (a [num_pages, layers, ...] allocation transposed, for example)."""
+    pages: torch.Tensor
+    rank: int
+
+    @staticmethod
+    def empty(layers: int, num_pages: int, page_size: int, rank: int, rope: int, dtype=torch.bfloat16,
+              device="cuda") -> "LatentCache":
+        return LatentCache(torch.zeros(layers, num_pages, page_size, rank + rope, dtype=dtype, device=device), rank)
+
+    @property
+    def rope(self) -> int:
+        return int(self.pages.shape[3]) - self.rank
+
+    def c(self) -> _LatentCache:
+        p = self.pages
+        if p.dtype not in _ELEM:
+            raise TypeError("latent cache dtype must be bfloat16 or float16")
+        layers, num, size, d = p.shape
+        _need(p.stride(3) == 1 and (size == 1 or p.stride(2) == d), "latent cache: a page must be contiguous")
+        return _LatentCache(self.rank, d - self.rank, size, layers, _ELEM[p.dtype], 0, num, p.stride(0), p.stride(1),
+                            ctypes.c_void_p(p.data_ptr()))
+
+
+@dataclass
+class PageTable:
+    """table [max_seqs, max_pages], lens [max_seqs], refcount [num_pages], all int32, and the page size.  An empty
+    pool has lens and refcount 0."""
+    table: torch.Tensor
+    lens: torch.Tensor
+    refcount: torch.Tensor
+    page_size: int
+
+    @staticmethod
+    def empty(max_seqs: int, max_pages: int, num_pages: int, page_size: int, device="cuda") -> "PageTable":
+        i32 = dict(dtype=torch.int32, device=device)
+        return PageTable(torch.full((max_seqs, max_pages), -1, **i32), torch.zeros(max_seqs, **i32),
+                         torch.zeros(num_pages, **i32), page_size)
+
+    def c(self) -> _PageTable:
+        t = self.table
+        _need(t.dtype == torch.int32 and t.dim() == 2, "page table: table must be int32 [max_seqs, max_pages]")
+        return _PageTable(t.shape[0], t.shape[1], self.page_size, 0, self.refcount.shape[0], _ptr(t),
+                          _int32(self.lens, "page table: lens", int(t.shape[0])),
+                          _int32(self.refcount, "page table: refcount"))
+
+
+@_on_device
+def kda_latent_append(cache: LatentCache, layer: int, pt: PageTable, rows, cu_tokens, latent, rope, dev_status,
+                      stream=None) -> None:
+    """Cache rows of new tokens into one layer; see include/kda.h.  rows int32 [n] or None (row b for sequence b),
+    cu_tokens int32 [n+1], latent [T, rank] and rope [T, rope] of the cache's type (rows may be strided; rope None
+    when the cache has none).  The tokens become the last ones of their rows, which pt.lens already counts."""
+    cc, pc = cache.c(), pt.c()
+    n, T = int(cu_tokens.shape[0]) - 1, int(latent.shape[0])
+    lp, ls = _rows_of(latent, "latent", cache.pages.dtype, (T, cache.rank))
+    rp, rs = (None, 0) if cache.rope == 0 else _rows_of(rope, "rope", cache.pages.dtype, (T, cache.rope))
+    rc = load_library().kda_latent_append(ctypes.byref(cc), int(layer), ctypes.byref(pc), n, _int32(rows, "rows", n),
+                                          _int32(cu_tokens, "cu_tokens"), T, lp, ls, rp, rs,
+                                          _int32(dev_status, "dev_status", 1), _stream(stream))
+    _check(rc, "kda_latent_append")
+
+
+def kda_latent_decode_workspace_bytes(cache: LatentCache, H: int, n: int, max_tokens: int) -> int:
+    with torch.cuda.device(cache.pages.device if cache.pages.is_cuda else -1):
+        cc = cache.c()
+        return int(load_library().kda_latent_decode_workspace_bytes(ctypes.byref(cc), int(H), int(n), int(max_tokens)))
+
+
+@_on_device
+def kda_latent_decode(cache: LatentCache, layer: int, pt: PageTable, rows, cu_tokens, max_tokens: int, q, out, lse,
+                      scale: float, workspace, dev_status, tree_mask=None, stream=None) -> None:
+    """Absorbed latent attention of the newest tokens over the paged cache; see include/kda.h.  q [T, H, rank+rope]
+    (token and head axes may be strided), out [T, H, rank], lse fp32 [T, H] or None; rows int32 [n] or None; cu_tokens int32
+    [n+1], or None for max_tokens queries each of n = len(rows) (or all table rows); tree_mask int64 [T] (bit i: the query
+    sees drafted token i of its sequence) or None; workspace uint8, kda_latent_decode_workspace_bytes() bytes."""
+    cc, pc = cache.c(), pt.c()
+    T, H, d = int(q.shape[0]), int(q.shape[1]), cache.rank + cache.rope
+    n = (int(cu_tokens.shape[0]) - 1 if cu_tokens is not None else
+         int(rows.shape[0]) if rows is not None else int(pt.table.shape[0]))
+    _need(rows is not None or n <= pt.table.shape[0], "kda_latent_decode: more sequences than table rows")
+    qp, qt, qh = _rows_of(q, "q", cache.pages.dtype, (T, H, d))
+    if tree_mask is not None:
+        _need(tree_mask.dtype == torch.int64 and tuple(tree_mask.shape) == (T,), f"tree_mask must be int64 [{T}]")
+    rc = load_library().kda_latent_decode(
+        ctypes.byref(cc), int(layer), ctypes.byref(pc), n, _int32(rows, "rows", n),
+        _int32(cu_tokens, "cu_tokens", n + 1), T, int(max_tokens), H, qp, qt, qh, _ptr(tree_mask), float(scale),
+        _out(out, "out", cache.pages.dtype, (T, H, cache.rank)), _out(lse, "lse", torch.float32, (T, H)),
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _int32(dev_status, "dev_status", 1), _stream(stream))
+    _check(rc, "kda_latent_decode")
+
+
+@_on_device
+def kda_latent_prefill(cu_q, cu_k, max_q: int, q, k_nope, k_rope, v, out, lse, scale: float, dev_status,
+                       causal: bool = True, stream=None) -> None:
+    """Expanded latent attention for prompts; see include/kda.h.  q [Tq, H, nope+rope], k_nope [Tk, H, nope],
+    k_rope [Tk, rope], v [Tk, H, dv], one type, token and head axes may be strided (k_nope and v as halves of one
+    tensor); out [Tq, H, dv], lse fp32 [Tq, H] or None; cu_q, cu_k int32 [nseq+1]."""
+    _need(q.dtype in _ELEM, "q must be bfloat16 or float16")
+    n = int(cu_q.shape[0]) - 1
+    Tq, H, dq = q.shape
+    Tk, _, nope = k_nope.shape
+    rope, dv = int(k_rope.shape[-1]), int(v.shape[-1])
+    _need(dq == nope + rope, "q's last axis must be that of k_nope and k_rope together")
+    qp, qt, qh = _rows_of(q, "q", q.dtype, (Tq, H, dq))
+    kp, kt, kh = _rows_of(k_nope, "k_nope", q.dtype, (Tk, H, nope))
+    rp, rt = _rows_of(k_rope, "k_rope", q.dtype, (Tk, rope))
+    vp, vt, vh = _rows_of(v, "v", q.dtype, (Tk, H, dv))
+    rc = load_library().kda_latent_prefill(
+        _ELEM[q.dtype], H, nope, rope, dv, n, _int32(cu_q, "cu_q"), _int32(cu_k, "cu_k", n + 1), Tq, Tk, int(max_q),
+        int(bool(causal)), qp, qt, qh, kp, kt, kh, rp, rt, vp, vt, vh, float(scale),
+        _out(out, "out", q.dtype, (Tq, H, dv)), _out(lse, "lse", torch.float32, (Tq, H)),
+        _int32(dev_status, "dev_status", 1), _stream(stream))
+    _check(rc, "kda_latent_prefill")
+
+
+def kda_pages_workspace_bytes(pt: PageTable, n: int) -> int:
+    pc = pt.c()
+    return int(load_library().kda_pages_workspace_bytes(ctypes.byref(pc), int(n)))
+
+
+def _pages_call(name: str, pt: PageTable, cache, arrays, workspace, dev_status, stream) -> None:
+    pc = pt.c()
+    head = [ctypes.byref(pc)]
+    if cache is not None:
+        cc = cache.c()
+        head.append(ctypes.byref(cc))
+    if arrays:
+        n = int(arrays[0].shape[0])
+        head += [n] + [_int32(x, f"{name}: items", n) for x in arrays]
+    rc = getattr(load_library(), name)(*head, _ptr(workspace),
+                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                       _int32(dev_status, "dev_status", 1), _stream(stream))
+    _check(rc, name)
+
+
+@_on_device
+def kda_pages_reserve(pt: PageTable, cache: LatentCache, rows, new_lens, workspace, dev_status, stream=None) -> None:
+    """Rows grow to new_lens tokens: pages from the lowest free ones, a shared partly filled last page copied first
+    (rows, new_lens int32 [n]; row -1 = padding).  See include/kda.h."""
+    _pages_call("kda_pages_reserve", pt, cache, (rows, new_lens), workspace, dev_status, stream)
+
+
+@_on_device
+def kda_pages_truncate(pt: PageTable, rows, keep_lens, workspace, dev_status, stream=None) -> None:
+    """Rows keep their first keep_lens tokens (0 ends them); pages behind lose a reference.  See include/kda.h."""
+    _pages_call("kda_pages_truncate", pt, None, (rows, keep_lens), workspace, dev_status, stream)
+
+
+@_on_device
+def kda_pages_fork(pt: PageTable, cache: LatentCache, parents, children, workspace, dev_status, stream=None) -> None:
+    """The empty rows children become copies of rows parents: full pages shared, a partly filled last one copied."""
+    _pages_call("kda_pages_fork", pt, cache, (parents, children), workspace, dev_status, stream)
+
+
+@_on_device
+def kda_pages_compact(pt: PageTable, cache: LatentCache, workspace, dev_status, stream=None) -> None:
+    """Moves the used pages into the lowest places; tables and refcounts follow.  See include/kda.h."""
+    _pages_call("kda_pages_compact", pt, cache, (), workspace, dev_status, stream)
+
+
+@_on_device
+def kda_pages_copy(cache: LatentCache, src, dst, dev_status, stream=None) -> None:
+    """Contents of pages src into pages dst in every layer (int32 [n]; -1 = skip), no bookkeeping."""
+    cc, n = cache.c(), int(src.shape[0])
+    rc = load_library().kda_pages_copy(ctypes.byref(cc), n, _int32(src, "src"), _int32(dst, "dst", n),
+                                       _int32(dev_status, "dev_status", 1), _stream(stream))
+    _check(rc, "kda_pages_copy")
 
 
 @dataclass

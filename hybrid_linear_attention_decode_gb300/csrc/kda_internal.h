@@ -77,6 +77,74 @@ struct ProjectArgs {
 };
 int launch_project(const ProjectArgs &a, cudaStream_t st);
 
+// Latent attention and its paged cache (kda_latent_api.cu validates, the kernel files launch).
+struct LatentCacheArgs {
+    int32_t rank, rope, page_size, layers, fp16;
+    int64_t num_pages, layer_stride, page_stride;  // elements
+    uint16_t *pages;
+};
+struct PageTableArgs {
+    int32_t max_seqs, max_pages, page_size;
+    int64_t num_pages;
+    int32_t *table, *lens, *refcount;
+};
+struct AppendArgs {
+    LatentCacheArgs c;  // pages already at the layer
+    PageTableArgs t;
+    int32_t n;
+    const int32_t *rows, *cu;
+    int64_t num_tokens;
+    const uint16_t *latent, *rope;
+    int64_t latent_stride, rope_stride;
+    int32_t *status;
+};
+int launch_latent_append(const AppendArgs &a, cudaStream_t st);
+
+struct LatentDecodeArgs {
+    LatentCacheArgs c;  // pages already at the layer
+    PageTableArgs t;
+    int32_t n, max_tokens, H;
+    const int32_t *rows, *cu;
+    int64_t num_tokens;
+    const uint16_t *q;
+    int64_t q_ts, q_hs;
+    const uint64_t *tree;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    void *ws;
+    int32_t *status;
+};
+size_t latent_decode_workspace_bytes(int rank, int H, int n, int max_tokens);
+int launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st);
+
+struct LatentPrefillArgs {
+    int32_t fp16, H, nope, rope, dv, nseq, max_q, causal;
+    const int32_t *cu_q, *cu_k;
+    int64_t num_q, num_k;
+    const uint16_t *q, *k, *r, *v;
+    int64_t q_ts, q_hs, k_ts, k_hs, r_ts, v_ts, v_hs;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    int32_t *status;
+};
+int launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st);
+
+enum PageOp { PAGES_RESERVE, PAGES_TRUNCATE, PAGES_FORK, PAGES_COMPACT };
+struct PagesArgs {
+    PageTableArgs t;
+    LatentCacheArgs c;
+    int32_t n;
+    const int32_t *x, *y;  // rows and lengths, or parents and children
+    int32_t *ws;
+    int32_t *status;
+};
+size_t pages_workspace_bytes(int32_t max_seqs, int64_t num_pages, int32_t n);
+int launch_pages(PageOp op, const PagesArgs &a, cudaStream_t st);
+int launch_pages_copy(const LatentCacheArgs &c, int32_t n, const int32_t *src, const int32_t *dst, int32_t *status,
+                      cudaStream_t st);
+
 bool prefill_supported(int dk, int dv, int W, int chunk);
 // The host-side argument checks of kda_prefill_chunked (everything but the workspace); KDA_OK or the failure
 // code with the reason recorded.  Makes no CUDA call.

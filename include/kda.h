@@ -57,7 +57,9 @@ enum kda_status {
 #define KDA_DEV_BAD_SLOT 0x1      /* a slot index outside [0, num_slots) (src may also be -1) */
 #define KDA_DEV_BAD_SEQLENS 0x2   /* cu_seqlens not non-decreasing from 0 to total_tokens, or start_pos < 0 */
 #define KDA_DEV_BAD_CKPT 0x4      /* ckpt_offsets does not give sequence n exactly its boundary count */
+#define KDA_DEV_BAD_PAGE 0x8      /* a page table entry in use outside [0, num_pages) */
 #define KDA_DEV_TIMEOUT 0x10      /* a bounded wait on an asynchronous copy gave up */
+#define KDA_DEV_NO_PAGES 0x20     /* a page pool operation found too few free pages for an item */
 
 /*
  * The state-slot pool ("The Hardest Part: Prefix Caching for KDA": the physical state block is
@@ -241,6 +243,163 @@ KDA_API int kda_prefill_chunked_noalloc(const kda_pool *pool, const kda_params *
  */
 KDA_API int kda_resume_from_slot(const kda_pool *pool, int32_t n, const int32_t *src_slot, const int32_t *dst_slot,
                          int32_t *dev_status, kda_stream_t stream);
+
+/*
+ * Latent attention, the other attention layer of a hybrid model ("A Preview of Production-Scale Kimi K3
+ * Support on vLLM", section on the MLA module: a full-attention layer beside the KDA layers).  Per token it
+ * keeps one row x_j = [c_j | r_j] for all heads: a latent vector of `rank` values and a rotary key of `rope`
+ * values (already rotated).  Keys and values of head h are linear in it, k = [W_K^h c | r] and v = W_V^h c, so
+ * attention has two forms:
+ *   absorbed  q~ = [W_K^h^T q_nope | q_rope]:  s_j = scale q~.x_j,  o~ = sum_j softmax(s)_j c_j  (then W_V^h o~):
+ *             every head reads the same rows, which suits few queries over a long cache (kda_latent_decode);
+ *   expanded  keys and values per head, fewer operations per pair: suits prompts (kda_latent_prefill).
+ * The projections W are plain matrix products and the caller's.
+ *
+ * The rows live in pages of page_size tokens: pages [layers][num_pages][page_size][rank + rope], where layers
+ * and pages may have any (16-byte aligned, not overlapping) stride.  One page index holds the same tokens in
+ * every layer.  Supported: rank in {128, 256, 384, 512}; rope a multiple of 16, 0 to 64; page_size 16, 32 or a
+ * multiple of 64 up to 1024.
+ */
+enum kda_elem_type { KDA_ELEM_BF16 = 0, KDA_ELEM_FP16 = 1 };
+
+typedef struct kda_latent_cache {
+    int32_t rank, rope, page_size, layers;
+    int32_t dtype;             /* enum kda_elem_type */
+    int32_t reserved;          /* 0 */
+    int64_t num_pages;
+    int64_t layer_stride;      /* elements from a page's copy in one layer to that in the next */
+    int64_t page_stride;       /* elements from one page to the next */
+    void *pages;               /* device, 16-byte aligned */
+} kda_latent_cache;
+
+/*
+ * Which pages hold which sequence: token j of table row s is row j % page_size of page
+ * table[s][j / page_size], for j < lens[s].  refcount[p] counts the table rows that page p serves (0 = free);
+ * only the kda_pages_* calls use it (it may be NULL for the others).  Entries behind a row's last page are not read.
+ */
+typedef struct kda_page_table {
+    int32_t max_seqs, max_pages;  /* rows, and entries of a row */
+    int32_t page_size;
+    int32_t reserved;             /* 0 */
+    int64_t num_pages;
+    int32_t *table;               /* device [max_seqs][max_pages] */
+    int32_t *lens;                /* device [max_seqs] */
+    int32_t *refcount;            /* device [num_pages] */
+} kda_page_table;
+
+/*
+ * Writes the cache rows of new tokens of n sequences into one layer.  Sequence b's tokens are rows
+ * cu_tokens[b] .. cu_tokens[b+1]-1 of latent and rope and become the LAST tokens of table row rows[b]
+ * (rows NULL: row b): lens already counts them, and their pages are in the table (kda_pages_reserve).
+ *   rows       device [n] int32 or NULL; -1 = a padding entry, whose tokens are not stored
+ *   cu_tokens  device [n+1] int32, non-decreasing, cu_tokens[n] <= num_tokens; tokens behind it are ignored
+ *   latent     device [num_tokens][rank], rope device [num_tokens][rope] (NULL when the cache has rope 0), the
+ *              cache's type, rows at the given strides (elements, multiples of 8), 16-byte aligned
+ * A sequence whose row, lengths or page is bad (KDA_DEV_BAD_SLOT, _SEQLENS, _PAGE) is not stored, as far as it is bad.
+ * No two tokens of a call may go to the same place.
+ */
+KDA_API int kda_latent_append(const kda_latent_cache *cache, int32_t layer, const kda_page_table *pt, int32_t n,
+                              const int32_t *rows, const int32_t *cu_tokens, int64_t num_tokens, const void *latent,
+                              int64_t latent_stride, const void *rope, int64_t rope_stride, int32_t *dev_status,
+                              kda_stream_t stream);
+
+/* Most query tokens per sequence of one kda_latent_decode call, and most heads. */
+#define KDA_LATENT_MAX_TOKENS 64
+#define KDA_LATENT_MAX_HEADS 128
+
+/* Bytes of device workspace kda_latent_decode needs on the current device for these sizes (0 for unsupported ones). */
+KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, int32_t H, int32_t n,
+                                                 int32_t max_tokens);
+
+/*
+ * Absorbed latent attention of n sequences' newest tokens over one layer of the paged cache: a decode step
+ * (one token a sequence) or the verification of drafted tokens (kda_decode_multi's counterpart), whose rows
+ * are in the cache already.  Sequence b has nq = cu_tokens[b+1] - cu_tokens[b] query tokens (at most
+ * max_tokens), the last nq of the len = lens[rows[b]] tokens of its table row.  Every query sees all tokens
+ * before those nq.  Among the nq, query t sees token i when
+ *   tree_mask NULL:  i <= t (a chain);
+ *   else             bit i of tree_mask[cu_tokens[b] + t] is set (a tree: its ancestors and itself).
+ *   rows       device [n] int32 table rows (repeats allowed), or NULL for row b; -1 = a padding entry
+ *   cu_tokens  device [n+1] int32, or NULL: max_tokens queries for every sequence (num_tokens = n*max_tokens)
+ *   q          device [num_tokens][H][rank+rope], the cache's type, at the given token and head strides
+ *              (elements, multiples of 8), 16-byte aligned
+ *   tree_mask  device [num_tokens] uint64, or NULL
+ *   scale      finite and > 0
+ *   out        device [num_tokens][H][rank] contiguous, the cache's type, 16-byte aligned
+ *   lse        device [num_tokens][H] fp32: the natural logarithm of the sum of exp(s); or NULL
+ * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so
+ * do the queries of a sequence with a bad row or length (flagged; a bad page's tokens read as zero rows).  Sequences with
+ * bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  What a cache row that no query of
+ * its sequence sees holds (even NaN) does not matter; a query that sees a non-finite row gets NaN.
+ * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product, outputs at
+ * the end.  Results do not depend on the other sequences' contents, but a sequence's split over CTAs (and so
+ * its last bits) depends on all lengths of the call.  The workspace keeps nothing between calls; calls that overlap on the GPU
+ * need one each.  1 <= H <= KDA_LATENT_MAX_HEADS, max_tokens <= KDA_LATENT_MAX_TOKENS, n <= 65535.
+ */
+KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, const kda_page_table *pt, int32_t n,
+                              const int32_t *rows, const int32_t *cu_tokens, int64_t num_tokens, int32_t max_tokens,
+                              int32_t H, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                              const uint64_t *tree_mask, float scale, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, kda_stream_t stream);
+
+/*
+ * Expanded latent attention of nseq sequences' queries over their own keys: s = scale (q_nope . k_nope +
+ * q_rope . r), o = softmax(s) v, per head, with one rotary key r for all heads.
+ *   cu_q, cu_k  device [nseq+1] int32, non-decreasing from 0 to at most num_q / num_k; max_q bounds the queries of one sequence
+ *   causal      1: query i of nq sees keys j <= i + nk - nq (the queries are the last nq tokens of nk, as when
+ *               the beginning of the prompt is in the cache already); 0: all nk
+ *   q           device [num_q][H][nope+rope]     k_nope  device [num_k][H][nope]
+ *   k_rope      device [num_k][rope]             v       device [num_k][H][dv]
+ *               all of one type (dtype, enum kda_elem_type), 16-byte aligned, with token and head strides in
+ *               elements (multiples of 8), so k_nope and v may be the halves of one [num_k][H][nope+dv] tensor
+ *   out         device [num_q][H][dv] contiguous, same type        lse  device [num_q][H] fp32, or NULL
+ * A query that sees no key gets out 0 and lse -inf; sequences with bad tables (KDA_DEV_BAD_SEQLENS) and rows
+ * behind cu_q[nseq] are left as they were.  Keys and values that a query does not see do not matter to it, even
+ * NaN.  Supported: nope and dv in {64, 128}; rope a multiple of 16, 16 to 64.
+ */
+KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int32_t dv, int32_t nseq,
+                               const int32_t *cu_q, const int32_t *cu_k, int64_t num_q, int64_t num_k, int32_t max_q,
+                               int32_t causal, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                               const void *k_nope, int64_t k_token_stride, int64_t k_head_stride, const void *k_rope,
+                               int64_t rope_token_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                               float scale, void *out, float *lse, int32_t *dev_status, kda_stream_t stream);
+
+/*
+ * The page pool's bookkeeping on the device, so that it can run inside a captured step.  Items are taken in
+ * order, and new pages are always the lowest free ones of the pool as it was before the call, so that results
+ * do not depend on timing.  An item with a bad row index or length, or whose row appears in an earlier item of
+ * the call as well, is flagged (KDA_DEV_BAD_SLOT, _SEQLENS) and left out; so is one for which free pages do
+ * not suffice (KDA_DEV_NO_PAGES; the demand of items before it counts whether they were served or not).  Row -1 = a padding item.
+ * Shared pages (refcount > 1) are never written.  cache (all layers) is what page copies apply to; its
+ * page_size and num_pages have to be the table's.
+ *
+ * kda_pages_reserve   row rows[i] grows to new_lens[i] tokens: pages are added behind its last one.  A partly
+ *                     filled last page that is shared is replaced by a private copy (copy on write).
+ * kda_pages_truncate  row rows[i] keeps its first keep_lens[i] tokens (0: the sequence ends; rejected drafts);
+ *                     pages behind them lose a reference, their entries become -1.
+ * kda_pages_fork      the empty row children[i] becomes a copy of row parents[i] (a parent may have many
+ *                     children): full pages are shared, a partly filled last page is copied into a new one.
+ * kda_pages_compact   pages in use move into the lowest places, [0, pages in use): the i-th used page behind them (ascending)
+ *                     moves into the i-th free one among them; tables and refcounts follow.
+ * kda_pages_copy      contents only, no bookkeeping: page dst[i] of every layer becomes page src[i] (-1 in
+ *                     either: skipped; bad indices flagged).  No dst may repeat or be a src.
+ *
+ * workspace: device, 16-byte aligned, kda_pages_workspace_bytes(pt, n) bytes (n = 0 for compact), not kept
+ * between calls.
+ */
+KDA_API size_t kda_pages_workspace_bytes(const kda_page_table *pt, int32_t n);
+KDA_API int kda_pages_reserve(const kda_page_table *pt, const kda_latent_cache *cache, int32_t n, const int32_t *rows,
+                              const int32_t *new_lens, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              kda_stream_t stream);
+KDA_API int kda_pages_truncate(const kda_page_table *pt, int32_t n, const int32_t *rows, const int32_t *keep_lens,
+                               void *workspace, size_t workspace_bytes, int32_t *dev_status, kda_stream_t stream);
+KDA_API int kda_pages_fork(const kda_page_table *pt, const kda_latent_cache *cache, int32_t n, const int32_t *parents,
+                           const int32_t *children, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                           kda_stream_t stream);
+KDA_API int kda_pages_compact(const kda_page_table *pt, const kda_latent_cache *cache, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, kda_stream_t stream);
+KDA_API int kda_pages_copy(const kda_latent_cache *cache, int32_t n, const int32_t *src, const int32_t *dst,
+                           int32_t *dev_status, kda_stream_t stream);
 
 /*
  * Host-side prefix index and retention policies ("A Preview of Production-Scale Kimi K3 Support on vLLM",
