@@ -1,0 +1,152 @@
+// kda_latent.cuh -- what the two latent attention kernels share: element types, MN-major operand tiles and
+// operands in tensor memory, 3-D tensor-map loads and the encoder of those maps.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "kda_device.cuh"
+#include "kda_internal.h"
+#include "kda_umma.cuh"
+
+namespace kda {
+namespace latent {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A running maximum is raised (and what was summed so far rescaled) only when a score exceeds it by more than
+// this, in units of log2: the weights stay below 2^8, where 16-bit types round them as finely as below 1, and
+// after the first tiles almost no rescaling is left.
+constexpr float kRaise = 8.f;
+
+__device__ __forceinline__ float exp2_(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// two floats rounded to the element type (nearest even), lo in the low half
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (FP16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool FP16>
+__device__ __forceinline__ uint16_t to_elem(float x) {
+    return FP16 ? __half_as_ushort(__float2half_rn(x)) : f2bf(x);
+}
+
+// Whether one of the two elements in a word is infinite or NaN (all exponent bits set).
+template <bool FP16>
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+    constexpr uint32_t e = FP16 ? 0x7c00u : 0x7f80u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+template <bool FP16>
+__device__ __forceinline__ bool nonfinite8(uint4 w) {
+    return nonfinite2<FP16>(w.x) || nonfinite2<FP16>(w.y) || nonfinite2<FP16>(w.z) || nonfinite2<FP16>(w.w);
+}
+
+// Instruction descriptor fields on top of umma::idesc(): 16-bit operand format, MN-major ("transposed") A or B.
+template <bool FP16>
+constexpr int kFmt = FP16 ? 0 : umma::kBF16;
+constexpr uint32_t kAMajorMN = 1u << 15;
+constexpr uint32_t kBMajorMN = 1u << 16;
+
+// Descriptor of an MN-major 16-bit tile in the 128-byte swizzle: atoms of 64 elements (128 bytes) along M or N
+// by 8 k, `mn_stride` bytes from one atom to the next along M or N, 1024 bytes from one group of 8 k to the next.
+// Rows of tokens that are a K-major operand of one product (k = channel) are an MN-major operand of
+// another (k = token) as they lie.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t mn_stride) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    d |= (uint64_t)((mn_stride >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// D += A B with A in tensor memory: lane = row, two consecutive 16-bit k in each column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
+            d_tmem),
+        "r"(a_tmem), "l"(b), "r"(id), "r"((uint32_t)acc));
+}
+
+// Warp-wide, asynchronous: lanes 0..15 of this warp's quarter x 64 consecutive columns.  Register 4n + i of
+// thread t holds lane t/4 + 8*(i/2), column 8n + 2*(t%4) + i%2.  Valid after umma::wait_ld(r).
+__device__ __forceinline__ void ld16x64_issue(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%"
+        "19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Warp-wide, asynchronous: store r[16] into 32 lanes x 16 consecutive columns.
+__device__ __forceinline__ void st16_issue(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encoder() {
+    static std::atomic<EncodeTiledFn> cached{nullptr};
+    EncodeTiledFn f = cached.load(std::memory_order_acquire);
+    if (f) return f;
+    void *fp = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fp, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fp)
+        return nullptr;
+    f = reinterpret_cast<EncodeTiledFn>(fp);
+    cached.store(f, std::memory_order_release);
+    return f;
+}
+
+// A 16-bit tensor [d2][d1][d0] with strides (elements) s2, s1 and contiguous d0, boxes of 64 x b1 x b2 in the
+// 128-byte swizzle; what lies outside reads as zero.
+inline bool map_3d(EncodeTiledFn enc, CUtensorMap *m, bool fp16, const void *base, int64_t d0, int64_t d1, int64_t d2,
+                   int64_t s1, int64_t s2, int b1, int b2) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)b1, (cuuint32_t)b2};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace latent
+}  // namespace kda

@@ -1,92 +1,682 @@
 // kda_latent_decode.cu -- absorbed latent attention over the paged cache (include/kda.h: kda_latent_decode).
 //
-// One warp per (query token, head): the query stays in registers, the keys stream past it, and the softmax runs
-// online (maximum m, sum l of exp(s - m), weighted sum o; all fp32).
-#include <cuda_fp16.h>
+//   s_rj = scale q_r . x_j,   o_r = sum_j softmax(s_r)_j c_j,   x_j = [c_j | r_j]
+//
+// for the R = queries x heads rows of a sequence, all over the same cache rows x_j.  The cache is read once, so
+// with few rows the bytes bound the call: 2 (rank + rope) a token, against 2 R (2 rank + rope) operations.
+//
+// Split: the 64-token tiles of all sequences form one list, and each group of CTAs takes an equal, contiguous
+// part of it (found on the device from lens, so a captured launch follows its lengths).  A group has one CTA for
+// each NR rows (NR = 16, 32 or 64), side by side in the grid, so that they read the same tiles at the
+// same time and all but one of them from L2.  A sequence that a group holds whole is written at once; one that is cut
+// leaves normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
+//
+// A tile, by one CTA of 6 warps (one CTA per SM, ring of tiles in shared memory):
+//   warp 4   TMA: one box per page (or 64 rows) and 64 channels, into K-major 128-byte-swizzled rows
+//   warp 5   S = Q X^T  (M 64 rows, N 64 tokens, k = channel) and O^T += C^T P^T  (M 128 channels, N = NR rows,
+//            k = token; C^T is the same shared memory read MN-major).  O^T is transposed because M must
+//            be 64 or 128 where the rows are few, and the channels are always a multiple of 128: no lane of the
+//            accumulator is idle, and rank 512 x 64 rows takes 256 of the 512 tensor-memory columns.
+//   warps 0-3  softmax of S (a quad of threads per row), P to shared memory, and at the end O^T out.
+// S of a tile is issued before P V of the one before, so the softmax overlaps the products.
+// The running maximum is raised only by more than 2^8 (kRaise); then O^T, one column a row, is rescaled in place.
+// Weights P are rounded to the element type for the second product (its operands are 16-bit); their sum is
+// kept in fp32 from the unrounded weights.
+#include <algorithm>
 
-#include "kda_device.cuh"
-#include "kda_internal.h"
+#include "kda_latent.cuh"
 
 namespace kda {
 namespace latent {
 
-__device__ __forceinline__ float elem(uint16_t x, bool fp16) {
-    return fp16 ? __half2float(__ushort_as_half(x)) : bf2f(x);
-}
-__device__ __forceinline__ uint16_t to_elem(float x, bool fp16) {
-    return fp16 ? __half_as_ushort(__float2half_rn(x)) : f2bf(x);
+constexpr int TILE = 64;             // tokens per tile
+constexpr int NT = 192;              // threads of the main kernel
+constexpr int SW = 4;                // softmax warps
+constexpr uint32_t CHUNK = TILE * 128;  // bytes of a tile's 64 channels
+constexpr int MAX_STAGES = 8;
+constexpr uint32_t SMEM_MAX = 227 * 1024;
+constexpr uint32_t MISC = 1536;      // barriers and small arrays
+constexpr int CW = 8;                // warps of a combine CTA
+
+struct Meta {
+    int32_t pieces, group, second, seq;  // parts of a cut sequence: first group, whether its part there is the second
+};
+
+struct DecodeP {
+    LatentDecodeArgs a;
+    int32_t groups, nrt, nst, nch, by_seq;
+    Meta *meta;    // [n] when by_seq, else [groups]
+    float *part;   // [groups * 2][nrt][NR][rank] normalised parts
+    float *part_l; // [groups * 2][nrt][NR] log2 of their sums
+};
+
+struct Seq {
+    int64_t c0;
+    int32_t nq, len, row, tiles, bits;
+};
+
+__device__ __forceinline__ Seq seq_of(const LatentDecodeArgs &a, int b) {
+    Seq s;
+    const int64_t c0 = a.cu ? (int64_t)a.cu[b] : (int64_t)b * a.max_tokens;
+    const int64_t c1 = a.cu ? (int64_t)a.cu[b + 1] : c0 + a.max_tokens;
+    s.row = a.rows ? a.rows[b] : b;
+    s.c0 = c0;
+    s.nq = (int32_t)(c1 - c0);
+    s.bits = 0;
+    s.len = 0;
+    if (c0 < 0 || c1 < c0 || c1 - c0 > a.max_tokens || c1 > a.num_tokens) {
+        s.bits = KDA_DEV_BAD_SEQLENS;
+        s.nq = 0;
+    } else if (s.row < -1 || s.row >= a.t.max_seqs) {
+        s.bits = KDA_DEV_BAD_SLOT;
+    } else if (s.row >= 0) {
+        s.len = a.t.lens[s.row];
+        if (s.len < 0 || s.len > (int64_t)a.t.max_pages * a.t.page_size) {
+            s.bits = KDA_DEV_BAD_SEQLENS;
+            s.len = 0;
+        }
+    }
+    s.tiles = s.nq > 0 ? (s.len + TILE - 1) / TILE : 0;
+    return s;
 }
 
-__global__ void __launch_bounds__(32) kda_latent_decode_kernel(const LatentDecodeArgs a) {
-    const int lane = threadIdx.x;
-    const int b = blockIdx.y, t = blockIdx.x / a.H, h = blockIdx.x - t * a.H;
-    const int64_t c0 = a.cu ? a.cu[b] : (int64_t)b * a.max_tokens;
-    const int64_t c1 = a.cu ? a.cu[b + 1] : c0 + a.max_tokens;
-    const int64_t nq = c1 - c0;
-    if (c0 < 0 || nq < 0 || nq > a.max_tokens || c1 > a.num_tokens) {
-        if (blockIdx.x == 0 && lane == 0) set_status(a.status, KDA_DEV_BAD_SEQLENS);
-        return;
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SW * 32) : "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "n"(SW * 32)
+                 : "memory");
+    return r != 0;
+}
+
+// The group's part of the list of tiles: `f(b, s, first tile, tiles, place in the list)` for each sequence in it;
+// `get(b)` reads the sequence.
+template <class G, class F>
+__device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64_t at, int64_t end, int rt, int NR, G get,
+                                     F f) {
+    for (; at < end && b < p.a.n; ++b, off = 0) {
+        const Seq s = get(b);
+        const int32_t nt = (int32_t)min((int64_t)(s.tiles - off), end - at);
+        if (nt <= 0) continue;
+        if (rt * NR < s.nq * p.a.H && !f(b, s, off, nt, at)) return;
+        at += nt;
     }
-    if (t >= nq) return;
-    const int32_t row = a.rows ? a.rows[b] : b;
-    int64_t len = 0;
-    if (row < -1 || row >= a.t.max_seqs) {
-        if (lane == 0) set_status(a.status, KDA_DEV_BAD_SLOT);
-    } else if (row >= 0) {
-        len = a.t.lens[row];
-        if (len < 0 || len > (int64_t)a.t.max_pages * a.t.page_size) {
-            len = 0;
-            if (lane == 0) set_status(a.status, KDA_DEV_BAD_SEQLENS);
+}
+
+template <int NR, bool FP16>
+__global__ void __launch_bounds__(NT, 1)
+    kda_latent_decode_kernel(const DecodeP p, const __grid_constant__ CUtensorMap map) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const LatentDecodeArgs &a = p.a;
+    const int nch = p.nch, nst = p.nst, rank = a.c.rank, d = rank + a.c.rope, H = a.H;
+    uint8_t *Q = sm;  // [nch][NR][128 bytes]; reads of rows NR..63 run on into KV and feed rows that nobody reads
+    uint8_t *KV = Q + (uint32_t)nch * NR * 128;  // [nst][nch][TILE][128 bytes]
+    uint8_t *P = KV + (uint32_t)nst * nch * CHUNK;  // [NR][128 bytes]
+    uint64_t *full = reinterpret_cast<uint64_t *>(P + NR * 128);
+    uint64_t *empty = full + MAX_STAGES;
+    uint64_t *s_full = empty + MAX_STAGES;  // [2]
+    uint64_t *p_ready = s_full + 2;
+    uint64_t *q_ready = p_ready + 1;
+    uint64_t *drain = q_ready + 1;
+    int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [8]
+    int64_t *start = scan + 8;                                   // total, first sequence, first tile in it
+    float *fs = reinterpret_cast<float *>(start + 4);            // [2][64] factors of the rows
+    float *inv = fs + 128;                                       // [64]
+    uint32_t *poison = reinterpret_cast<uint32_t *>(inv + 64);   // [64] tile rows that are not finite
+    Seq *seq_s = reinterpret_cast<Seq *>(poison + 64);
+    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(seq_s + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rt = blockIdx.x % p.nrt, g = blockIdx.x / p.nrt;
+    constexpr uint32_t TCOLS = NR == 64 ? 512 : 256;
+    constexpr uint32_t T_S = NR * 4;  // O^T: rank/128 blocks of NR columns; then two S buffers of 64
+
+    if (warp == 5) umma::alloc(tmem_s, TCOLS);
+    if (tid == 0) {
+        start[1] = a.n;
+        start[2] = 0;
+        for (int s = 0; s < MAX_STAGES; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(s_full + 1, 1);
+        mbar_init(p_ready, SW);
+        mbar_init(q_ready, SW);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+
+    // ---- this group's part of the list: prefix sums of the sequences' tiles, each thread a run of sequences ----
+    const int run = (a.n + NT - 1) / NT;
+    const int r0 = min(a.n, tid * run), r1 = min(a.n, r0 + run);
+    int64_t mine = 0;
+    for (int b = r0; b < r1; ++b) mine += seq_of(a, b).tiles;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int64_t per = (total + p.groups - 1) / p.groups;
+    const int64_t g0 = min(total, g * per), g1 = min(total, g0 + per);
+    if (mine > 0 && g0 >= before && g0 < before + mine) {
+        int64_t at = before;
+        for (int b = r0; b < r1; ++b) {
+            const int32_t t = seq_of(a, b).tiles;
+            if (g0 < at + t) {
+                start[1] = b;
+                start[2] = g0 - at;
+                break;
+            }
+            at += t;
         }
     }
-    const int d = a.c.rank + a.c.rope;
-    const uint64_t seen = a.tree ? a.tree[c0 + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
-    const uint16_t *qp = a.q + (c0 + t) * a.q_ts + h * a.q_hs;
-    float q[18], o[16];
+    if (!p.by_seq && rt == 0 && tid == 0) p.meta[g].pieces = 0;
+    // queries of empty (or bad) sequences: zeros
+    for (int b = blockIdx.x; b < a.n; b += gridDim.x) {
+        const Seq s = seq_of(a, b);
+        if (s.bits && tid == 0) set_status(a.status, s.bits);
+        if (s.tiles > 0) continue;
+        if (p.by_seq && tid == 0) p.meta[b].pieces = 0;
+        uint4 *o = reinterpret_cast<uint4 *>(a.out + s.c0 * H * rank);
+        for (int64_t i = tid; i < (int64_t)s.nq * H * rank / 8; i += NT) o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int i = tid; i < s.nq * H; i += NT) a.lse[s.c0 * H + i] = -INFINITY;
+    }
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = *tmem_s;
+    const int b_start = g0 < g1 ? (int)start[1] : 0;
+    const int32_t off_start = g0 < g1 ? (int32_t)start[2] : 0;
+    bool ok = true;
+    auto read = [&](int b) { return seq_of(a, b); };
+
+    if (warp == 4) {
+        // ================================ producer ================================
+        const int ps = a.c.page_size, bps = min(ps, TILE), nb = TILE / bps;
+        int it = 0, st = 0;
+        uint32_t ph = 1;  // a fresh ring is empty
+        walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int64_t) {
+            const int32_t *trow = a.t.table + (int64_t)s.row * a.t.max_pages;
+            for (int j = 0; j < nt; ++j, ++it) {
+                const int key = (off + j) * TILE + lane * bps;  // below 2^31: len is
+                int page = (int)a.c.num_pages;  // a box outside the tensor reads as zeros
+                if (lane < nb && key < s.len) {
+                    const int e = __ldg(trow + key / ps);
+                    if (e >= 0 && e < a.c.num_pages)
+                        page = e;
+                    else
+                        set_status(a.status, KDA_DEV_BAD_PAGE);
+                }
+                ok = __all_sync(0xffffffffu, it < nst || mbar_wait(empty + st, ph));
+                if (!ok) return false;
+                if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)nch * CHUNK);
+                __syncwarp();
+                uint8_t *dst = KV + (uint32_t)(st * nch) * CHUNK;
+                for (int u0 = 0; u0 < nb * nch; u0 += 32) {
+                    const int u = u0 + lane, box = u % nb, c = u / nb;
+                    const int pg = __shfl_sync(0xffffffffu, page, box);
+                    if (u < nb * nch)
+                        tma_load_3d(dst + c * CHUNK + box * bps * 128, &map, c * 64,
+                                    ((off + j) * TILE + box * bps) % ps, pg, full + st);
+                }
+                if (++st == nst) st = 0, ph ^= 1;
+            }
+            return true;
+        });
+        if (__syncthreads_or(!ok)) {  // copies still in flight land before the CTA ends (short bounded waits)
+            for (int k = 0; k < min(it, nst); ++k) {
+                st = st ? st - 1 : nst - 1;
+                mbar_wait(full + st, (uint32_t)((it - 1 - k) / nst) & 1u, 10000000ull);
+            }
+        }
+    } else if (warp == 5) {
+        // ================================ MMA issuer ================================
+        if (lane == 0) {
+            const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
+            const uint32_t id_o = umma::idesc(kFmt<FP16>, 128, NR) | kAMajorMN;
+            const uint64_t dq = umma::sdesc(smem_addr(Q)), dp = umma::sdesc(smem_addr(P));
+            const int nk = d / 16;
+            uint32_t pieces = 0;
+            int it = 0, st = 0;          // tile whose P V comes next, and its stage
+            uint32_t ph = 0;             // parity of the stage's full barrier
+            walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &, int32_t, int32_t nt, int64_t) {
+                ok = mbar_wait(q_ready, pieces++ & 1u);
+                if (!ok) return false;
+                umma::fence_after();
+                auto issue_s = [&](int buf, int stage) {
+                    const uint64_t dx = umma::sdesc(smem_addr(KV + (uint32_t)(stage * nch) * CHUNK));
+                    for (int k = 0; k < nk; ++k)
+                        umma::mma_bf16(tmem + T_S + buf * TILE, umma::sdesc_at(dq, NR, k), umma::sdesc_at(dx, TILE, k),
+                                       id_s, k > 0);
+                    umma::commit(s_full + buf);
+                };
+                bool issued = false;  // S of tile `it`
+                for (int j = 0; j < nt; ++j, ++it) {
+                    if (!issued) {
+                        ok = mbar_wait(full + st, ph);
+                        if (!ok) return false;
+                        umma::fence_after();
+                        issue_s(it & 1, st);
+                    }
+                    const int st1 = st + 1 == nst ? 0 : st + 1;
+                    const uint32_t ph1 = st1 ? ph : ph ^ 1u;
+                    // whichever comes first: the weights of this tile, or the rows of the next
+                    issued = false;
+                    uint64_t t0 = 0;
+                    for (uint32_t spin = 1; !mbar_try_wait(p_ready, it & 1u); ++spin) {
+                        if (!issued && j + 1 < nt && mbar_try_wait(full + st1, ph1)) {
+                            umma::fence_after();
+                            issue_s((it + 1) & 1, st1);
+                            issued = true;
+                        }
+                        if ((spin & 255u) == 0) {
+                            const uint64_t t = global_timer_ns();
+                            if (!t0) t0 = t;
+                            if (t - t0 > kWaitLimitNs) {
+                                ok = false;
+                                return false;
+                            }
+                        }
+                    }
+                    umma::fence_after();
+                    const uint32_t x = smem_addr(KV + (uint32_t)(st * nch) * CHUNK);
+                    for (int m = 0; m < rank / 128; ++m) {
+                        const uint64_t dc = sdesc_mn(x + 2 * m * CHUNK, CHUNK);
 #pragma unroll
-    for (int k = 0; k < 18; ++k) q[k] = lane + 32 * k < d ? elem(qp[lane + 32 * k], a.c.fp16) * a.scale : 0.f;
+                        for (int k = 0; k < TILE / 16; ++k)
+                            umma::mma_bf16(tmem + m * NR, dc + (uint64_t)(k * 2048 >> 4), umma::sdesc_at(dp, NR, k), id_o,
+                                           j > 0 || k > 0);
+                    }
+                    umma::commit(empty + st);  // O^T holds this tile, and its stage is free
+                    st = st1;
+                    ph = ph1;
+                }
+                return true;
+            });
+        }
+        if (__syncthreads_or(!ok) && lane == 0) {
+            umma::commit(drain);
+            mbar_wait(drain, 0, 10000000ull);
+        }
+    } else {
+        // ================================ softmax ================================
+        // These warps meet at named barriers, so they take every decision alike: one thread reads each sequence
+        // for all, and a wait that gives up leads on through the same barriers (without further waits) to the end.
+        auto read_once = [&](int b) {
+            softmax_sync();
+            if (tid == 0) *seq_s = seq_of(a, b);
+            softmax_sync();
+            return *seq_s;
+        };
+        auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity)); };
+        const uint32_t quad = tmem + ((uint32_t)(32 * warp) << 16);
+        const float scale2 = a.scale * kLog2e;
+        const int i0 = 16 * warp + (lane >> 2);  // this thread's rows of the row tile: i0 and i0 + 8
+        int it = 0;
+        int st_prev = 0;          // stage and parity of the empty barrier of tile it - 1
+        uint32_t ph_prev = 0;
+        int st = 0;
+        uint32_t ph = 0;
+        walk(p, b_start, off_start, g0, g1, rt, NR, read_once, [&](int b, const Seq &s, int32_t off, int32_t nt, int64_t at) {
+            const int rows = min(NR, s.nq * H - rt * NR);
+            const bool act = 16 * warp < rows;
+            const int64_t orow = s.c0 * H + rt * NR;  // output row of the row tile's first row
+            // ---- the queries, K-major; every product that read the last piece's is done ----
+            const int nw = d / 8;
+            for (int u = tid; u < NR * nw; u += SW * 32) {
+                const int i = u / nw, w = u - i * nw, r = rt * NR + i;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (i < rows) {
+                    const int t = r / H, h = r - t * H;
+                    v = __ldg(reinterpret_cast<const uint4 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs) + w);
+                }
+                *reinterpret_cast<uint4 *>(Q + (w >> 3) * (NR * 128) + i * 128 + (((w ^ i) & 7) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
+            if (rt == 0 && tid == 0 && off == 0) {
+                const int64_t last = (at + s.tiles - 1) / per;
+                Meta m;
+                m.pieces = (int32_t)(last - g) + 1;
+                m.group = g;
+                m.second = at != g0;
+                m.seq = b;
+                if (p.by_seq)
+                    p.meta[b] = m;
+                else if (m.pieces > 1)
+                    p.meta[g] = m;
+            }
+            // what the thread's two rows see among the drafted tokens
+            const int base = s.len - s.nq;
+            uint64_t see[2];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+            for (int k = 0; k < 2; ++k) {
+                const int i = i0 + 8 * k;
+                const int t = i < rows ? (rt * NR + i) / H : 0;
+                const uint64_t chain = t >= 63 ? ~0ull : (2ull << t) - 1, all = s.nq >= 64 ? ~0ull : (1ull << s.nq) - 1;
+                see[k] = (a.tree ? a.tree[s.c0 + t] : chain) & all;
+            }
+            const bool scan_drafts = s.nq > 1 || a.tree;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int j = 0; j < nt; ++j, ++it) {
+                const int key0 = (off + j) * TILE;
+                wait(s_full + (it & 1), (uint32_t)(it >> 1) & 1u);
+                umma::fence_after();
+                const bool tail = key0 + TILE > base;
+                if (tail) {
+                    // rows behind the sequence become zeros (a zero weight times NaN is NaN); drafted rows that
+                    // are not finite do too, and count as NaN scores for the queries that see them
+                    wait(full + st, ph);
+                    uint8_t *x = KV + (uint32_t)(st * nch) * CHUNK;
+                    const int valid = min(TILE, s.len - key0);
+                    for (int r = valid + warp; r < TILE; r += SW)
+                        for (int w = lane; w < rank / 8; w += 32)
+                            *reinterpret_cast<uint4 *>(x + (w >> 3) * CHUNK + r * 128 + ((w & 7) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                    if (scan_drafts)
+                        for (int r = max(0, base - key0) + warp; r < valid; r += SW) {
+                            bool bad = false;
+                            for (int w = lane; w < nw; w += 32)
+                                bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(
+                                    x + (w >> 3) * CHUNK + r * 128 + (((w ^ r) & 7) << 4)));
+                            bad = __any_sync(0xffffffffu, bad);
+                            if (bad)
+                                for (int w = lane; w < rank / 8; w += 32)
+                                    *reinterpret_cast<uint4 *>(x + (w >> 3) * CHUNK + r * 128 + ((w & 7) << 4)) =
+                                        make_uint4(0, 0, 0, 0);
+                            if (lane == 0) poison[r] = bad;
+                        }
+                    fence_proxy_async_smem();
+                    softmax_sync();
+                }
+                uint32_t sr[32];
+                bool raised = false;
+                if (act) {
+                    ld16x64_issue(quad + T_S + (it & 1) * TILE, sr);
+                    umma::wait_ld(sr);
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int k = (e >> 1) & 1;
+                        float x = __uint_as_float(sr[e]) * scale2;
+                        if (tail) {
+                            const int col = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), dr = key0 + col - base;
+                            if (dr >= 0) {
+                                if (dr >= 64 || !(see[k] >> dr & 1))
+                                    x = -INFINITY;
+                                else if (scan_drafts && poison[col])
+                                    x = NAN;
+                            }
+                        }
+                        sr[e] = __float_as_uint(x);
+                        mx[k] = fmaxf(mx[k], x);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                        float f = 1.f;
+                        if (j == 0) {
+                            m[k] = mx[k];
+                        } else if (mx[k] > m[k] + kRaise) {
+                            f = exp2_(m[k] - mx[k]);  // 0 from -inf
+                            m[k] = mx[k];
+                            l[k] *= f;
+                            raised = true;
+                        }
+                        if ((lane & 3) == 0) fs[(it & 1) * 64 + i0 + 8 * k] = f;
+                    }
+                }
+                const bool rescale = j > 0 && softmax_any(raised);
+                if (it > 0) {  // O^T and P are this warp's again
+                    wait(empty + st_prev, ph_prev);
+                    umma::fence_after();
+                }
+                if (rescale) {
+                    const float *f = fs + (it & 1) * 64;
+                    for (int mb = 0; mb < rank / 128; ++mb)
+                        for (int c = 0; c < NR; c += 16) {
+                            uint32_t o[16];
+                            umma::ld16_issue(quad + mb * NR + c, o);
+                            umma::wait_ld16(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[c + e]);
+                            st16_issue(quad + mb * NR + c, o);
+                        }
+                    umma::wait_st();
+                }
+                if (act) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float mm = m[k] == -INFINITY ? 0.f : m[k];
+                        const int i = i0 + 8 * k;
+                        uint8_t *prow = P + i * 128;
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            const float p0 = exp2_(__uint_as_float(sr[4 * n + 2 * k]) - mm);
+                            const float p1 = exp2_(__uint_as_float(sr[4 * n + 2 * k + 1]) - mm);
+                            l[k] += p0 + p1;
+                            *reinterpret_cast<uint32_t *>(prow + (((n ^ i) & 7) << 4) + 4 * (lane & 3)) =
+                                pack2<FP16>(p0, p1);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready);
+                st_prev = st;
+                ph_prev = ph;
+                if (++st == nst) st = 0, ph ^= 1;
+            }
+            // ---- the piece is done: O^T / l out ----
+            const bool whole = off == 0 && nt == s.tiles;
+            const int64_t slot = ((int64_t)g * 2 + (at != g0)) * p.nrt + rt;
+            if (act) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                    const int i = i0 + 8 * k;
+                    if ((lane & 3) == 0) {
+                        inv[i] = l[k] == 0.f ? 0.f : 1.f / l[k];
+                        const float l2 = l[k] == 0.f ? -INFINITY : m[k] + __log2f(l[k]);
+                        if (!whole)
+                            p.part_l[slot * NR + i] = l2;
+                        else if (a.lse && i < rows)
+                            a.lse[orow + i] = l2 * kLn2;
+                    }
+                }
+            }
+            softmax_sync();
+            wait(empty + st_prev, ph_prev);
+            umma::fence_after();
+            for (int mb = 0; mb < rank / 128; ++mb) {
+                const int ch = mb * 128 + 32 * warp + lane;  // this thread's channel
+                for (int c = 0; c < rows; c += 16) {
+                    uint32_t o[16];
+                    umma::ld16_issue(quad + mb * NR + c, o);
+                    umma::wait_ld16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int i = c + e;
+                        if (i < rows) {
+                            const float v = __uint_as_float(o[e]) * inv[i];
+                            if (whole)
+                                a.out[(orow + i) * rank + ch] = to_elem<FP16>(v);
+                            else
+                                p.part[(slot * NR + i) * rank + ch] = v;
+                        }
+                    }
+                }
+            }
+            umma::fence_before();
+            return true;
+        });
+        __syncthreads_or(!ok);
+    }
+    if (!ok && lane == 0) set_status(a.status, KDA_DEV_TIMEOUT);
+    umma::fence_before();
+    __syncthreads();
+    if (warp == 5) umma::dealloc(tmem, TCOLS);
+}
+
+// Joins the parts of cut sequences: one CTA per row and cut sequence; its warps take parts in turn.
+template <int NR, bool FP16>
+__global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const DecodeP p) {
+    __shared__ float acc_s[CW][512];
+    __shared__ float ml[CW][2];
+    const LatentDecodeArgs &a = p.a;
+    const Meta mt = p.meta[blockIdx.y];
+    if (mt.pieces < 2) return;
+    const Seq s = seq_of(a, mt.seq);
+    const int r = blockIdx.x, rt = r / NR, i = r - rt * NR;
+    if (r >= s.nq * a.H) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.c.rank, nv = rank / 128;
     float m = -INFINITY, l = 0.f;
-    for (int64_t j = 0; j < len; ++j) {
-        const int64_t drafted = j - (len - nq);
-        if (drafted >= 0 && !(seen >> drafted & 1)) continue;
-        const int32_t page = a.t.table[(int64_t)row * a.t.max_pages + j / a.t.page_size];
-        const bool ok = page >= 0 && page < a.t.num_pages;
-        if (!ok && lane == 0) set_status(a.status, KDA_DEV_BAD_PAGE);
-        const uint16_t *x = a.c.pages + (ok ? page : 0) * a.c.page_stride + (j % a.t.page_size) * d;
-        float v[18], s = 0.f;
+    float4 acc[4];
 #pragma unroll
-        for (int k = 0; k < 18; ++k) {
-            v[k] = ok && lane + 32 * k < d ? elem(x[lane + 32 * k], a.c.fp16) : 0.f;
-            s = fmaf(q[k], v[k], s);
-        }
-        s = warp_sum(s);
-        bool fin = true;  // a key that is not finite makes its queries NaN, also where the score would hide it
+    for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = warp; k < mt.pieces; k += CW) {
+        const int64_t slot = ((int64_t)(mt.group + k) * 2 + (k == 0 ? mt.second : 0)) * p.nrt + rt;
+        const float lk = p.part_l[slot * NR + i];
+        const float4 *o = reinterpret_cast<const float4 *>(p.part + (slot * NR + i) * rank);
+        float4 x[4];
 #pragma unroll
-        for (int k = 0; k < 18; ++k) fin &= isfinite(v[k]);
-        if (!__all_sync(0xffffffffu, fin)) s = NAN;
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - mn);
-        l = l * f + p;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * f + p * v[k];
+        for (int v = 0; v < 4; ++v)
+            if (v < nv) x[v] = __ldcs(o + v * 32 + lane);
+        if (lk == -INFINITY) continue;  // nothing seen in this part
+        const float mn = fmaxf(m, lk), f = m == -INFINITY ? 0.f : exp2_(m - mn), w = exp2_(lk - mn);
+        l = l * f + w;
         m = mn;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = a.out + ((c0 + t) * a.H + h) * a.c.rank;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        if (lane + 32 * k < a.c.rank) out[lane + 32 * k] = to_elem(o[k] * inv, a.c.fp16);
-    if (a.lse && lane == 0) a.lse[(c0 + t) * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
+        for (int v = 0; v < 4; ++v)
+            if (v < nv) {
+                acc[v].x = acc[v].x * f + w * x[v].x;
+                acc[v].y = acc[v].y * f + w * x[v].y;
+                acc[v].z = acc[v].z * f + w * x[v].z;
+                acc[v].w = acc[v].w * f + w * x[v].w;
+            }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (v < nv) *reinterpret_cast<float4 *>(&acc_s[warp][(v * 32 + lane) * 4]) = acc[v];
+    if (lane == 0) {
+        ml[warp][0] = m;
+        ml[warp][1] = l;
+    }
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.f, f[CW];
+#pragma unroll
+    for (int w = 0; w < CW; ++w) mm = fmaxf(mm, ml[w][0]);
+#pragma unroll
+    for (int w = 0; w < CW; ++w) {
+        f[w] = ml[w][0] == -INFINITY ? 0.f : exp2_(ml[w][0] - mm);
+        ll += f[w] * ml[w][1];
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int64_t orow = s.c0 * a.H + r;
+    for (int ch = threadIdx.x * 2; ch < rank; ch += CW * 64) {
+        float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+            o0 += f[w] * acc_s[w][ch];
+            o1 += f[w] * acc_s[w][ch + 1];
+        }
+        *reinterpret_cast<uint32_t *>(a.out + orow * rank + ch) = pack2<FP16>(o0 * inv, o1 * inv);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[orow] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
+}
+
+// Rows of a row tile: the fewest that hold all rows of a sequence, 64 where none does.
+static int rows_per_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct Plan {
+    int NR, nrt, groups, slots_meta;
+    size_t off_part, off_l, bytes;
+};
+
+static Plan plan(int rank, int H, int n, int max_tokens) {
+    Plan q;
+    const int rows = H * max_tokens;
+    q.NR = rows_per_tile(rows);
+    q.nrt = (rows + q.NR - 1) / q.NR;
+    q.groups = std::max(1, current_device_sms() / q.nrt);
+    q.slots_meta = std::min(n, q.groups);
+    const size_t parts = (size_t)q.groups * 2 * q.nrt * q.NR;
+    q.off_part = ((size_t)q.slots_meta * sizeof(Meta) + 255) / 256 * 256;
+    q.off_l = q.off_part + parts * rank * 4;
+    q.bytes = q.off_l + parts * 4;
+    return q;
+}
+
+template <int NR, bool FP16>
+static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return launch_result("latent decode: cudaGetDevice");
+    if (!(done.load() >> dev & 1)) {
+        if (cudaFuncSetAttribute(kda_latent_decode_kernel<NR, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SMEM_MAX) != cudaSuccess)
+            return launch_result("latent decode: cudaFuncSetAttribute");
+        done.fetch_or(1ull << dev);
+    }
+    const EncodeTiledFn enc = encoder();
+    if (!enc) return fail(KDA_ERR_CUDA, "latent decode: cuTensorMapEncodeTiled is not available");
+    CUtensorMap map;
+    const int d = a.c.rank + a.c.rope;
+    if (!map_3d(enc, &map, FP16, a.c.pages, d, a.c.page_size, a.c.num_pages, d, a.c.page_stride,
+                std::min(a.c.page_size, TILE), 1))
+        return fail(KDA_ERR_CUDA, "latent decode: tensor map encoding failed");
+    DecodeP p;
+    p.a = a;
+    p.groups = q.groups;
+    p.nrt = q.nrt;
+    p.nch = (d + 63) / 64;
+    p.by_seq = a.n <= q.groups;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    p.meta = reinterpret_cast<Meta *>(ws);
+    p.part = reinterpret_cast<float *>(ws + q.off_part);
+    p.part_l = reinterpret_cast<float *>(ws + q.off_l);
+    const uint32_t fixed = 1024 + (uint32_t)p.nch * NR * 128 + NR * 128 + MISC;
+    p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / (p.nch * CHUNK));
+    const uint32_t smem = fixed + p.nst * p.nch * CHUNK;
+    kda_latent_decode_kernel<NR, FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map);
+    const int rc = launch_result("kda_latent_decode_kernel launch");
+    if (rc != KDA_OK) return rc;
+    kda_latent_combine_kernel<NR, FP16><<<dim3(a.H * a.max_tokens, q.slots_meta), CW * 32, 0, st>>>(p);
+    return launch_result("kda_latent_combine_kernel launch");
 }
 
 }  // namespace latent
 
-size_t latent_decode_workspace_bytes(int, int, int, int) { return 16; }
+size_t latent_decode_workspace_bytes(int rank, int H, int n, int max_tokens) {
+    return latent::plan(rank, H, std::max(n, 1), max_tokens).bytes;
+}
 
 int launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st) {
-    latent::kda_latent_decode_kernel<<<dim3(a.max_tokens * a.H, a.n), 32, 0, st>>>(a);
-    return launch_result("kda_latent_decode_kernel launch");
+    using namespace latent;
+    const Plan q = plan(a.c.rank, a.H, a.n, a.max_tokens);
+    if (a.c.fp16)
+        return q.NR == 16   ? launch<16, true>(a, q, st)
+               : q.NR == 32 ? launch<32, true>(a, q, st)
+                            : launch<64, true>(a, q, st);
+    return q.NR == 16   ? launch<16, false>(a, q, st)
+           : q.NR == 32 ? launch<32, false>(a, q, st)
+                        : launch<64, false>(a, q, st);
 }
 
 }  // namespace kda
