@@ -1,67 +1,426 @@
 // kda_latent_prefill.cu -- expanded latent attention for prompts (include/kda.h: kda_latent_prefill).
 //
-// One warp per (query, head): the query stays in registers, the keys stream past it, and the softmax runs
-// online (maximum m, sum l of exp(s - m), weighted sum o; all fp32).
-#include <cuda_fp16.h>
+//   s_ij = scale (q_i . [k_j | r_j]),   o_i = sum_j softmax(s_i)_j v_j   per head, r shared by the heads
+//
+// 2 (nope + rope + dv) operations a pair against a few bytes: the tensor cores bound it.  One CTA takes 256 queries
+// (two tiles of 128) of one head and walks the keys in tiles of 128; the scores of one query tile are turned into
+// weights while the tensor core works for the other.  12 warps, one CTA per SM:
+//   warps 0-3, 4-7  softmax of query tile 0, 1: a thread per row (tensor-memory lane), so maxima and sums need no
+//                   exchange; the weights go back to tensor memory over the scores they came from
+//   warp 8   TMA: keys, rotary keys and values as units of 128 rows x 64 channels (16 KiB), one ring
+//   warp 9   MMA: S = Q [K | R]^T (M 128, N 128), then O += P V with P in tensor memory and V as it lies (MN-major).
+//            Order O0(j), S0(j+1), O1(j), S1(j+1): one tile's softmax runs beside the other's two products.
+//   warp 10  value rows that a query of the CTA does not see: those behind the sequence become zeros, and
+//            those that are not finite too (0 x NaN is NaN), with a mark that makes the weights of the queries
+//            that see them NaN.  Only tiles that some query sees in part need it.
+// Tensor memory: S0 S1 O0 O1, 128 columns each.  The running maximum is raised only by more than 2^8 (kRaise), by the
+// row's own thread in place.  Weights are rounded to the element type for the second product (its operands are
+// 16-bit); their sum is kept in fp32 from the unrounded weights.
+// Query tiles are dealt out from the last (under a causal mask the longest) to the first.
+#include <algorithm>
 
-#include "kda_device.cuh"
-#include "kda_internal.h"
+#include "kda_latent.cuh"
 
 namespace kda {
 namespace latent {
 
-__device__ __forceinline__ float elem2(uint16_t x, bool fp16) {
-    return fp16 ? __half2float(__ushort_as_half(x)) : bf2f(x);
-}
-__device__ __forceinline__ uint16_t to_elem2(float x, bool fp16) {
-    return fp16 ? __half_as_ushort(__float2half_rn(x)) : f2bf(x);
-}
+constexpr int PQ = 128, PK = 128;        // queries of a tile, keys of a tile
+constexpr int PNT = 384;                 // threads: 12 warps, the last of them idle (registers come in warpgroups)
+// Registers: launched with 168 a thread (64,512 of 65,536); the two softmax warpgroups take 208, the other gives down
+// to 80: 2 * 128 * 208 + 128 * 80 = 63,488, within what the launch holds.
+constexpr uint32_t UNIT = PK * 128;      // bytes of 128 rows x 64 channels
+constexpr int MAX_UNITS = 11;            // less than four tiles of the fewest units (3)
+constexpr uint32_t PSMEM_MAX = 227 * 1024;
+constexpr uint32_t PMISC = 1024;         // barriers and marks
 
-__global__ void __launch_bounds__(128) kda_latent_prefill_kernel(const LatentPrefillArgs a) {
-    const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
-    const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.num_q || k0 < 0 || k1 < k0 || k1 > a.num_k || q1 - q0 > a.max_q) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, KDA_DEV_BAD_SEQLENS);
+struct PrefillP {
+    LatentPrefillArgs a;
+    int32_t units;  // of the ring
+};
+
+template <bool FP16>
+__global__ void __launch_bounds__(PNT, 1)
+    kda_latent_prefill_kernel(const PrefillP p, const __grid_constant__ CUtensorMap mq,
+                              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
+                              const __grid_constant__ CUtensorMap mv) {
+    const LatentPrefillArgs &a = p.a;
+    const int h = blockIdx.x, b = blockIdx.y;
+    const int64_t q_lo = a.cu_q[b], q_hi = a.cu_q[b + 1], k_lo = a.cu_k[b], k_hi = a.cu_k[b + 1];
+    if (q_lo < 0 || q_hi < q_lo || q_hi > a.num_q || k_lo < 0 || k_hi < k_lo || k_hi > a.num_k || q_hi - q_lo > a.max_q) {
+        if (h == 0 && blockIdx.z == 0 && threadIdx.x == 0) set_status(a.status, KDA_DEV_BAD_SEQLENS);
         return;
     }
-    const int64_t nq = q1 - q0, nk = k1 - k0, i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (i >= nq) return;
-    const int64_t end = a.causal ? max((int64_t)0, min(nk, i + nk - nq + 1)) : nk;
-    const int dq = a.nope + a.rope;
-    const uint16_t *qp = a.q + (q0 + i) * a.q_ts + h * a.q_hs;
-    float q[6], o[4] = {0.f, 0.f, 0.f, 0.f};
+    const int nq = (int)(q_hi - q_lo), nk = (int)(k_hi - k_lo);
+    const int qt = (int)(gridDim.z - 1 - blockIdx.z) * 2 * PQ;  // first query of the CTA
+    if (qt >= nq) return;
+    // keys that query i sees: [0, limit(i))
+    const int shift = nk - nq + 1;
+    auto limit = [&](int i) { return a.causal ? max(0, min(nk, i + shift)) : nk; };
+    int nt[2];  // key tiles of the two query tiles
 #pragma unroll
-    for (int k = 0; k < 6; ++k) q[k] = lane + 32 * k < dq ? elem2(qp[lane + 32 * k], a.fp16) * a.scale : 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int64_t j = k0; j < k0 + end; ++j) {
-        const uint16_t *kp = a.k + j * a.k_ts + h * a.k_hs, *rp = a.r + j * a.r_ts, *vp = a.v + j * a.v_ts + h * a.v_hs;
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 6; ++k) {
-            const int e = lane + 32 * k;
-            if (e < dq) s = fmaf(q[k], elem2(e < a.nope ? kp[e] : rp[e - a.nope], a.fp16), s);
-        }
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - mn);
-        l = l * f + p;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < a.dv) o[k] = o[k] * f + p * elem2(vp[lane + 32 * k], a.fp16);
-        m = mn;
+    for (int t = 0; t < 2; ++t) {
+        const int last = min(nq, qt + (t + 1) * PQ) - 1;
+        nt[t] = last < qt + t * PQ ? 0 : (limit(last) + PK - 1) / PK;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = a.out + ((q0 + i) * a.H + h) * a.dv;
+    const int ntile = max(nt[0], nt[1]);
+    const int jf = limit(qt) / PK;  // from this tile on some query sees a part only
+    const int kc = a.nope / 64 + 1, vc = a.dv / 64, per = kc + vc;  // units of a key tile, of a value tile, of both
+    const int NU = p.units;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *Q = sm;                                  // [2][kc] units
+    uint8_t *R = Q + (uint32_t)(2 * kc) * UNIT;       // the ring
+    uint64_t *full = reinterpret_cast<uint64_t *>(R + (uint32_t)NU * UNIT);
+    uint64_t *empty = full + MAX_UNITS;
+    uint64_t *q_full = empty + MAX_UNITS;
+    uint64_t *s_full = q_full + 1;   // [2] scores of a query tile
+    uint64_t *p_ready = s_full + 2;  // [2] its weights
+    uint64_t *o_done = p_ready + 2;  // [2] its output
+    uint64_t *fixed = o_done + 2;    // [4] value tiles looked over by warp 10
+    uint64_t *v_raw = fixed + 4;     // [4] such tiles as they were loaded (at most 3 fit the ring)
+    uint64_t *drain = v_raw + 4;
+    uint32_t *any = reinterpret_cast<uint32_t *>(drain + 1);  // [4] whether a value tile has marks
+    uint32_t *tmem_s = any + 4;
+    uint8_t *mark = reinterpret_cast<uint8_t *>(tmem_s + 1);  // [4][PK]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 9) umma::alloc(tmem_s, 512);
+    if (tid == 0) {
+        for (int u = 0; u < MAX_UNITS; ++u) {
+            mbar_init(full + u, 1);
+            mbar_init(empty + u, 1);
+        }
+        mbar_init(q_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + t, 1);
+            mbar_init(p_ready + t, 4);
+            mbar_init(o_done + t, 1);
+        }
+        for (int t = 0; t < 4; ++t) {
+            mbar_init(fixed + t, 1);
+            mbar_init(v_raw + t, 1);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = *tmem_s;
+    constexpr uint32_t T_O = 2 * PK;
+    bool ok = true;
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+        // ================================ producer ================================
+        int idx = 0;
+        if (lane == 0 && ntile > 0) {
+            mbar_arrive_expect_tx(q_full, (uint32_t)(2 * kc) * UNIT);
+            for (int t = 0; t < 2; ++t)
+                for (int c = 0; c < kc; ++c)
+                    tma_load_3d(Q + (uint32_t)(t * kc + c) * UNIT, &mq, c * 64, h, (int)q_lo + qt + t * PQ, q_full);
+            int u = 0;
+            uint32_t ph = 1;
+            for (int j = 0; j < ntile && ok; ++j) {
+                const int row = (int)k_lo + j * PK;
+                for (int c = 0; c < per; ++c, ++idx) {
+                    ok = idx < NU || mbar_wait(empty + u, ph);
+                    if (!ok) break;
+                    uint8_t *dst = R + (uint32_t)u * UNIT;
+                    if (c >= kc && j >= jf) {  // values that warp 10 looks over first: it has their barrier
+                        uint64_t *bar = v_raw + ((j - jf) & 3);
+                        if (c == kc) mbar_arrive_expect_tx(bar, (uint32_t)vc * UNIT);
+                        tma_load_3d(dst, &mv, (c - kc) * 64, h, row, bar);
+                        mbar_arrive(full + u);
+                        if (++u == NU) u = 0, ph ^= 1;
+                        continue;
+                    }
+                    mbar_arrive_expect_tx(full + u, UNIT);
+                    if (c < kc - 1)
+                        tma_load_3d(dst, &mk, c * 64, h, row, full + u);
+                    else if (c < kc)
+                        tma_load_3d(dst, &mr, 0, 0, row, full + u);
+                    else
+                        tma_load_3d(dst, &mv, (c - kc) * 64, h, row, full + u);
+                    if (++u == NU) u = 0, ph ^= 1;
+                }
+            }
+        }
+        if (__syncthreads_or(!ok) && lane == 0 && ntile > 0) {  // copies still in flight land before the CTA ends
+            constexpr uint64_t kDrainNs = 10000000ull;
+            mbar_wait(q_full, 0, kDrainNs);
+            for (int k = max(0, idx - NU); k < idx; ++k) {
+                mbar_wait(full + k % NU, (uint32_t)(k / NU) & 1u, kDrainNs);
+                const int f = k / per - jf;
+                if (f >= 0 && k % per >= kc) mbar_wait(v_raw + (f & 3), (uint32_t)(f >> 2) & 1u, kDrainNs);
+            }
+        }
+    } else if (warp == 9) {
+        // ================================ MMA issuer ================================
+        if (lane == 0 && ntile > 0) {
+            const uint32_t id_s = umma::idesc(kFmt<FP16>, PQ, PK);
+            const uint32_t id_o = umma::idesc(kFmt<FP16>, PQ, 64) | kBMajorMN;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
+            auto scores = [&](int t, int j) {  // S_t = Q_t [K | R]^T of tile j, whose units are in
+                for (int c = 0; c < kc; ++c) {
+                    const int u = (j * per + c) % NU;
+                    const uint64_t dq = umma::sdesc(smem_addr(Q + (uint32_t)(t * kc + c) * UNIT));
+                    const uint64_t dk = umma::sdesc(smem_addr(R + (uint32_t)u * UNIT));
+                    const int ks = c < kc - 1 ? 4 : a.rope / 16;
+                    for (int k = 0; k < ks; ++k)
+                        umma::mma_bf16(tmem + t * PK, dq + 2 * k, dk + 2 * k, id_s, c > 0 || k > 0);
+                }
+                umma::commit(s_full + t);
+            };
+            auto units_in = [&](int first, int n) {
+                for (int i = first; i < first + n; ++i) wait(full + i % NU, (uint32_t)(i / NU) & 1u);
+            };
+            auto release = [&](int first, int n) {
+                for (int i = first; i < first + n; ++i) umma::commit(empty + i % NU);
+            };
+            wait(q_full, 0);
+            units_in(0, kc);
+            umma::fence_after();
+            if (ok) {
+                for (int t = 0; t < 2; ++t)
+                    if (nt[t] > 0) scores(t, 0);
+                release(0, kc);
+            }
+            for (int j = 0; j < ntile && ok; ++j) {
+                const int v0 = j * per + kc, k1 = (j + 1) * per;
+                bool v_in = false, k_in = false;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j >= nt[t]) continue;
+                    if (!v_in) {
+                        units_in(v0, vc);
+                        if (j >= jf) wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
+                        v_in = true;
+                    }
+                    wait(p_ready + t, (uint32_t)j & 1u);
+                    if (!ok) break;
+                    umma::fence_after();
+                    for (int c = 0; c < vc; ++c) {
+                        const uint64_t dv = sdesc_mn(smem_addr(R + (uint32_t)((v0 + c) % NU) * UNIT), UNIT);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (lane + 32 * k < a.dv) out[lane + 32 * k] = to_elem2(o[k] * inv, a.fp16);
-    if (a.lse && lane == 0) a.lse[(q0 + i) * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
+                        for (int k = 0; k < PK / 16; ++k)
+                            mma_ts(tmem + T_O + t * 128 + c * 64, tmem + t * PK + k * 8, dv + (uint64_t)(k * 2048 >> 4),
+                                   id_o, j > 0 || k > 0);
+                    }
+                    if (j + 1 == nt[t]) umma::commit(o_done + t);
+                    if (t == 1 || j >= nt[1]) release(v0, vc);
+                    if (j + 1 < nt[t]) {
+                        if (!k_in) {
+                            units_in(k1, kc);
+                            if (!ok) break;
+                            umma::fence_after();
+                            k_in = true;
+                        }
+                        scores(t, j + 1);
+                        if (t == 1 || j + 1 >= nt[1]) release(k1, kc);
+                    }
+                }
+            }
+        }
+        if (__syncthreads_or(!ok) && lane == 0) {
+            umma::commit(drain);
+            mbar_wait(drain, 0, 10000000ull);
+        }
+    } else if (warp == 10) {
+        // ================================ value rows that not every query sees ================================
+        for (int j = jf; j < ntile && ok; ++j) {
+            const int f = j - jf, v0 = j * per + kc, valid = min(PK, nk - j * PK);
+            ok = __all_sync(0xffffffffu, mbar_wait(v_raw + (f & 3), (uint32_t)(f >> 2) & 1u));
+            if (!ok) break;
+            uint8_t *mk4 = mark + (f & 3) * PK;
+            bool found = false;
+            // a lane per group of rows: each row's 64 or 128 channels are 8 or 16 words
+            for (int r0 = 0; r0 < PK; r0 += 32) {
+                const int r = r0 + lane;
+                bool bad = false;
+                for (int c = 0; c < vc; ++c) {
+                    const uint8_t *row = R + (uint32_t)((v0 + c) % NU) * UNIT + r * 128;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w)
+                        bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(row + (((w ^ lane) & 7) << 4)));
+                }
+                const bool mine = bad && r < valid;
+                if (bad || r >= valid)
+                    for (int c = 0; c < vc; ++c) {
+                        uint8_t *row = R + (uint32_t)((v0 + c) % NU) * UNIT + r * 128;
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+                            *reinterpret_cast<uint4 *>(row + (((w ^ lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                mk4[r] = mine;
+                found |= mine;
+            }
+            found = __any_sync(0xffffffffu, found);
+            if (lane == 0) any[f & 3] = found;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fixed + (f & 3));
+        }
+        __syncthreads_or(!ok);
+    } else {
+        __syncthreads_or(false);
+    }
+    } else {
+        // ================================ softmax ================================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + t * PK, to = tmem + lanes + T_O + t * 128;
+        const int i = qt + t * PQ + 32 * (warp & 3) + lane;  // this thread's query
+        const int lim = i < nq ? limit(i) : 0;
+        const float c = a.scale * kLog2e, raise = kRaise / c;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < nt[t] && ok; ++j) {
+            ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, (uint32_t)j & 1u));
+            if (!ok) break;
+            umma::fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) umma::ld32_issue(ts + 32 * g, s[g]);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) umma::wait_ld(s[g]);
+            if (j >= jf) {
+                const int left = lim - j * PK;  // keys of the tile that this query sees
+                ok = __all_sync(0xffffffffu, mbar_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u));
+                if (!ok) break;
+                if (any[(j - jf) & 3]) {
+                    const uint8_t *mk4 = mark + ((j - jf) & 3) * PK;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (mk4[32 * g + e]) s[g][e] = 0x7fffffffu;  // NaN
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * g + e >= left) s[g][e] = 0xff800000u;  // -inf
+            }
+            float mx[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                mx[g] = __uint_as_float(s[g][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[g] = fmaxf(mx[g], __uint_as_float(s[g][e]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float f = 1.f;
+            if (j == 0) {
+                m = top;
+            } else if (top > m + raise) {
+                f = exp2_((m - top) * c);  // 0 from -inf
+                m = top;
+                l *= f;
+            }
+            // the scores' commit covers the products before it: O of this query tile is complete up to tile j - 1
+            if (__any_sync(0xffffffffu, f != 1.f)) {
+                for (int k = 0; k < a.dv; k += 16) {
+                    uint32_t o[16];
+                    umma::ld16_issue(to + k, o);
+                    umma::wait_ld16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    st16_issue(to + k, o);
+                }
+                umma::wait_st();
+            }
+            const float mc = m == -INFINITY ? 0.f : m * c;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = exp2_(fmaf(__uint_as_float(s[g][e]), c, -mc));
+                    const float p1 = exp2_(fmaf(__uint_as_float(s[g][e + 1]), c, -mc));
+                    sum[(e >> 1) & 3] += p0 + p1;
+                    w[e >> 1] = pack2<FP16>(p0, p1);
+                }
+                st16_issue(ts + 16 * g, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            umma::wait_st();
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_ready + t);
+        }
+        if (ok && nt[t] > 0) ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, 0));
+        umma::fence_after();
+        if (ok && qt + t * PQ + 32 * (warp & 3) < nq) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int64_t row = (q_lo + i) * a.H + h;
+            for (int k = 0; k < a.dv; k += 16) {
+                uint32_t o[16];
+                if (nt[t] > 0) {
+                    umma::ld16_issue(to + k, o);
+                    umma::wait_ld16(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0;
+                }
+                if (i < nq) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = pack2<FP16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * a.dv + k);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+            if (a.lse && i < nq) a.lse[row] = l == 0.f ? -INFINITY : (m * c + __log2f(l)) * kLn2;
+        }
+        __syncthreads_or(!ok);
+    }
+    if (!ok && lane == 0) set_status(a.status, KDA_DEV_TIMEOUT);
+    umma::fence_before();
+    __syncthreads();
+    if (warp == 9) umma::dealloc(tmem, 512);
+}
+
+template <bool FP16>
+static int launch(const LatentPrefillArgs &a, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return launch_result("latent prefill: cudaGetDevice");
+    if (!(done.load() >> dev & 1)) {
+        if (cudaFuncSetAttribute(kda_latent_prefill_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PSMEM_MAX) != cudaSuccess)
+            return launch_result("latent prefill: cudaFuncSetAttribute");
+        done.fetch_or(1ull << dev);
+    }
+    const EncodeTiledFn enc = encoder();
+    if (!enc) return fail(KDA_ERR_CUDA, "latent prefill: cuTensorMapEncodeTiled is not available");
+    CUtensorMap mq, mk, mr, mv;
+    const int64_t nk = std::max<int64_t>(1, a.num_k);
+    // without any key the key maps are never read; the queries stand in for their memory
+    const void *k = a.num_k ? (const void *)a.k : a.q, *r = a.num_k ? (const void *)a.r : a.q,
+               *v = a.num_k ? (const void *)a.v : a.q;
+    if (!map_3d(enc, &mq, FP16, a.q, a.nope + a.rope, a.H, a.num_q, a.q_hs, a.q_ts, 1, PQ) ||
+        !map_3d(enc, &mk, FP16, k, a.nope, a.H, nk, a.k_hs, a.k_ts, 1, PK) ||
+        !map_3d(enc, &mr, FP16, r, a.rope, 1, nk, a.r_ts, a.r_ts, 1, PK) ||
+        !map_3d(enc, &mv, FP16, v, a.dv, a.H, nk, a.v_hs, a.v_ts, 1, PK))
+        return fail(KDA_ERR_CUDA, "latent prefill: tensor map encoding failed");
+    PrefillP p;
+    p.a = a;
+    const uint32_t kc = a.nope / 64 + 1, fixed = 1024 + 2 * kc * UNIT + PMISC;
+    p.units = std::min<int>(MAX_UNITS, (PSMEM_MAX - fixed) / UNIT);
+    const dim3 grid(a.H, a.nseq, (a.max_q + 2 * PQ - 1) / (2 * PQ));
+    kda_latent_prefill_kernel<FP16><<<grid, PNT, fixed + p.units * UNIT, st>>>(p, mq, mk, mr, mv);
+    return launch_result("kda_latent_prefill_kernel launch");
 }
 
 }  // namespace latent
 
 int launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st) {
-    latent::kda_latent_prefill_kernel<<<dim3((a.max_q + 3) / 4, a.H, a.nseq), 128, 0, st>>>(a);
-    return launch_result("kda_latent_prefill_kernel launch");
+    return a.fp16 ? latent::launch<true>(a, st) : latent::launch<false>(a, st);
 }
 
 }  // namespace kda
