@@ -74,12 +74,30 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t mn_stride)
     return d;
 }
 
+// One lane of a converged warp, the same each time.  MMAs are issued inside `if (elect_one())`: the compiler then knows
+// that a single thread is active and keeps their descriptors in uniform registers.  With `if (lane == 0)`, or with a
+// per-lane predicate on each instruction, one M 128, N 64 instruction took 85-90 cycles to issue (32 to execute).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
 // D += A B with A in tensor memory: lane = row, two consecutive 16-bit k in each column.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, bool acc) {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
             d_tmem),
         "r"(a_tmem), "l"(b), "r"(id), "r"((uint32_t)acc));
+}
+
+// mbar_wait() by a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 255u) == 0 && __any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
 }
 
 // Warp-wide, asynchronous: lanes 0..15 of this warp's quarter x 64 consecutive columns.  Register 4n + i of

@@ -204,13 +204,14 @@ __global__ void __launch_bounds__(NT, 1)
 
     if (warp == 4) {
         // ================================ producer ================================
-        const int ps = a.c.page_size, bps = min(ps, TILE), nb = TILE / bps;
+        const int ps = a.c.page_size, bps = min(ps, TILE), nb = TILE / bps, lb = 31 - __clz(nb);  // nb 1, 2 or 4
         int it = 0, st = 0;
         uint32_t ph = 1;  // a fresh ring is empty
         walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int64_t) {
             const int32_t *trow = a.t.table + (int64_t)s.row * a.t.max_pages;
             for (int j = 0; j < nt; ++j, ++it) {
                 const int key = (off + j) * TILE + lane * bps;  // below 2^31: len is
+                const int in_page = (off + j) * TILE % ps;      // of the tile's first box; 0 when a page is a box or less
                 int page = (int)a.c.num_pages;  // a box outside the tensor reads as zeros
                 if (lane < nb && key < s.len) {
                     const int e = __ldg(trow + key / ps);
@@ -219,17 +220,17 @@ __global__ void __launch_bounds__(NT, 1)
                     else
                         set_status(a.status, KDA_DEV_BAD_PAGE);
                 }
-                ok = __all_sync(0xffffffffu, it < nst || mbar_wait(empty + st, ph));
+                ok = it < nst || warp_wait(empty + st, ph);
                 if (!ok) return false;
                 if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)nch * CHUNK);
                 __syncwarp();
                 uint8_t *dst = KV + (uint32_t)(st * nch) * CHUNK;
                 for (int u0 = 0; u0 < nb * nch; u0 += 32) {
-                    const int u = u0 + lane, box = u % nb, c = u / nb;
+                    const int u = u0 + lane, box = u & (nb - 1), c = u >> lb;
                     const int pg = __shfl_sync(0xffffffffu, page, box);
                     if (u < nb * nch)
                         tma_load_3d(dst + c * CHUNK + box * bps * 128, &map, c * 64,
-                                    ((off + j) * TILE + box * bps) % ps, pg, full + st);
+                                    in_page, pg, full + st);
                 }
                 if (++st == nst) st = 0, ph ^= 1;
             }
@@ -243,71 +244,81 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp == 5) {
         // ================================ MMA issuer ================================
-        if (lane == 0) {
-            const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
-            const uint32_t id_o = umma::idesc(kFmt<FP16>, 128, NR) | kAMajorMN;
-            const uint64_t dq = umma::sdesc(smem_addr(Q)), dp = umma::sdesc(smem_addr(P));
-            const int nk = d / 16;
-            uint32_t pieces = 0;
-            int it = 0, st = 0;          // tile whose P V comes next, and its stage
-            uint32_t ph = 0;             // parity of the stage's full barrier
-            walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &, int32_t, int32_t nt, int64_t) {
-                ok = mbar_wait(q_ready, pieces++ & 1u);
-                if (!ok) return false;
-                umma::fence_after();
-                auto issue_s = [&](int buf, int stage) {
-                    const uint64_t dx = umma::sdesc(smem_addr(KV + (uint32_t)(stage * nch) * CHUNK));
-                    for (int k = 0; k < nk; ++k)
-                        umma::mma_bf16(tmem + T_S + buf * TILE, umma::sdesc_at(dq, NR, k), umma::sdesc_at(dx, TILE, k),
-                                       id_s, k > 0);
-                    umma::commit(s_full + buf);
-                };
-                bool issued = false;  // S of tile `it`
-                for (int j = 0; j < nt; ++j, ++it) {
-                    if (!issued) {
-                        ok = mbar_wait(full + st, ph);
-                        if (!ok) return false;
-                        umma::fence_after();
-                        issue_s(it & 1, st);
-                    }
-                    const int st1 = st + 1 == nst ? 0 : st + 1;
-                    const uint32_t ph1 = st1 ? ph : ph ^ 1u;
-                    // whichever comes first: the weights of this tile, or the rows of the next
-                    issued = false;
-                    uint64_t t0 = 0;
-                    for (uint32_t spin = 1; !mbar_try_wait(p_ready, it & 1u); ++spin) {
-                        if (!issued && j + 1 < nt && mbar_try_wait(full + st1, ph1)) {
-                            umma::fence_after();
-                            issue_s((it + 1) & 1, st1);
-                            issued = true;
-                        }
-                        if ((spin & 255u) == 0) {
-                            const uint64_t t = global_timer_ns();
-                            if (!t0) t0 = t;
-                            if (t - t0 > kWaitLimitNs) {
-                                ok = false;
-                                return false;
-                            }
-                        }
-                    }
+        const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
+        const uint32_t id_o = umma::idesc(kFmt<FP16>, 128, NR) | kAMajorMN;
+        const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dp = umma::sdesc(smem_addr(P));
+        const uint64_t dx0 = umma::sdesc(smem_addr(KV)), dc0 = sdesc_mn(smem_addr(KV), CHUNK);
+        const int ncr = rank / 64, kr = a.c.rope / 16;  // full chunks; instructions of the rotary chunk
+        const uint32_t stage_words = (uint32_t)nch * CHUNK >> 4;
+        uint32_t pieces = 0;
+        int it = 0, st = 0;  // tile whose P V comes next, and its stage
+        uint32_t ph = 0;     // parity of the stage's full barrier
+        walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &, int32_t, int32_t nt, int64_t) {
+            ok = warp_wait(q_ready, pieces++ & 1u);
+            if (!ok) return false;
+            umma::fence_after();
+            auto issue_s = [&](int buf, int stage) {
+                if (!elect_one()) return;
+                const uint32_t ts = tmem + T_S + buf * TILE;
+                uint64_t dq = dq0, dx = dx0 + (uint64_t)(stage * stage_words);
+                for (int c = 0; c < ncr; ++c) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, k > 0 || c > 0);
+                    dq += NR * 128 >> 4;
+                    dx += CHUNK >> 4;
+                }
+                for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, true);
+                umma::commit(s_full + buf);
+            };
+            bool issued = false;  // S of tile `it`
+            for (int j = 0; j < nt; ++j, ++it) {
+                if (!issued) {
+                    ok = warp_wait(full + st, ph);
+                    if (!ok) return false;
                     umma::fence_after();
-                    const uint32_t x = smem_addr(KV + (uint32_t)(st * nch) * CHUNK);
+                    issue_s(it & 1, st);
+                }
+                const int st1 = st + 1 == nst ? 0 : st + 1;
+                const uint32_t ph1 = st1 ? ph : ph ^ 1u;
+                // whichever comes first: the weights of this tile, or the rows of the next
+                issued = false;
+                uint64_t t0 = 0;
+                for (uint32_t spin = 1; !__all_sync(0xffffffffu, mbar_try_wait(p_ready, it & 1u)); ++spin) {
+                    if (!issued && j + 1 < nt && __all_sync(0xffffffffu, mbar_try_wait(full + st1, ph1))) {
+                        umma::fence_after();
+                        issue_s((it + 1) & 1, st1);
+                        issued = true;
+                    }
+                    if ((spin & 255u) == 0) {
+                        const uint64_t t = global_timer_ns();
+                        if (!t0) t0 = t;
+                        if (__any_sync(0xffffffffu, t - t0 > kWaitLimitNs)) {
+                            ok = false;
+                            return false;
+                        }
+                    }
+                }
+                umma::fence_after();
+                if (elect_one()) {
+                    uint64_t dc = dc0 + (uint64_t)(st * stage_words);
+                    uint32_t to = tmem;
                     for (int m = 0; m < rank / 128; ++m) {
-                        const uint64_t dc = sdesc_mn(x + 2 * m * CHUNK, CHUNK);
 #pragma unroll
                         for (int k = 0; k < TILE / 16; ++k)
-                            umma::mma_bf16(tmem + m * NR, dc + (uint64_t)(k * 2048 >> 4), umma::sdesc_at(dp, NR, k), id_o,
-                                           j > 0 || k > 0);
+                            umma::mma_bf16(to, dc + (uint64_t)(k * 2048 >> 4), dp + 2 * k, id_o, j > 0 || k > 0);
+                        dc += 2 * CHUNK >> 4;
+                        to += NR;
                     }
                     umma::commit(empty + st);  // O^T holds this tile, and its stage is free
-                    st = st1;
-                    ph = ph1;
                 }
-                return true;
-            });
-        }
-        if (__syncthreads_or(!ok) && lane == 0) {
-            umma::commit(drain);
+                __syncwarp();
+                st = st1;
+                ph = ph1;
+            }
+            return true;
+        });
+        if (__syncthreads_or(!ok)) {
+            if (elect_one()) umma::commit(drain);
             mbar_wait(drain, 0, 10000000ull);
         }
     } else {

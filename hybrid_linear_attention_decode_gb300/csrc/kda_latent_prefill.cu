@@ -159,72 +159,94 @@ __global__ void __launch_bounds__(PNT, 1)
         }
     } else if (warp == 9) {
         // ================================ MMA issuer ================================
-        if (lane == 0 && ntile > 0) {
-            const uint32_t id_s = umma::idesc(kFmt<FP16>, PQ, PK);
-            const uint32_t id_o = umma::idesc(kFmt<FP16>, PQ, 64) | kBMajorMN;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
-            auto scores = [&](int t, int j) {  // S_t = Q_t [K | R]^T of tile j, whose units are in
-                for (int c = 0; c < kc; ++c) {
-                    const int u = (j * per + c) % NU;
-                    const uint64_t dq = umma::sdesc(smem_addr(Q + (uint32_t)(t * kc + c) * UNIT));
-                    const uint64_t dk = umma::sdesc(smem_addr(R + (uint32_t)u * UNIT));
-                    const int ks = c < kc - 1 ? 4 : a.rope / 16;
-                    for (int k = 0; k < ks; ++k)
-                        umma::mma_bf16(tmem + t * PK, dq + 2 * k, dk + 2 * k, id_s, c > 0 || k > 0);
-                }
-                umma::commit(s_full + t);
-            };
-            auto units_in = [&](int first, int n) {
-                for (int i = first; i < first + n; ++i) wait(full + i % NU, (uint32_t)(i / NU) & 1u);
-            };
-            auto release = [&](int first, int n) {
-                for (int i = first; i < first + n; ++i) umma::commit(empty + i % NU);
-            };
-            wait(q_full, 0);
-            units_in(0, kc);
+        const uint32_t id_s = umma::idesc(kFmt<FP16>, PQ, PK);
+        const uint32_t id_o = umma::idesc(kFmt<FP16>, PQ, 64) | kBMajorMN;
+        const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dr0 = umma::sdesc(smem_addr(R)),
+                       dv0 = sdesc_mn(smem_addr(R), UNIT);
+        const int kr = a.rope / 16;
+        constexpr uint32_t UW = UNIT >> 4;  // a unit in descriptor words
+        int cu = 0;                         // ring position and parity of the next unit to wait for
+        uint32_t cph = 0;
+        auto take = [&](int n) {            // waits for the next n units
+            for (int c = 0; c < n; ++c) {
+                ok = ok && warp_wait(full + cu, cph);
+                if (++cu == NU) cu = 0, cph ^= 1;
+            }
+        };
+        // the two lambdas below run in one thread
+        auto release = [&](int u, int n) {  // units u, u + 1, ... are free once the products so far are done
+            for (int c = 0; c < n; ++c) {
+                umma::commit(empty + u);
+                if (++u == NU) u = 0;
+            }
+        };
+        auto scores = [&](int t, int u) {  // S_t = Q_t [K | R]^T of the key tile at ring position u
+            const uint32_t ts = tmem + t * PK;
+            uint64_t dq = dq0 + (uint64_t)(t * kc * UW);
+            for (int c = 0; c < kc - 1; ++c) {
+                const uint64_t dk = dr0 + (uint64_t)(u * UW);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, c > 0 || k > 0);
+                dq += UW;
+                if (++u == NU) u = 0;
+            }
+            const uint64_t dk = dr0 + (uint64_t)(u * UW);
+            for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, true);
+            umma::commit(s_full + t);
+        };
+        if (ntile > 0) {
+            ok = warp_wait(q_full, 0);
+            take(kc);
             umma::fence_after();
-            if (ok) {
+            if (ok && elect_one()) {
                 for (int t = 0; t < 2; ++t)
                     if (nt[t] > 0) scores(t, 0);
                 release(0, kc);
             }
-            for (int j = 0; j < ntile && ok; ++j) {
-                const int v0 = j * per + kc, k1 = (j + 1) * per;
-                bool v_in = false, k_in = false;
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j >= nt[t]) continue;
-                    if (!v_in) {
-                        units_in(v0, vc);
-                        if (j >= jf) wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
-                        v_in = true;
-                    }
-                    wait(p_ready + t, (uint32_t)j & 1u);
-                    if (!ok) break;
-                    umma::fence_after();
+            __syncwarp();
+        }
+        for (int j = 0; j < ntile && ok; ++j) {
+            const int uv = cu;  // values of tile j, then keys of tile j + 1
+            take(vc);
+            if (j >= jf) ok = ok && warp_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
+            const int uk = cu;
+            bool k_in = false;
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (j >= nt[t]) continue;
+                ok = warp_wait(p_ready + t, (uint32_t)j & 1u);
+                if (!ok) break;
+                umma::fence_after();
+                if (elect_one()) {
+                    int u = uv;
                     for (int c = 0; c < vc; ++c) {
-                        const uint64_t dv = sdesc_mn(smem_addr(R + (uint32_t)((v0 + c) % NU) * UNIT), UNIT);
+                        const uint64_t dv = dv0 + (uint64_t)(u * UW);
+                        const uint32_t to = tmem + T_O + t * 128 + c * 64;
 #pragma unroll
                         for (int k = 0; k < PK / 16; ++k)
-                            mma_ts(tmem + T_O + t * 128 + c * 64, tmem + t * PK + k * 8, dv + (uint64_t)(k * 2048 >> 4),
-                                   id_o, j > 0 || k > 0);
+                            mma_ts(to, tmem + t * PK + k * 8, dv + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
+                        if (++u == NU) u = 0;
                     }
                     if (j + 1 == nt[t]) umma::commit(o_done + t);
-                    if (t == 1 || j >= nt[1]) release(v0, vc);
-                    if (j + 1 < nt[t]) {
-                        if (!k_in) {
-                            units_in(k1, kc);
-                            if (!ok) break;
-                            umma::fence_after();
-                            k_in = true;
-                        }
-                        scores(t, j + 1);
-                        if (t == 1 || j + 1 >= nt[1]) release(k1, kc);
+                    if (t == 1 || j >= nt[1]) release(uv, vc);
+                }
+                __syncwarp();
+                if (j + 1 < nt[t]) {
+                    if (!k_in) {
+                        take(kc);
+                        if (!ok) break;
+                        umma::fence_after();
+                        k_in = true;
                     }
+                    if (elect_one()) {
+                        scores(t, uk);
+                        if (t == 1 || j + 1 >= nt[1]) release(uk, kc);
+                    }
+                    __syncwarp();
                 }
             }
         }
-        if (__syncthreads_or(!ok) && lane == 0) {
-            umma::commit(drain);
+        if (__syncthreads_or(!ok)) {
+            if (elect_one()) umma::commit(drain);
             mbar_wait(drain, 0, 10000000ull);
         }
     } else if (warp == 10) {
