@@ -11,12 +11,13 @@
 // same time and all but one of them from L2.  A sequence that a group holds whole is written at once; one that is cut
 // leaves normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
-// A tile, by one CTA of 6 warps (one CTA per SM, ring of tiles in shared memory):
+// A tile, by one CTA of 8 warps (one CTA per SM, ring of tiles in shared memory):
 //   warp 4   TMA: one box per page (or 64 rows) and 64 channels, into K-major 128-byte-swizzled rows
 //   warp 5   S = Q X^T  (M 64 rows, N 64 tokens, k = channel) and O^T += C^T P^T  (M 128 channels, N = NR rows,
 //            k = token; C^T is the same shared memory read MN-major).  O^T is transposed because M must
 //            be 64 or 128 where the rows are few, and the channels are always a multiple of 128: no lane of the
 //            accumulator is idle, and rank 512 x 64 rows takes 256 of the 512 tensor-memory columns.
+//   warps 6, 7  the queries of the next sequence, as soon as the last S of this one is done
 //   warps 0-3  softmax of S (a quad of threads per row), P to shared memory, and at the end O^T out.
 // S of a tile is issued before P V of the one before, so the softmax overlaps the products.
 // The running maximum is raised only by more than 2^8 (kRaise); then O^T, one column a row, is rescaled in place.
@@ -30,7 +31,7 @@ namespace kda {
 namespace latent {
 
 constexpr int TILE = 64;             // tokens per tile
-constexpr int NT = 192;              // threads of the main kernel
+constexpr int NT = 256;              // threads of the main kernel
 constexpr int SW = 4;                // softmax warps
 constexpr uint32_t CHUNK = TILE * 128;  // bytes of a tile's 64 channels
 constexpr int MAX_STAGES = 8;
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(NT, 1)
     uint64_t *s_full = empty + MAX_STAGES;  // [2]
     uint64_t *p_ready = s_full + 2;
     uint64_t *q_ready = p_ready + 1;
-    uint64_t *drain = q_ready + 1;
+    uint64_t *q_free = q_ready + 1;
+    uint64_t *drain = q_free + 1;
     int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [8]
     int64_t *start = scan + 8;                                   // total, first sequence, first tile in it
     float *fs = reinterpret_cast<float *>(start + 4);            // [2][64] factors of the rows
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(s_full, 1);
         mbar_init(s_full + 1, 1);
         mbar_init(p_ready, SW);
-        mbar_init(q_ready, SW);
+        mbar_init(q_ready, 2);
+        mbar_init(q_free, 1);
         mbar_init(drain, 1);
         fence_mbar_init();
     }
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(NT, 1)
             ok = warp_wait(q_ready, pieces++ & 1u);
             if (!ok) return false;
             umma::fence_after();
-            auto issue_s = [&](int buf, int stage) {
+            auto issue_s = [&](int buf, int stage, bool last) {
                 if (!elect_one()) return;
                 const uint32_t ts = tmem + T_S + buf * TILE;
                 uint64_t dq = dq0, dx = dx0 + (uint64_t)(stage * stage_words);
@@ -267,8 +270,14 @@ __global__ void __launch_bounds__(NT, 1)
                     dq += NR * 128 >> 4;
                     dx += CHUNK >> 4;
                 }
-                for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, true);
+                if (kr == 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, true);
+                } else {
+                    for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, true);
+                }
                 umma::commit(s_full + buf);
+                if (last) umma::commit(q_free);  // this sequence's queries are read
             };
             bool issued = false;  // S of tile `it`
             for (int j = 0; j < nt; ++j, ++it) {
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(NT, 1)
                     ok = warp_wait(full + st, ph);
                     if (!ok) return false;
                     umma::fence_after();
-                    issue_s(it & 1, st);
+                    issue_s(it & 1, st, j + 1 == nt);
                 }
                 const int st1 = st + 1 == nst ? 0 : st + 1;
                 const uint32_t ph1 = st1 ? ph : ph ^ 1u;
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(NT, 1)
                 for (uint32_t spin = 1; !__all_sync(0xffffffffu, mbar_try_wait(p_ready, it & 1u)); ++spin) {
                     if (!issued && j + 1 < nt && __all_sync(0xffffffffu, mbar_try_wait(full + st1, ph1))) {
                         umma::fence_after();
-                        issue_s((it + 1) & 1, st1);
+                        issue_s((it + 1) & 1, st1, j + 2 == nt);
                         issued = true;
                     }
                     if ((spin & 255u) == 0) {
@@ -321,6 +330,38 @@ __global__ void __launch_bounds__(NT, 1)
             if (elect_one()) umma::commit(drain);
             mbar_wait(drain, 0, 10000000ull);
         }
+    } else if (warp >= 6) {
+        // ================================ queries ================================
+        const int nw = d / 8;  // 16-byte words of a row, at most 72
+        uint32_t pieces = 0;
+        walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &s, int32_t, int32_t, int64_t) {
+            if (pieces > 0) {
+                ok = warp_wait(q_free, (pieces - 1) & 1u);
+                if (!ok) return false;
+            }
+            ++pieces;
+            const int rows = min(NR, s.nq * H - rt * NR);
+            for (int i = warp - 6; i < NR; i += 2) {
+                const int r = rt * NR + i, t = r / H, h = r - t * H;
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const int w = lane + 32 * k;
+                    if (w >= nw) continue;
+                    uint8_t *dst = Q + (w >> 3) * (NR * 128) + i * 128 + (((w ^ i) & 7) << 4);
+                    if (i < rows)
+                        cp_async16(dst, src + w);
+                    else
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            cp_async_wait();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
+            return true;
+        });
+        __syncthreads_or(!ok);
     } else {
         // ================================ softmax ================================
         // These warps meet at named barriers, so they take every decision alike: one thread reads each sequence
@@ -333,7 +374,8 @@ __global__ void __launch_bounds__(NT, 1)
         };
         auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity)); };
         const uint32_t quad = tmem + ((uint32_t)(32 * warp) << 16);
-        const float scale2 = a.scale * kLog2e;
+        const float c = a.scale * kLog2e, raise = kRaise / c;
+        const int nw = d / 8;
         const int i0 = 16 * warp + (lane >> 2);  // this thread's rows of the row tile: i0 and i0 + 8
         int it = 0;
         int st_prev = 0;          // stage and parity of the empty barrier of tile it - 1
@@ -344,20 +386,6 @@ __global__ void __launch_bounds__(NT, 1)
             const int rows = min(NR, s.nq * H - rt * NR);
             const bool act = 16 * warp < rows;
             const int64_t orow = s.c0 * H + rt * NR;  // output row of the row tile's first row
-            // ---- the queries, K-major; every product that read the last piece's is done ----
-            const int nw = d / 8;
-            for (int u = tid; u < NR * nw; u += SW * 32) {
-                const int i = u / nw, w = u - i * nw, r = rt * NR + i;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (i < rows) {
-                    const int t = r / H, h = r - t * H;
-                    v = __ldg(reinterpret_cast<const uint4 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs) + w);
-                }
-                *reinterpret_cast<uint4 *>(Q + (w >> 3) * (NR * 128) + i * 128 + (((w ^ i) & 7) << 4)) = v;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
             if (rt == 0 && tid == 0 && off == 0) {
                 const int64_t last = (at + s.tiles - 1) / per;
                 Meta m;
@@ -418,22 +446,31 @@ __global__ void __launch_bounds__(NT, 1)
                 if (act) {
                     ld16x64_issue(quad + T_S + (it & 1) * TILE, sr);
                     umma::wait_ld(sr);
-                    float mx[2] = {-INFINITY, -INFINITY};
+                    if (tail) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int k = (e >> 1) & 1;
-                        float x = __uint_as_float(sr[e]) * scale2;
-                        if (tail) {
+                        for (int e = 0; e < 32; ++e) {
                             const int col = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), dr = key0 + col - base;
                             if (dr >= 0) {
-                                if (dr >= 64 || !(see[k] >> dr & 1))
-                                    x = -INFINITY;
+                                if (dr >= 64 || !(see[(e >> 1) & 1] >> dr & 1))
+                                    sr[e] = 0xff800000u;  // -inf
                                 else if (scan_drafts && poison[col])
-                                    x = NAN;
+                                    sr[e] = 0x7fffffffu;  // NaN
                             }
                         }
-                        sr[e] = __float_as_uint(x);
-                        mx[k] = fmaxf(mx[k], x);
+                    }
+                    float mx[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float y[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            y[u] = fmaxf(__uint_as_float(sr[16 * u + 2 * k]), __uint_as_float(sr[16 * u + 2 * k + 1]));
+#pragma unroll
+                            for (int n = 1; n < 4; ++n)
+                                y[u] = fmaxf(y[u], fmaxf(__uint_as_float(sr[16 * u + 4 * n + 2 * k]),
+                                                         __uint_as_float(sr[16 * u + 4 * n + 2 * k + 1])));
+                        }
+                        mx[k] = fmaxf(y[0], y[1]);
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -442,8 +479,8 @@ __global__ void __launch_bounds__(NT, 1)
                         float f = 1.f;
                         if (j == 0) {
                             m[k] = mx[k];
-                        } else if (mx[k] > m[k] + kRaise) {
-                            f = exp2_(m[k] - mx[k]);  // 0 from -inf
+                        } else if (mx[k] > m[k] + raise) {
+                            f = exp2_((m[k] - mx[k]) * c);  // 0 from -inf
                             m[k] = mx[k];
                             l[k] *= f;
                             raised = true;
@@ -472,17 +509,25 @@ __global__ void __launch_bounds__(NT, 1)
                 if (act) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float mm = m[k] == -INFINITY ? 0.f : m[k];
+                        const float mc = m[k] == -INFINITY ? 0.f : m[k] * c;
+                        const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
                         const int i = i0 + 8 * k;
-                        uint8_t *prow = P + i * 128;
+                        uint8_t *prow = P + i * 128 + 4 * (lane & 3);
+                        uint64_t sum = 0;
 #pragma unroll
                         for (int n = 0; n < 8; ++n) {
-                            const float p0 = exp2_(__uint_as_float(sr[4 * n + 2 * k]) - mm);
-                            const float p1 = exp2_(__uint_as_float(sr[4 * n + 2 * k + 1]) - mm);
-                            l[k] += p0 + p1;
-                            *reinterpret_cast<uint32_t *>(prow + (((n ^ i) & 7) << 4) + 4 * (lane & 3)) =
-                                pack2<FP16>(p0, p1);
+                            float p0, p1;
+                            unpair(fma2(pair(__uint_as_float(sr[4 * n + 2 * k]), __uint_as_float(sr[4 * n + 2 * k + 1])), c2,
+                                        mc2),
+                                   p0, p1);
+                            p0 = exp2_(p0);
+                            p1 = exp2_(p1);
+                            sum = add2(sum, pair(p0, p1));
+                            *reinterpret_cast<uint32_t *>(prow + (((n ^ i) & 7) << 4)) = pack2<FP16>(p0, p1);
                         }
+                        float s0, s1;
+                        unpair(sum, s0, s1);
+                        l[k] += s0 + s1;
                     }
                 }
                 fence_proxy_async_smem();
@@ -504,7 +549,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int i = i0 + 8 * k;
                     if ((lane & 3) == 0) {
                         inv[i] = l[k] == 0.f ? 0.f : 1.f / l[k];
-                        const float l2 = l[k] == 0.f ? -INFINITY : m[k] + __log2f(l[k]);
+                        const float l2 = l[k] == 0.f ? -INFINITY : m[k] * c + __log2f(l[k]);
                         if (!whole)
                             p.part_l[slot * NR + i] = l2;
                         else if (a.lse && i < rows)
@@ -515,25 +560,24 @@ __global__ void __launch_bounds__(NT, 1)
             softmax_sync();
             wait(empty + st_prev, ph_prev);
             umma::fence_after();
-            for (int mb = 0; mb < rank / 128; ++mb) {
-                const int ch = mb * 128 + 32 * warp + lane;  // this thread's channel
-                for (int c = 0; c < rows; c += 16) {
-                    uint32_t o[16];
-                    umma::ld16_issue(quad + mb * NR + c, o);
-                    umma::wait_ld16(o);
+            // a lane is a channel: 32 neighbouring ones make 64 (or, in fp32, 128) bytes of a row
+            auto store = [&](auto *dst, auto cvt) {
+                dst += 32 * warp + lane;
+                for (int mb = 0; mb < rank / 128; ++mb)
+                    for (int i0 = 0; i0 < rows; i0 += 16) {
+                        uint32_t o[16];
+                        umma::ld16_issue(quad + mb * NR + i0, o);
+                        umma::wait_ld16(o);
+                        auto *q = dst + (int64_t)i0 * rank + mb * 128;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int i = c + e;
-                        if (i < rows) {
-                            const float v = __uint_as_float(o[e]) * inv[i];
-                            if (whole)
-                                a.out[(orow + i) * rank + ch] = to_elem<FP16>(v);
-                            else
-                                p.part[(slot * NR + i) * rank + ch] = v;
-                        }
+                        for (int e = 0; e < 16; ++e, q += rank)
+                            if (i0 + e < rows) *q = cvt(__uint_as_float(o[e]) * inv[i0 + e]);
                     }
-                }
-            }
+            };
+            if (whole)
+                store(a.out + orow * rank, [](float v) { return to_elem<FP16>(v); });
+            else
+                store(p.part + slot * NR * rank, [](float v) { return v; });
             umma::fence_before();
             return true;
         });

@@ -71,15 +71,15 @@ __global__ void __launch_bounds__(PNT, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Q = sm;                                  // [2][kc] units
     uint8_t *R = Q + (uint32_t)(2 * kc) * UNIT;       // the ring
-    uint64_t *full = reinterpret_cast<uint64_t *>(R + (uint32_t)NU * UNIT);
-    uint64_t *empty = full + MAX_UNITS;
-    uint64_t *q_full = empty + MAX_UNITS;
-    uint64_t *s_full = q_full + 1;   // [2] scores of a query tile
-    uint64_t *p_ready = s_full + 2;  // [2] its weights
-    uint64_t *o_done = p_ready + 2;  // [2] its output
-    uint64_t *fixed = o_done + 2;    // [4] value tiles looked over by warp 10
-    uint64_t *v_raw = fixed + 4;     // [4] such tiles as they were loaded (at most 3 fit the ring)
-    uint64_t *drain = v_raw + 4;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(R + (uint32_t)NU * UNIT);
+    uint64_t *k_full = bars, *k_empty = bars + 4;    // [4] key tiles, by tile number (fewer than 4 fit the ring)
+    uint64_t *v_full = bars + 8, *v_empty = bars + 12;  // [4] value tiles
+    uint64_t *v_raw = bars + 16, *fixed = bars + 20;  // [4] value tiles for warp 10: as loaded, and looked over
+    uint64_t *s_full = bars + 24;   // [2] scores of a query tile
+    uint64_t *p_ready = bars + 26;  // [2] its weights
+    uint64_t *o_done = bars + 28;   // [2] its output
+    uint64_t *q_full = bars + 30;
+    uint64_t *drain = bars + 31;
     uint32_t *any = reinterpret_cast<uint32_t *>(drain + 1);  // [4] whether a value tile has marks
     uint32_t *tmem_s = any + 4;
     uint8_t *mark = reinterpret_cast<uint8_t *>(tmem_s + 1);  // [4][PK]
@@ -87,21 +87,7 @@ __global__ void __launch_bounds__(PNT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 9) umma::alloc(tmem_s, 512);
     if (tid == 0) {
-        for (int u = 0; u < MAX_UNITS; ++u) {
-            mbar_init(full + u, 1);
-            mbar_init(empty + u, 1);
-        }
-        mbar_init(q_full, 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full + t, 1);
-            mbar_init(p_ready + t, 4);
-            mbar_init(o_done + t, 1);
-        }
-        for (int t = 0; t < 4; ++t) {
-            mbar_init(fixed + t, 1);
-            mbar_init(v_raw + t, 1);
-        }
-        mbar_init(drain, 1);
+        for (int i = 0; i < 32; ++i) mbar_init(bars + i, i == 26 || i == 27 ? 4 : 1);  // p_ready: four warps
         fence_mbar_init();
     }
     umma::fence_before();
@@ -115,101 +101,100 @@ __global__ void __launch_bounds__(PNT, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 8) {
         // ================================ producer ================================
-        int idx = 0;
+        int j = 0;
         if (lane == 0 && ntile > 0) {
             mbar_arrive_expect_tx(q_full, (uint32_t)(2 * kc) * UNIT);
             for (int t = 0; t < 2; ++t)
                 for (int c = 0; c < kc; ++c)
                     tma_load_3d(Q + (uint32_t)(t * kc + c) * UNIT, &mq, c * 64, h, (int)q_lo + qt + t * PQ, q_full);
-            int u = 0;
-            uint32_t ph = 1;
-            for (int j = 0; j < ntile && ok; ++j) {
-                const int row = (int)k_lo + j * PK;
-                for (int c = 0; c < per; ++c, ++idx) {
-                    ok = idx < NU || mbar_wait(empty + u, ph);
-                    if (!ok) break;
-                    uint8_t *dst = R + (uint32_t)u * UNIT;
-                    if (c >= kc && j >= jf) {  // values that warp 10 looks over first: it has their barrier
-                        uint64_t *bar = v_raw + ((j - jf) & 3);
-                        if (c == kc) mbar_arrive_expect_tx(bar, (uint32_t)vc * UNIT);
-                        tma_load_3d(dst, &mv, (c - kc) * 64, h, row, bar);
-                        mbar_arrive(full + u);
-                        if (++u == NU) u = 0, ph ^= 1;
-                        continue;
-                    }
-                    mbar_arrive_expect_tx(full + u, UNIT);
-                    if (c < kc - 1)
-                        tma_load_3d(dst, &mk, c * 64, h, row, full + u);
-                    else if (c < kc)
-                        tma_load_3d(dst, &mr, 0, 0, row, full + u);
-                    else
-                        tma_load_3d(dst, &mv, (c - kc) * 64, h, row, full + u);
-                    if (++u == NU) u = 0, ph ^= 1;
+            int u = 0, used = 0;     // ring position, units in use up to the whole ring
+            int old = 0, oldc = 0;   // tile and part of the unit that was there before
+            auto next = [&]() {      // waits until the unit at u is free and returns it
+                if (used < NU) {
+                    ++used;
+                } else {
+                    ok = ok && mbar_wait((oldc < kc ? k_empty : v_empty) + (old & 3), (uint32_t)(old >> 2) & 1u);
+                    if (++oldc == per) oldc = 0, ++old;
                 }
+                const int r = u;
+                if (++u == NU) u = 0;
+                return r;
+            };
+            for (; j < ntile; ++j) {
+                const int row = (int)k_lo + j * PK;
+                uint64_t *kb = k_full + (j & 3), *vb = j < jf ? v_full + (j & 3) : v_raw + ((j - jf) & 3);
+                for (int c = 0; c < kc; ++c) {
+                    uint8_t *dst = R + (uint32_t)next() * UNIT;
+                    if (!ok) break;
+                    if (c == 0) mbar_arrive_expect_tx(kb, (uint32_t)kc * UNIT);
+                    if (c < kc - 1)
+                        tma_load_3d(dst, &mk, c * 64, h, row, kb);
+                    else
+                        tma_load_3d(dst, &mr, 0, 0, row, kb);
+                }
+                if (!ok) break;
+                const int u0 = next(), u1 = vc == 2 ? next() : u0;
+                if (!ok) break;
+                mbar_arrive_expect_tx(vb, (uint32_t)vc * UNIT);
+                tma_load_3d(R + (uint32_t)min(u0, u1) * UNIT, &mv, 0, h, row, vb);
+                if (vc == 2) tma_load_3d(R + (uint32_t)max(u0, u1) * UNIT, &mv, 64, h, row, vb);
             }
         }
         if (__syncthreads_or(!ok) && lane == 0 && ntile > 0) {  // copies still in flight land before the CTA ends
             constexpr uint64_t kDrainNs = 10000000ull;
             mbar_wait(q_full, 0, kDrainNs);
-            for (int k = max(0, idx - NU); k < idx; ++k) {
-                mbar_wait(full + k % NU, (uint32_t)(k / NU) & 1u, kDrainNs);
-                const int f = k / per - jf;
-                if (f >= 0 && k % per >= kc) mbar_wait(v_raw + (f & 3), (uint32_t)(f >> 2) & 1u, kDrainNs);
+            for (int i = max(0, j - 3); i <= min(j, ntile - 1); ++i) {
+                mbar_wait(k_full + (i & 3), (uint32_t)(i >> 2) & 1u, kDrainNs);
+                if (i < jf)
+                    mbar_wait(v_full + (i & 3), (uint32_t)(i >> 2) & 1u, kDrainNs);
+                else
+                    mbar_wait(v_raw + ((i - jf) & 3), (uint32_t)((i - jf) >> 2) & 1u, kDrainNs);
             }
         }
     } else if (warp == 9) {
         // ================================ MMA issuer ================================
         const uint32_t id_s = umma::idesc(kFmt<FP16>, PQ, PK);
-        const uint32_t id_o = umma::idesc(kFmt<FP16>, PQ, 64) | kBMajorMN;
-        const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dr0 = umma::sdesc(smem_addr(R)),
-                       dv0 = sdesc_mn(smem_addr(R), UNIT);
+        const uint32_t id_o = umma::idesc(kFmt<FP16>, PQ, a.dv) | kBMajorMN;
+        const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dr0 = umma::sdesc(smem_addr(R));
         const int kr = a.rope / 16;
         constexpr uint32_t UW = UNIT >> 4;  // a unit in descriptor words
-        int cu = 0;                         // ring position and parity of the next unit to wait for
-        uint32_t cph = 0;
-        auto take = [&](int n) {            // waits for the next n units
-            for (int c = 0; c < n; ++c) {
-                ok = ok && warp_wait(full + cu, cph);
-                if (++cu == NU) cu = 0, cph ^= 1;
-            }
-        };
-        // the two lambdas below run in one thread
-        auto release = [&](int u, int n) {  // units u, u + 1, ... are free once the products so far are done
-            for (int c = 0; c < n; ++c) {
-                umma::commit(empty + u);
-                if (++u == NU) u = 0;
-            }
-        };
-        auto scores = [&](int t, int u) {  // S_t = Q_t [K | R]^T of the key tile at ring position u
+        int u = 0;                          // ring position of the key tile whose scores come next
+        auto after = [&](int v, int n) { return v + n < NU ? v + n : v + n - NU; };
+        auto scores = [&](int t, int v) {  // one thread: S_t = Q_t [K | R]^T of the key tile at ring position v
             const uint32_t ts = tmem + t * PK;
             uint64_t dq = dq0 + (uint64_t)(t * kc * UW);
             for (int c = 0; c < kc - 1; ++c) {
-                const uint64_t dk = dr0 + (uint64_t)(u * UW);
+                const uint64_t dk = dr0 + (uint64_t)(v * UW);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, c > 0 || k > 0);
                 dq += UW;
-                if (++u == NU) u = 0;
+                v = after(v, 1);
             }
-            const uint64_t dk = dr0 + (uint64_t)(u * UW);
-            for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, true);
+            const uint64_t dk = dr0 + (uint64_t)(v * UW);
+            if (kr == 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, true);
+            } else {
+                for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, true);
+            }
             umma::commit(s_full + t);
         };
         if (ntile > 0) {
-            ok = warp_wait(q_full, 0);
-            take(kc);
+            ok = warp_wait(q_full, 0) && warp_wait(k_full, 0);
             umma::fence_after();
             if (ok && elect_one()) {
                 for (int t = 0; t < 2; ++t)
                     if (nt[t] > 0) scores(t, 0);
-                release(0, kc);
+                umma::commit(k_empty);
             }
             __syncwarp();
         }
         for (int j = 0; j < ntile && ok; ++j) {
-            const int uv = cu;  // values of tile j, then keys of tile j + 1
-            take(vc);
-            if (j >= jf) ok = ok && warp_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
-            const int uk = cu;
+            const int v0 = after(u, kc), v1 = vc == 2 ? after(v0, 1) : v0;  // values of tile j
+            u = after(v0, vc);                                             // keys of tile j + 1
+            const uint64_t dv = sdesc_mn(smem_addr(R + (uint32_t)min(v0, v1) * UNIT), (uint32_t)abs(v1 - v0) * UNIT);
+            ok = j < jf ? warp_wait(v_full + (j & 3), (uint32_t)(j >> 2) & 1u)
+                        : warp_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
             bool k_in = false;
             for (int t = 0; t < 2 && ok; ++t) {
                 if (j >= nt[t]) continue;
@@ -217,29 +202,24 @@ __global__ void __launch_bounds__(PNT, 1)
                 if (!ok) break;
                 umma::fence_after();
                 if (elect_one()) {
-                    int u = uv;
-                    for (int c = 0; c < vc; ++c) {
-                        const uint64_t dv = dv0 + (uint64_t)(u * UW);
-                        const uint32_t to = tmem + T_O + t * 128 + c * 64;
+                    const uint32_t to = tmem + T_O + t * 128, tp = tmem + t * PK;
 #pragma unroll
-                        for (int k = 0; k < PK / 16; ++k)
-                            mma_ts(to, tmem + t * PK + k * 8, dv + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
-                        if (++u == NU) u = 0;
-                    }
+                    for (int k = 0; k < PK / 16; ++k)
+                        mma_ts(to, tp + k * 8, dv + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
                     if (j + 1 == nt[t]) umma::commit(o_done + t);
-                    if (t == 1 || j >= nt[1]) release(uv, vc);
+                    if (t == 1 || j >= nt[1]) umma::commit(v_empty + (j & 3));
                 }
                 __syncwarp();
                 if (j + 1 < nt[t]) {
                     if (!k_in) {
-                        take(kc);
+                        ok = warp_wait(k_full + ((j + 1) & 3), (uint32_t)((j + 1) >> 2) & 1u);
                         if (!ok) break;
                         umma::fence_after();
                         k_in = true;
                     }
                     if (elect_one()) {
-                        scores(t, uk);
-                        if (t == 1 || j + 1 >= nt[1]) release(uk, kc);
+                        scores(t, u);
+                        if (t == 1 || j + 1 >= nt[1]) umma::commit(k_empty + ((j + 1) & 3));
                     }
                     __syncwarp();
                 }
@@ -251,8 +231,9 @@ __global__ void __launch_bounds__(PNT, 1)
         }
     } else if (warp == 10) {
         // ================================ value rows that not every query sees ================================
-        for (int j = jf; j < ntile && ok; ++j) {
-            const int f = j - jf, v0 = j * per + kc, valid = min(PK, nk - j * PK);
+        int u = (int)(((int64_t)jf * per + kc) % NU);  // ring position of the tile
+        for (int j = jf; j < ntile && ok; ++j, u = (u + per) % NU) {
+            const int f = j - jf, valid = min(PK, nk - j * PK);
             ok = __all_sync(0xffffffffu, mbar_wait(v_raw + (f & 3), (uint32_t)(f >> 2) & 1u));
             if (!ok) break;
             uint8_t *mk4 = mark + (f & 3) * PK;
@@ -262,7 +243,7 @@ __global__ void __launch_bounds__(PNT, 1)
                 const int r = r0 + lane;
                 bool bad = false;
                 for (int c = 0; c < vc; ++c) {
-                    const uint8_t *row = R + (uint32_t)((v0 + c) % NU) * UNIT + r * 128;
+                    const uint8_t *row = R + (uint32_t)((u + c) % NU) * UNIT + r * 128;
 #pragma unroll
                     for (int w = 0; w < 8; ++w)
                         bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(row + (((w ^ lane) & 7) << 4)));
@@ -270,7 +251,7 @@ __global__ void __launch_bounds__(PNT, 1)
                 const bool mine = bad && r < valid;
                 if (bad || r >= valid)
                     for (int c = 0; c < vc; ++c) {
-                        uint8_t *row = R + (uint32_t)((v0 + c) % NU) * UNIT + r * 128;
+                        uint8_t *row = R + (uint32_t)((u + c) % NU) * UNIT + r * 128;
 #pragma unroll
                         for (int w = 0; w < 8; ++w)
                             *reinterpret_cast<uint4 *>(row + (((w ^ lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -328,9 +309,10 @@ __global__ void __launch_bounds__(PNT, 1)
             float mx[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                mx[g] = __uint_as_float(s[g][0]);
+                mx[g] = fmaxf(__uint_as_float(s[g][0]), __uint_as_float(s[g][1]));
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mx[g] = fmaxf(mx[g], __uint_as_float(s[g][e]));
+                for (int e = 2; e < 32; e += 2)
+                    mx[g] = fmaxf(mx[g], fmaxf(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])));
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             float f = 1.f;
@@ -354,20 +336,25 @@ __global__ void __launch_bounds__(PNT, 1)
                 umma::wait_st();
             }
             const float mc = m == -INFINITY ? 0.f : m * c;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float p0 = exp2_(fmaf(__uint_as_float(s[g][e]), c, -mc));
-                    const float p1 = exp2_(fmaf(__uint_as_float(s[g][e + 1]), c, -mc));
-                    sum[(e >> 1) & 3] += p0 + p1;
-                    w[e >> 1] = pack2<FP16>(p0, p1);
+                    float x0, x1;
+                    unpair(fma2(pair(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])), c2, mc2), x0, x1);
+                    x0 = exp2_(x0);
+                    x1 = exp2_(x1);
+                    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(x0, x1));
+                    w[e >> 1] = pack2<FP16>(x0, x1);
                 }
                 st16_issue(ts + 16 * g, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float l0, l1;
+            unpair(add2(sum[0], sum[1]), l0, l1);
+            l += l0 + l1;
             umma::wait_st();
             umma::fence_before();
             __syncwarp();
