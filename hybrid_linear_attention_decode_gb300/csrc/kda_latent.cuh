@@ -133,6 +133,18 @@ __device__ __forceinline__ void ld16x64_issue(uint32_t taddr, uint32_t *r) {
         : "r"(taddr));
 }
 
+// The store of the same shape.
+__device__ __forceinline__ void st16x64_issue(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%"
+        "19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 // Warp-wide, asynchronous: store r[16] into 32 lanes x 16 consecutive columns.
 __device__ __forceinline__ void st16_issue(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -148,6 +160,15 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
         : "memory");
 }
 
@@ -179,17 +200,29 @@ inline EncodeTiledFn encoder() {
     return f;
 }
 
-// A 16-bit tensor [d2][d1][d0] with strides (elements) s2, s1 and contiguous d0, boxes of 64 x b1 x b2 in the
-// 128-byte swizzle; what lies outside reads as zero.
+// A 16-bit tensor of rank n (outermost last) with strides[k] elements from one index of axis k + 1 to the next and
+// axis 0 contiguous, read in boxes in the 128-byte swizzle; what lies outside reads as zero.
+inline bool tensor_map(EncodeTiledFn enc, CUtensorMap *m, bool fp16, const void *base, int n, const int64_t *dims,
+                       const int64_t *strides, const int *box) {
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], one[5];
+    for (int k = 0; k < n; ++k) {
+        d[k] = (cuuint64_t)dims[k];
+        b[k] = (cuuint32_t)box[k];
+        one[k] = 1;
+        if (k) s[k - 1] = (cuuint64_t)strides[k - 1] * 2;
+    }
+    return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)n,
+               const_cast<void *>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [d2][d1][d0] in boxes of 64 x b1 x b2.
 inline bool map_3d(EncodeTiledFn enc, CUtensorMap *m, bool fp16, const void *base, int64_t d0, int64_t d1, int64_t d2,
                    int64_t s1, int64_t s2, int b1, int b2) {
-    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)b1, (cuuint32_t)b2};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
-               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const int64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
+    const int box[3] = {64, b1, b2};
+    return tensor_map(enc, m, fp16, base, 3, dims, strides, box);
 }
 
 }  // namespace latent

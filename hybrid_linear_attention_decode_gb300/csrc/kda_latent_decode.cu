@@ -13,14 +13,15 @@
 //
 // A tile, by one CTA of 8 warps (one CTA per SM, ring of tiles in shared memory):
 //   warp 4   TMA: one box per page (or 64 rows) and 64 channels, into K-major 128-byte-swizzled rows
-//   warp 5   S = Q X^T  (M 64 rows, N 64 tokens, k = channel) and O^T += C^T P^T  (M 128 channels, N = NR rows,
-//            k = token; C^T is the same shared memory read MN-major).  O^T is transposed because M must
-//            be 64 or 128 where the rows are few, and the channels are always a multiple of 128: no lane of the
-//            accumulator is idle, and rank 512 x 64 rows takes 256 of the 512 tensor-memory columns.
+//   warp 5   S = Q X^T (M 64 rows, N 64 tokens, k = channel) and O += P C (M 64 rows, N 256 or 128 channels,
+//            k = token; C is the same shared memory, read MN-major).  With M 64 an accumulator has half of the
+//            tensor-memory lanes: O, rank columns wide, takes lanes 0-15 of each warp's quarter and S lanes 16-31.
+//            (The transposed product O^T += C^T P^T would leave no row of M unused, but an MN-major A operand
+//            of M 128, N 32 took 187 cycles an instruction; as B it takes 128 for N 256.)
 //   warps 6, 7  the queries of the next sequence, as soon as the last S of this one is done
-//   warps 0-3  softmax of S (a quad of threads per row), P to shared memory, and at the end O^T out.
+//   warps 0-3  softmax of S (16 rows a warp, a quad of threads a row), P to shared memory, and at the end O out.
 // S of a tile is issued before P V of the one before, so the softmax overlaps the products.
-// The running maximum is raised only by more than 2^8 (kRaise); then O^T, one column a row, is rescaled in place.
+// The running maximum is raised only by more than 2^8 (kRaise); then its warp rescales the rows of O in place.
 // Weights P are rounded to the element type for the second product (its operands are 16-bit); their sum is
 // kept in fp32 from the unrounded weights.
 #include <algorithm>
@@ -82,15 +83,6 @@ __device__ __forceinline__ Seq seq_of(const LatentDecodeArgs &a, int b) {
 }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SW * 32) : "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-                 : "=r"(r)
-                 : "r"((uint32_t)x), "n"(SW * 32)
-                 : "memory");
-    return r != 0;
-}
-
 // The group's part of the list of tiles: `f(b, s, first tile, tiles, place in the list)` for each sequence in it;
 // `get(b)` reads the sequence.
 template <class G, class F>
@@ -107,15 +99,17 @@ __device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64
 
 template <int NR, bool FP16>
 __global__ void __launch_bounds__(NT, 1)
-    kda_latent_decode_kernel(const DecodeP p, const __grid_constant__ CUtensorMap map) {
+    kda_latent_decode_kernel(const DecodeP p, const __grid_constant__ CUtensorMap map_c,
+                             const __grid_constant__ CUtensorMap map_r) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const LatentDecodeArgs &a = p.a;
     const int nch = p.nch, nst = p.nst, rank = a.c.rank, d = rank + a.c.rope, H = a.H;
-    uint8_t *Q = sm;  // [nch][NR][128 bytes]; reads of rows NR..63 run on into KV and feed rows that nobody reads
-    uint8_t *KV = Q + (uint32_t)nch * NR * 128;  // [nst][nch][TILE][128 bytes]
-    uint8_t *P = KV + (uint32_t)nst * nch * CHUNK;  // [NR][128 bytes]
-    uint64_t *full = reinterpret_cast<uint64_t *>(P + NR * 128);
+    // Q and P have NR rows; the products' rows NR..63 are read from what lies behind them, and nobody reads the results
+    uint8_t *Q = sm;                            // [nch][NR][128 bytes]
+    uint8_t *P = Q + (uint32_t)nch * NR * 128;  // [NR][128 bytes]
+    uint8_t *KV = P + NR * 128;                 // [nst][nch][TILE][128 bytes]
+    uint64_t *full = reinterpret_cast<uint64_t *>(KV + (uint32_t)nst * nch * CHUNK);
     uint64_t *empty = full + MAX_STAGES;
     uint64_t *s_full = empty + MAX_STAGES;  // [2]
     uint64_t *p_ready = s_full + 2;
@@ -124,16 +118,14 @@ __global__ void __launch_bounds__(NT, 1)
     uint64_t *drain = q_free + 1;
     int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [8]
     int64_t *start = scan + 8;                                   // total, first sequence, first tile in it
-    float *fs = reinterpret_cast<float *>(start + 4);            // [2][64] factors of the rows
-    float *inv = fs + 128;                                       // [64]
-    uint32_t *poison = reinterpret_cast<uint32_t *>(inv + 64);   // [64] tile rows that are not finite
+    uint32_t *poison = reinterpret_cast<uint32_t *>(start + 4);  // [64] tile rows that are not finite
     Seq *seq_s = reinterpret_cast<Seq *>(poison + 64);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(seq_s + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % p.nrt, g = blockIdx.x / p.nrt;
-    constexpr uint32_t TCOLS = NR == 64 ? 512 : 256;
-    constexpr uint32_t T_S = NR * 4;  // O^T: rank/128 blocks of NR columns; then two S buffers of 64
+    constexpr uint32_t TCOLS = 512;
+    constexpr uint32_t T_S = 16u << 16;  // two S buffers of 64 columns, in the lanes that O leaves
 
     if (warp == 5) umma::alloc(tmem_s, TCOLS);
     if (tid == 0) {
@@ -207,7 +199,8 @@ __global__ void __launch_bounds__(NT, 1)
 
     if (warp == 4) {
         // ================================ producer ================================
-        const int ps = a.c.page_size, bps = min(ps, TILE), nb = TILE / bps, lb = 31 - __clz(nb);  // nb 1, 2 or 4
+        // a lane per box; a box that is a whole tile takes all latent chunks at once
+        const int ps = a.c.page_size, bps = min(ps, TILE), nb = TILE / bps;
         int it = 0, st = 0;
         uint32_t ph = 1;  // a fresh ring is empty
         walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int64_t) {
@@ -227,13 +220,15 @@ __global__ void __launch_bounds__(NT, 1)
                 if (!ok) return false;
                 if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)nch * CHUNK);
                 __syncwarp();
-                uint8_t *dst = KV + (uint32_t)(st * nch) * CHUNK;
-                for (int u0 = 0; u0 < nb * nch; u0 += 32) {
-                    const int u = u0 + lane, box = u & (nb - 1), c = u >> lb;
-                    const int pg = __shfl_sync(0xffffffffu, page, box);
-                    if (u < nb * nch)
-                        tma_load_3d(dst + c * CHUNK + box * bps * 128, &map, c * 64,
-                                    in_page, pg, full + st);
+                if (lane < nb) {
+                    uint8_t *dst = KV + (uint32_t)(st * nch) * CHUNK + lane * bps * 128;
+                    if (nb == 1) {  // all latent chunks in one box
+                        tma_load_4d(dst, &map_c, 0, in_page, 0, page, full + st);
+                    } else {
+                        for (int c = 0; c < rank / 64; ++c)
+                            tma_load_4d(dst + c * CHUNK, &map_c, 0, in_page, c, page, full + st);
+                    }
+                    if (a.c.rope) tma_load_3d(dst + rank / 64 * CHUNK, &map_r, 0, in_page, page, full + st);
                 }
                 if (++st == nst) st = 0, ph ^= 1;
             }
@@ -248,7 +243,8 @@ __global__ void __launch_bounds__(NT, 1)
     } else if (warp == 5) {
         // ================================ MMA issuer ================================
         const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
-        const uint32_t id_o = umma::idesc(kFmt<FP16>, 128, NR) | kAMajorMN;
+        const uint32_t id_o = umma::idesc(kFmt<FP16>, 64, min(rank, 256)) | kBMajorMN;
+        const uint32_t id_o2 = umma::idesc(kFmt<FP16>, 64, max(rank - 256, 128)) | kBMajorMN;  // the rest of rank > 256
         const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dp = umma::sdesc(smem_addr(P));
         const uint64_t dx0 = umma::sdesc(smem_addr(KV)), dc0 = sdesc_mn(smem_addr(KV), CHUNK);
         const int ncr = rank / 64, kr = a.c.rope / 16;  // full chunks; instructions of the rotary chunk
@@ -309,16 +305,17 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 umma::fence_after();
                 if (elect_one()) {
-                    uint64_t dc = dc0 + (uint64_t)(st * stage_words);
-                    uint32_t to = tmem;
-                    for (int m = 0; m < rank / 128; ++m) {
+                    const uint64_t dc = dc0 + (uint64_t)(st * stage_words);
+#pragma unroll
+                    for (int k = 0; k < TILE / 16; ++k)
+                        umma::mma_bf16(tmem, dp + 2 * k, dc + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
+                    if (rank > 256) {
 #pragma unroll
                         for (int k = 0; k < TILE / 16; ++k)
-                            umma::mma_bf16(to, dc + (uint64_t)(k * 2048 >> 4), dp + 2 * k, id_o, j > 0 || k > 0);
-                        dc += 2 * CHUNK >> 4;
-                        to += NR;
+                            umma::mma_bf16(tmem + 256, dp + 2 * k, dc + (uint64_t)((k * 2048 + 4 * CHUNK) >> 4), id_o2,
+                                           j > 0 || k > 0);
                     }
-                    umma::commit(empty + st);  // O^T holds this tile, and its stage is free
+                    umma::commit(empty + st);  // O holds this tile, and its stage is free
                 }
                 __syncwarp();
                 st = st1;
@@ -441,14 +438,15 @@ __global__ void __launch_bounds__(NT, 1)
                     fence_proxy_async_smem();
                     softmax_sync();
                 }
-                uint32_t sr[32];
+                uint32_t sr[32];  // 4n + i: row i0 + 8*(i/2), token 8n + 2*(lane%4) + i%2
                 bool raised = false;
+                float f[2] = {1.f, 1.f};
                 if (act) {
                     ld16x64_issue(quad + T_S + (it & 1) * TILE, sr);
                     umma::wait_ld(sr);
                     if (tail) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < TILE / 2; ++e) {
                             const int col = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), dr = key0 + col - base;
                             if (dr >= 0) {
                                 if (dr >= 64 || !(see[(e >> 1) & 1] >> dr & 1))
@@ -464,11 +462,12 @@ __global__ void __launch_bounds__(NT, 1)
                         float y[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            y[u] = fmaxf(__uint_as_float(sr[16 * u + 2 * k]), __uint_as_float(sr[16 * u + 2 * k + 1]));
+                            constexpr int HALF = TILE / 16;  // registers 4n + .. of half the columns
+                            y[u] = -INFINITY;
 #pragma unroll
-                            for (int n = 1; n < 4; ++n)
-                                y[u] = fmaxf(y[u], fmaxf(__uint_as_float(sr[16 * u + 4 * n + 2 * k]),
-                                                         __uint_as_float(sr[16 * u + 4 * n + 2 * k + 1])));
+                            for (int n = u * HALF; n < (u + 1) * HALF; ++n)
+                                y[u] = fmaxf(y[u], fmaxf(__uint_as_float(sr[4 * n + 2 * k]),
+                                                         __uint_as_float(sr[4 * n + 2 * k + 1])));
                         }
                         mx[k] = fmaxf(y[0], y[1]);
                     }
@@ -476,34 +475,29 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int k = 0; k < 2; ++k) {
                         mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
                         mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-                        float f = 1.f;
                         if (j == 0) {
                             m[k] = mx[k];
                         } else if (mx[k] > m[k] + raise) {
-                            f = exp2_((m[k] - mx[k]) * c);  // 0 from -inf
+                            f[k] = exp2_((m[k] - mx[k]) * c);  // 0 from -inf
                             m[k] = mx[k];
-                            l[k] *= f;
+                            l[k] *= f[k];
                             raised = true;
                         }
-                        if ((lane & 3) == 0) fs[(it & 1) * 64 + i0 + 8 * k] = f;
                     }
                 }
-                const bool rescale = j > 0 && softmax_any(raised);
-                if (it > 0) {  // O^T and P are this warp's again
+                if (it > 0) {  // O and P are this warp's again
                     wait(empty + st_prev, ph_prev);
                     umma::fence_after();
                 }
-                if (rescale) {
-                    const float *f = fs + (it & 1) * 64;
-                    for (int mb = 0; mb < rank / 128; ++mb)
-                        for (int c = 0; c < NR; c += 16) {
-                            uint32_t o[16];
-                            umma::ld16_issue(quad + mb * NR + c, o);
-                            umma::wait_ld16(o);
+                if (__any_sync(0xffffffffu, raised)) {
+                    for (int ch = 0; ch < rank; ch += 64) {
+                        uint32_t o[32];
+                        ld16x64_issue(quad + ch, o);
+                        umma::wait_ld(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[c + e]);
-                            st16_issue(quad + mb * NR + c, o);
-                        }
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(e >> 1) & 1]);
+                        st16x64_issue(quad + ch, o);
+                    }
                     umma::wait_st();
                 }
                 if (act) {
@@ -515,7 +509,7 @@ __global__ void __launch_bounds__(NT, 1)
                         uint8_t *prow = P + i * 128 + 4 * (lane & 3);
                         uint64_t sum = 0;
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) {
+                        for (int n = 0; n < TILE / 8; ++n) {
                             float p0, p1;
                             unpair(fma2(pair(__uint_as_float(sr[4 * n + 2 * k]), __uint_as_float(sr[4 * n + 2 * k + 1])), c2,
                                         mc2),
@@ -538,17 +532,20 @@ __global__ void __launch_bounds__(NT, 1)
                 ph_prev = ph;
                 if (++st == nst) st = 0, ph ^= 1;
             }
-            // ---- the piece is done: O^T / l out ----
+            // ---- the piece is done: O / l out ----
             const bool whole = off == 0 && nt == s.tiles;
             const int64_t slot = ((int64_t)g * 2 + (at != g0)) * p.nrt + rt;
+            wait(empty + st_prev, ph_prev);
+            umma::fence_after();
             if (act) {
+                float inv[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
                     const int i = i0 + 8 * k;
+                    inv[k] = l[k] == 0.f ? 0.f : 1.f / l[k];
                     if ((lane & 3) == 0) {
-                        inv[i] = l[k] == 0.f ? 0.f : 1.f / l[k];
                         const float l2 = l[k] == 0.f ? -INFINITY : m[k] * c + __log2f(l[k]);
                         if (!whole)
                             p.part_l[slot * NR + i] = l2;
@@ -556,28 +553,28 @@ __global__ void __launch_bounds__(NT, 1)
                             a.lse[orow + i] = l2 * kLn2;
                     }
                 }
-            }
-            softmax_sync();
-            wait(empty + st_prev, ph_prev);
-            umma::fence_after();
-            // a lane is a channel: 32 neighbouring ones make 64 (or, in fp32, 128) bytes of a row
-            auto store = [&](auto *dst, auto cvt) {
-                dst += 32 * warp + lane;
-                for (int mb = 0; mb < rank / 128; ++mb)
-                    for (int i0 = 0; i0 < rows; i0 += 16) {
-                        uint32_t o[16];
-                        umma::ld16_issue(quad + mb * NR + i0, o);
-                        umma::wait_ld16(o);
-                        auto *q = dst + (int64_t)i0 * rank + mb * 128;
+                uint16_t *out = a.out + (orow + i0) * rank + 2 * (lane & 3);
+                float *part = p.part + (slot * NR + i0) * rank + 2 * (lane & 3);
+                for (int ch = 0; ch < rank; ch += 64) {
+                    uint32_t o[32];
+                    ld16x64_issue(quad + ch, o);
+                    umma::wait_ld(o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e, q += rank)
-                            if (i0 + e < rows) *q = cvt(__uint_as_float(o[e]) * inv[i0 + e]);
+                    for (int k = 0; k < 2; ++k) {
+                        if (i0 + 8 * k >= rows) continue;
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            const float v0 = __uint_as_float(o[4 * n + 2 * k]) * inv[k];
+                            const float v1 = __uint_as_float(o[4 * n + 2 * k + 1]) * inv[k];
+                            const int at8 = 8 * k * rank + ch + 8 * n;
+                            if (whole)
+                                *reinterpret_cast<uint32_t *>(out + at8) = pack2<FP16>(v0, v1);
+                            else
+                                *reinterpret_cast<float2 *>(part + at8) = make_float2(v0, v1);
+                        }
                     }
-            };
-            if (whole)
-                store(a.out + orow * rank, [](float v) { return to_elem<FP16>(v); });
-            else
-                store(p.part + slot * NR * rank, [](float v) { return v; });
+                }
+            }
             umma::fence_before();
             return true;
         });
@@ -691,10 +688,13 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     }
     const EncodeTiledFn enc = encoder();
     if (!enc) return fail(KDA_ERR_CUDA, "latent decode: cuTensorMapEncodeTiled is not available");
-    CUtensorMap map;
-    const int d = a.c.rank + a.c.rope;
-    if (!map_3d(enc, &map, FP16, a.c.pages, d, a.c.page_size, a.c.num_pages, d, a.c.page_stride,
-                std::min(a.c.page_size, TILE), 1))
+    CUtensorMap map_c, map_r;
+    const int d = a.c.rank + a.c.rope, rows = std::min(a.c.page_size, TILE);
+    const int64_t dims[4] = {64, a.c.page_size, a.c.rank / 64, a.c.num_pages}, strides[3] = {d, 64, a.c.page_stride};
+    const int box[4] = {64, rows, rows == TILE ? a.c.rank / 64 : 1, 1};
+    if (!tensor_map(enc, &map_c, FP16, a.c.pages, 4, dims, strides, box) ||
+        (a.c.rope && !map_3d(enc, &map_r, FP16, a.c.pages + a.c.rank, a.c.rope, a.c.page_size, a.c.num_pages, d,
+                             a.c.page_stride, rows, 1)))
         return fail(KDA_ERR_CUDA, "latent decode: tensor map encoding failed");
     DecodeP p;
     p.a = a;
@@ -709,7 +709,7 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     const uint32_t fixed = 1024 + (uint32_t)p.nch * NR * 128 + NR * 128 + MISC;
     p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / (p.nch * CHUNK));
     const uint32_t smem = fixed + p.nst * p.nch * CHUNK;
-    kda_latent_decode_kernel<NR, FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map);
+    kda_latent_decode_kernel<NR, FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, a.c.rope ? map_r : map_c);
     const int rc = launch_result("kda_latent_decode_kernel launch");
     if (rc != KDA_OK) return rc;
     kda_latent_combine_kernel<NR, FP16><<<dim3(a.H * a.max_tokens, q.slots_meta), CW * 32, 0, st>>>(p);
