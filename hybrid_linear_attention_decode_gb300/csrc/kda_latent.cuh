@@ -80,15 +80,15 @@ constexpr int kFmt = FP16 ? 0 : umma::kBF16;
 constexpr uint32_t kAMajorMN = 1u << 15;
 constexpr uint32_t kBMajorMN = 1u << 16;
 
-// Descriptor of an MN-major 16-bit tile in the 128-byte swizzle: atoms of 64 elements (128 bytes) along M or N
-// by 8 k, `mn_stride` bytes from one atom to the next along M or N, 1024 bytes from one group of 8 k to the next.
-// Rows of tokens that are a K-major operand of one product (k = channel) are an MN-major operand of
-// another (k = token) as they lie.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t mn_stride) {
+// Descriptor of an operand in the 128-byte swizzle, whose atoms are 8 rows of 128 bytes.  K-major (rows = M or N, k
+// along the row): `sbo` bytes from one group of 8 rows to the next, lbo unused.  MN-major (rows = k, 64 elements of M or N
+// along the row): `lbo` bytes from one group of 64 of M or N to the next, `sbo` from one group of 8 k to the next.  So rows
+// of tokens are a K-major operand of one product (k = channel) and an MN-major one of another (k = token).
+__device__ __forceinline__ uint64_t sdesc_at(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-    d |= (uint64_t)((mn_stride >> 4) & 0x3FFF) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
@@ -108,6 +108,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
             d_tmem),
         "r"(a_tmem), "l"(b), "r"(id), "r"((uint32_t)acc));
+}
+
+// Whether the phase is complete, without the suspended wait of mbar_try_wait(): for a warp that watches two barriers.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 // mbar_wait() by a whole warp, with one answer for all lanes.

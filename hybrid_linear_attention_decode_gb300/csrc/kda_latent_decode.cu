@@ -7,18 +7,18 @@
 //
 // Split: the 64-token tiles of all sequences form one list, and each group of CTAs takes an equal, contiguous
 // part of it (found on the device from lens, so a captured launch follows its lengths).  A group has one CTA for
-// each NR rows (NR = 16, 32 or 64), side by side in the grid, so that they read the same tiles at the
-// same time and all but one of them from L2.  A sequence that a group holds whole is written at once; one that is cut
+// each 64 rows, side by side in the grid, so that they read the same tiles at the same time and all but one of
+// them from L2.  A sequence that a group holds whole is written at once; one that is cut
 // leaves normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
-// A tile, by one CTA of 8 warps (one CTA per SM, ring of tiles in shared memory):
-//   warp 4   TMA: one box per page (or 64 rows) and 64 channels, into K-major 128-byte-swizzled rows
+// A tile, by one CTA of 10 warps (one CTA per SM, ring of tiles in shared memory):
+//   warp 4   TMA: boxes of 8 tokens with all their channels, into K-major 128-byte-swizzled rows
 //   warp 5   S = Q X^T (M 64 rows, N 64 tokens, k = channel) and O += P C (M 64 rows, N 256 or 128 channels,
 //            k = token; C is the same shared memory, read MN-major).  With M 64 an accumulator has half of the
 //            tensor-memory lanes: O, rank columns wide, takes lanes 0-15 of each warp's quarter and S lanes 16-31.
 //            (The transposed product O^T += C^T P^T would leave no row of M unused, but an MN-major A operand
 //            of M 128, N 32 took 187 cycles an instruction; as B it takes 128 for N 256.)
-//   warps 6, 7  the queries of the next sequence, as soon as the last S of this one is done
+//   warps 6-9  the queries of the next sequence into tensor memory, as soon as the last S of this one is done
 //   warps 0-3  softmax of S (16 rows a warp, a quad of threads a row), P to shared memory, and at the end O out.
 // S of a tile is issued before P V of the one before, so the softmax overlaps the products.
 // The running maximum is raised only by more than 2^8 (kRaise); then its warp rescales the rows of O in place.
@@ -32,9 +32,11 @@ namespace kda {
 namespace latent {
 
 constexpr int TILE = 64;             // tokens per tile
-constexpr int NT = 256;              // threads of the main kernel
+constexpr int NR = 64;               // rows (query, head) per CTA
+constexpr int NT = 320;              // threads of the main kernel
 constexpr int SW = 4;                // softmax warps
-constexpr uint32_t CHUNK = TILE * 128;  // bytes of a tile's 64 channels
+constexpr int QW = 4;                // query warps, one for each quarter of the lanes
+constexpr uint32_t ATOM = 1024;      // bytes of 8 tokens x 64 channels
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t SMEM_MAX = 227 * 1024;
 constexpr uint32_t MISC = 1536;      // barriers and small arrays
@@ -46,7 +48,7 @@ struct Meta {
 
 struct DecodeP {
     LatentDecodeArgs a;
-    int32_t groups, nrt, nst, nch, by_seq;
+    int32_t groups, nrt, nst, nch, by_seq, split_rope;
     Meta *meta;    // [n] when by_seq, else [groups]
     float *part;   // [groups * 2][nrt][NR][rank] normalised parts
     float *part_l; // [groups * 2][nrt][NR] log2 of their sums
@@ -86,7 +88,7 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" 
 // The group's part of the list of tiles: `f(b, s, first tile, tiles, place in the list)` for each sequence in it;
 // `get(b)` reads the sequence.
 template <class G, class F>
-__device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64_t at, int64_t end, int rt, int NR, G get,
+__device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64_t at, int64_t end, int rt, G get,
                                      F f) {
     for (; at < end && b < p.a.n; ++b, off = 0) {
         const Seq s = get(b);
@@ -97,7 +99,7 @@ __device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64
     }
 }
 
-template <int NR, bool FP16>
+template <bool FP16>
 __global__ void __launch_bounds__(NT, 1)
     kda_latent_decode_kernel(const DecodeP p, const __grid_constant__ CUtensorMap map_c,
                              const __grid_constant__ CUtensorMap map_r) {
@@ -105,29 +107,28 @@ __global__ void __launch_bounds__(NT, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const LatentDecodeArgs &a = p.a;
     const int nch = p.nch, nst = p.nst, rank = a.c.rank, d = rank + a.c.rope, H = a.H;
-    // Q and P have NR rows; the products' rows NR..63 are read from what lies behind them, and nobody reads the results
-    uint8_t *Q = sm;                            // [nch][NR][128 bytes]
-    uint8_t *P = Q + (uint32_t)nch * NR * 128;  // [NR][128 bytes]
-    uint8_t *KV = P + NR * 128;                 // [nst][nch][TILE][128 bytes]
-    uint64_t *full = reinterpret_cast<uint64_t *>(KV + (uint32_t)nst * nch * CHUNK);
+    uint8_t *P = sm;             // [NR][128 bytes]
+    uint8_t *KV = P + NR * 128;  // [nst][TILE / 8][nch][8][128 bytes]: 8 tokens' rows, then the next 8
+    const uint32_t GROUP = (uint32_t)nch * ATOM, STAGE = TILE / 8 * GROUP;
+    uint64_t *full = reinterpret_cast<uint64_t *>(KV + (uint32_t)nst * STAGE);
     uint64_t *empty = full + MAX_STAGES;
     uint64_t *s_full = empty + MAX_STAGES;  // [2]
     uint64_t *p_ready = s_full + 2;
     uint64_t *q_ready = p_ready + 1;
     uint64_t *q_free = q_ready + 1;
     uint64_t *drain = q_free + 1;
-    int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [8]
-    int64_t *start = scan + 8;                                   // total, first sequence, first tile in it
+    int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [NT / 32]
+    int64_t *start = scan + NT / 32;                                   // total, first sequence, first tile in it
     uint32_t *poison = reinterpret_cast<uint32_t *>(start + 4);  // [64] tile rows that are not finite
     Seq *seq_s = reinterpret_cast<Seq *>(poison + 64);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(seq_s + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % p.nrt, g = blockIdx.x / p.nrt;
-    constexpr uint32_t TCOLS = 512;
-    constexpr uint32_t T_S = 16u << 16;  // two S buffers of 64 columns, in the lanes that O leaves
+    // tensor memory: Q (288 columns) and two S buffers of 64 in lanes 0-15 of each quarter, O in lanes 16-31
+    constexpr uint32_t T_S = 384, T_O = 16u << 16;
 
-    if (warp == 5) umma::alloc(tmem_s, TCOLS);
+    if (warp == 5) umma::alloc(tmem_s, 512);
     if (tid == 0) {
         start[1] = a.n;
         start[2] = 0;
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(s_full, 1);
         mbar_init(s_full + 1, 1);
         mbar_init(p_ready, SW);
-        mbar_init(q_ready, 2);
+        mbar_init(q_ready, QW);
         mbar_init(q_free, 1);
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -199,17 +200,17 @@ __global__ void __launch_bounds__(NT, 1)
 
     if (warp == 4) {
         // ================================ producer ================================
-        // a lane per box; a box that is a whole tile takes all latent chunks at once
-        const int ps = a.c.page_size, bps = min(ps, TILE), nb = TILE / bps;
+        // A box is 8 tokens with all their channels: 8 (rank + rope) 2 bytes in a row in the cache, whatever the page
+        // size.  (Boxes of 64 tokens x 64 channels, which read 128 bytes of each row at a time, reached 4.0 TB/s of DRAM.)
+        const int ps = a.c.page_size;
         int it = 0, st = 0;
         uint32_t ph = 1;  // a fresh ring is empty
-        walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int64_t) {
+        walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &s, int32_t off, int32_t nt, int64_t) {
             const int32_t *trow = a.t.table + (int64_t)s.row * a.t.max_pages;
             for (int j = 0; j < nt; ++j, ++it) {
-                const int key = (off + j) * TILE + lane * bps;  // below 2^31: len is
-                const int in_page = (off + j) * TILE % ps;      // of the tile's first box; 0 when a page is a box or less
-                int page = (int)a.c.num_pages;  // a box outside the tensor reads as zeros
-                if (lane < nb && key < s.len) {
+                const int key = (off + j) * TILE + (lane & 7) * 8;  // below 2^31: len is
+                int page = (int)a.c.num_pages;                      // a box outside the tensor reads as zeros
+                if (lane < 8 && key < s.len) {
                     const int e = __ldg(trow + key / ps);
                     if (e >= 0 && e < a.c.num_pages)
                         page = e;
@@ -218,17 +219,12 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 ok = it < nst || warp_wait(empty + st, ph);
                 if (!ok) return false;
-                if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)nch * CHUNK);
+                if (lane == 0) mbar_arrive_expect_tx(full + st, STAGE);
                 __syncwarp();
-                if (lane < nb) {
-                    uint8_t *dst = KV + (uint32_t)(st * nch) * CHUNK + lane * bps * 128;
-                    if (nb == 1) {  // all latent chunks in one box
-                        tma_load_4d(dst, &map_c, 0, in_page, 0, page, full + st);
-                    } else {
-                        for (int c = 0; c < rank / 64; ++c)
-                            tma_load_4d(dst + c * CHUNK, &map_c, 0, in_page, c, page, full + st);
-                    }
-                    if (a.c.rope) tma_load_3d(dst + rank / 64 * CHUNK, &map_r, 0, in_page, page, full + st);
+                if (lane < 8) {
+                    uint8_t *dst = KV + (uint32_t)st * STAGE + lane * GROUP;
+                    tma_load_4d(dst, &map_c, 0, key % ps, 0, page, full + st);
+                    if (p.split_rope) tma_load_3d(dst + rank / 64 * ATOM, &map_r, 0, key % ps, page, full + st);
                 }
                 if (++st == nst) st = 0, ph ^= 1;
             }
@@ -245,32 +241,33 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
         const uint32_t id_o = umma::idesc(kFmt<FP16>, 64, min(rank, 256)) | kBMajorMN;
         const uint32_t id_o2 = umma::idesc(kFmt<FP16>, 64, max(rank - 256, 128)) | kBMajorMN;  // the rest of rank > 256
-        const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dp = umma::sdesc(smem_addr(P));
-        const uint64_t dx0 = umma::sdesc(smem_addr(KV)), dc0 = sdesc_mn(smem_addr(KV), CHUNK);
+        const uint64_t dp = umma::sdesc(smem_addr(P));
+        const uint64_t dx0 = sdesc_at(smem_addr(KV), 0, GROUP), dc0 = sdesc_at(smem_addr(KV), ATOM, GROUP);
         const int ncr = rank / 64, kr = a.c.rope / 16;  // full chunks; instructions of the rotary chunk
-        const uint32_t stage_words = (uint32_t)nch * CHUNK >> 4;
+        const uint32_t stage_words = STAGE >> 4, k_words = 2 * GROUP >> 4;  // of a stage, of 16 tokens
         uint32_t pieces = 0;
         int it = 0, st = 0;  // tile whose P V comes next, and its stage
         uint32_t ph = 0;     // parity of the stage's full barrier
-        walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &, int32_t, int32_t nt, int64_t) {
+        walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &, int32_t, int32_t nt, int64_t) {
             ok = warp_wait(q_ready, pieces++ & 1u);
             if (!ok) return false;
             umma::fence_after();
             auto issue_s = [&](int buf, int stage, bool last) {
                 if (!elect_one()) return;
                 const uint32_t ts = tmem + T_S + buf * TILE;
-                uint64_t dq = dq0, dx = dx0 + (uint64_t)(stage * stage_words);
+                uint32_t tq = tmem;
+                uint64_t dx = dx0 + (uint64_t)(stage * stage_words);
                 for (int c = 0; c < ncr; ++c) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, k > 0 || c > 0);
-                    dq += NR * 128 >> 4;
-                    dx += CHUNK >> 4;
+                    for (int k = 0; k < 4; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, k > 0 || c > 0);
+                    tq += 32;
+                    dx += ATOM >> 4;
                 }
                 if (kr == 4) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, true);
+                    for (int k = 0; k < 4; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, true);
                 } else {
-                    for (int k = 0; k < kr; ++k) umma::mma_bf16(ts, dq + 2 * k, dx + 2 * k, id_s, true);
+                    for (int k = 0; k < kr; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, true);
                 }
                 umma::commit(s_full + buf);
                 if (last) umma::commit(q_free);  // this sequence's queries are read
@@ -288,8 +285,8 @@ __global__ void __launch_bounds__(NT, 1)
                 // whichever comes first: the weights of this tile, or the rows of the next
                 issued = false;
                 uint64_t t0 = 0;
-                for (uint32_t spin = 1; !__all_sync(0xffffffffu, mbar_try_wait(p_ready, it & 1u)); ++spin) {
-                    if (!issued && j + 1 < nt && __all_sync(0xffffffffu, mbar_try_wait(full + st1, ph1))) {
+                for (uint32_t spin = 1; !__all_sync(0xffffffffu, mbar_test(p_ready, it & 1u)); ++spin) {
+                    if (!issued && j + 1 < nt && __all_sync(0xffffffffu, mbar_test(full + st1, ph1))) {
                         umma::fence_after();
                         issue_s((it + 1) & 1, st1, j + 2 == nt);
                         issued = true;
@@ -308,11 +305,11 @@ __global__ void __launch_bounds__(NT, 1)
                     const uint64_t dc = dc0 + (uint64_t)(st * stage_words);
 #pragma unroll
                     for (int k = 0; k < TILE / 16; ++k)
-                        umma::mma_bf16(tmem, dp + 2 * k, dc + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
+                        umma::mma_bf16(tmem + T_O, dp + 2 * k, dc + (uint64_t)(k * k_words), id_o, j > 0 || k > 0);
                     if (rank > 256) {
 #pragma unroll
                         for (int k = 0; k < TILE / 16; ++k)
-                            umma::mma_bf16(tmem + 256, dp + 2 * k, dc + (uint64_t)((k * 2048 + 4 * CHUNK) >> 4), id_o2,
+                            umma::mma_bf16(tmem + T_O + 256, dp + 2 * k, dc + (uint64_t)(k * k_words + (4 * ATOM >> 4)), id_o2,
                                            j > 0 || k > 0);
                     }
                     umma::commit(empty + st);  // O holds this tile, and its stage is free
@@ -329,31 +326,41 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp >= 6) {
         // ================================ queries ================================
-        const int nw = d / 8;  // 16-byte words of a row, at most 72
+        const int w4 = warp & 3;                                 // quarter of the lanes
+        const uint32_t tq = tmem + ((uint32_t)(32 * w4) << 16);
+        const int i0 = 16 * w4 + (lane >> 2);                    // this thread's rows: i0 and i0 + 8
         uint32_t pieces = 0;
-        walk(p, b_start, off_start, g0, g1, rt, NR, read, [&](int, const Seq &s, int32_t, int32_t, int64_t) {
-            if (pieces > 0) {
-                ok = warp_wait(q_free, (pieces - 1) & 1u);
-                if (!ok) return false;
+        walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &s, int32_t, int32_t, int64_t) {
+            const int rows = min(NR, s.nq * H - rt * NR);
+            const uint2 *src[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = rt * NR + i0 + 8 * k, t = r / H, h = r - t * H;
+                src[k] = reinterpret_cast<const uint2 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs) + (lane & 3);
+            }
+            bool first = true;
+            for (int ch = 0; ch < d; ch += 128) {  // 64 columns: this thread's 8-byte words 4n + lane % 4 of the 128 channels
+                uint32_t v[32];
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint2 x = make_uint2(0, 0);
+                        if (i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
+                        v[4 * n + 2 * k] = x.x;
+                        v[4 * n + 2 * k + 1] = x.y;
+                    }
+                if (first && pieces > 0) {
+                    ok = warp_wait(q_free, (pieces - 1) & 1u);
+                    if (!ok) return false;
+                    umma::fence_after();
+                }
+                first = false;
+                st16x64_issue(tq + ch / 2, v);
             }
             ++pieces;
-            const int rows = min(NR, s.nq * H - rt * NR);
-            for (int i = warp - 6; i < NR; i += 2) {
-                const int r = rt * NR + i, t = r / H, h = r - t * H;
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const int w = lane + 32 * k;
-                    if (w >= nw) continue;
-                    uint8_t *dst = Q + (w >> 3) * (NR * 128) + i * 128 + (((w ^ i) & 7) << 4);
-                    if (i < rows)
-                        cp_async16(dst, src + w);
-                    else
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            cp_async_wait();
-            fence_proxy_async_smem();
+            umma::wait_st();
+            umma::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
             return true;
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(NT, 1)
         uint32_t ph_prev = 0;
         int st = 0;
         uint32_t ph = 0;
-        walk(p, b_start, off_start, g0, g1, rt, NR, read_once, [&](int b, const Seq &s, int32_t off, int32_t nt, int64_t at) {
+        walk(p, b_start, off_start, g0, g1, rt, read_once, [&](int b, const Seq &s, int32_t off, int32_t nt, int64_t at) {
             const int rows = min(NR, s.nq * H - rt * NR);
             const bool act = 16 * warp < rows;
             const int64_t orow = s.c0 * H + rt * NR;  // output row of the row tile's first row
@@ -416,22 +423,22 @@ __global__ void __launch_bounds__(NT, 1)
                     // rows behind the sequence become zeros (a zero weight times NaN is NaN); drafted rows that
                     // are not finite do too, and count as NaN scores for the queries that see them
                     wait(full + st, ph);
-                    uint8_t *x = KV + (uint32_t)(st * nch) * CHUNK;
+                    uint8_t *x = KV + (uint32_t)st * STAGE;
                     const int valid = min(TILE, s.len - key0);
                     for (int r = valid + warp; r < TILE; r += SW)
                         for (int w = lane; w < rank / 8; w += 32)
-                            *reinterpret_cast<uint4 *>(x + (w >> 3) * CHUNK + r * 128 + ((w & 7) << 4)) =
+                            *reinterpret_cast<uint4 *>(x + (r >> 3) * GROUP + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
                                 make_uint4(0, 0, 0, 0);
                     if (scan_drafts)
                         for (int r = max(0, base - key0) + warp; r < valid; r += SW) {
                             bool bad = false;
                             for (int w = lane; w < nw; w += 32)
                                 bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(
-                                    x + (w >> 3) * CHUNK + r * 128 + (((w ^ r) & 7) << 4)));
+                                    x + (r >> 3) * GROUP + (w >> 3) * ATOM + (r & 7) * 128 + (((w ^ r) & 7) << 4)));
                             bad = __any_sync(0xffffffffu, bad);
                             if (bad)
                                 for (int w = lane; w < rank / 8; w += 32)
-                                    *reinterpret_cast<uint4 *>(x + (w >> 3) * CHUNK + r * 128 + ((w & 7) << 4)) =
+                                    *reinterpret_cast<uint4 *>(x + (r >> 3) * GROUP + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
                                         make_uint4(0, 0, 0, 0);
                             if (lane == 0) poison[r] = bad;
                         }
@@ -492,11 +499,11 @@ __global__ void __launch_bounds__(NT, 1)
                 if (__any_sync(0xffffffffu, raised)) {
                     for (int ch = 0; ch < rank; ch += 64) {
                         uint32_t o[32];
-                        ld16x64_issue(quad + ch, o);
+                        ld16x64_issue(quad + T_O + ch, o);
                         umma::wait_ld(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(e >> 1) & 1]);
-                        st16x64_issue(quad + ch, o);
+                        st16x64_issue(quad + T_O + ch, o);
                     }
                     umma::wait_st();
                 }
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(NT, 1)
                 float *part = p.part + (slot * NR + i0) * rank + 2 * (lane & 3);
                 for (int ch = 0; ch < rank; ch += 64) {
                     uint32_t o[32];
-                    ld16x64_issue(quad + ch, o);
+                    ld16x64_issue(quad + T_O + ch, o);
                     umma::wait_ld(o);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -583,11 +590,11 @@ __global__ void __launch_bounds__(NT, 1)
     if (!ok && lane == 0) set_status(a.status, KDA_DEV_TIMEOUT);
     umma::fence_before();
     __syncthreads();
-    if (warp == 5) umma::dealloc(tmem, TCOLS);
+    if (warp == 5) umma::dealloc(tmem, 512);
 }
 
 // Joins the parts of cut sequences: one CTA per row and cut sequence; its warps take parts in turn.
-template <int NR, bool FP16>
+template <bool FP16>
 __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const DecodeP p) {
     __shared__ float acc_s[CW][512];
     __shared__ float ml[CW][2];
@@ -653,35 +660,31 @@ __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const Decod
     if (a.lse && threadIdx.x == 0) a.lse[orow] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
 }
 
-// Rows of a row tile: the fewest that hold all rows of a sequence, 64 where none does.
-static int rows_per_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
 struct Plan {
-    int NR, nrt, groups, slots_meta;
+    int nrt, groups, slots_meta;
     size_t off_part, off_l, bytes;
 };
 
 static Plan plan(int rank, int H, int n, int max_tokens) {
     Plan q;
     const int rows = H * max_tokens;
-    q.NR = rows_per_tile(rows);
-    q.nrt = (rows + q.NR - 1) / q.NR;
+    q.nrt = (rows + NR - 1) / NR;
     q.groups = std::max(1, current_device_sms() / q.nrt);
     q.slots_meta = std::min(n, q.groups);
-    const size_t parts = (size_t)q.groups * 2 * q.nrt * q.NR;
+    const size_t parts = (size_t)q.groups * 2 * q.nrt * NR;
     q.off_part = ((size_t)q.slots_meta * sizeof(Meta) + 255) / 256 * 256;
     q.off_l = q.off_part + parts * rank * 4;
     q.bytes = q.off_l + parts * 4;
     return q;
 }
 
-template <int NR, bool FP16>
+template <bool FP16>
 static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return launch_result("latent decode: cudaGetDevice");
     if (!(done.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(kda_latent_decode_kernel<NR, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(kda_latent_decode_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SMEM_MAX) != cudaSuccess)
             return launch_result("latent decode: cudaFuncSetAttribute");
         done.fetch_or(1ull << dev);
@@ -689,30 +692,32 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     const EncodeTiledFn enc = encoder();
     if (!enc) return fail(KDA_ERR_CUDA, "latent decode: cuTensorMapEncodeTiled is not available");
     CUtensorMap map_c, map_r;
-    const int d = a.c.rank + a.c.rope, rows = std::min(a.c.page_size, TILE);
-    const int64_t dims[4] = {64, a.c.page_size, a.c.rank / 64, a.c.num_pages}, strides[3] = {d, 64, a.c.page_stride};
-    const int box[4] = {64, rows, rows == TILE ? a.c.rank / 64 : 1, 1};
+    const int d = a.c.rank + a.c.rope, split = a.c.rope % 64 != 0;
+    const int nc = split ? a.c.rank / 64 : d / 64;  // 64-channel chunks that one box takes
+    const int64_t dims[4] = {64, a.c.page_size, nc, a.c.num_pages}, strides[3] = {d, 64, a.c.page_stride};
+    const int box[4] = {64, 8, nc, 1};
     if (!tensor_map(enc, &map_c, FP16, a.c.pages, 4, dims, strides, box) ||
-        (a.c.rope && !map_3d(enc, &map_r, FP16, a.c.pages + a.c.rank, a.c.rope, a.c.page_size, a.c.num_pages, d,
-                             a.c.page_stride, rows, 1)))
+        (split && !map_3d(enc, &map_r, FP16, a.c.pages + a.c.rank, a.c.rope, a.c.page_size, a.c.num_pages, d,
+                          a.c.page_stride, 8, 1)))
         return fail(KDA_ERR_CUDA, "latent decode: tensor map encoding failed");
     DecodeP p;
     p.a = a;
     p.groups = q.groups;
     p.nrt = q.nrt;
     p.nch = (d + 63) / 64;
+    p.split_rope = split;
     p.by_seq = a.n <= q.groups;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     p.meta = reinterpret_cast<Meta *>(ws);
     p.part = reinterpret_cast<float *>(ws + q.off_part);
     p.part_l = reinterpret_cast<float *>(ws + q.off_l);
-    const uint32_t fixed = 1024 + (uint32_t)p.nch * NR * 128 + NR * 128 + MISC;
-    p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / (p.nch * CHUNK));
-    const uint32_t smem = fixed + p.nst * p.nch * CHUNK;
-    kda_latent_decode_kernel<NR, FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, a.c.rope ? map_r : map_c);
+    const uint32_t fixed = 1024 + NR * 128 + MISC;
+    p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / (p.nch * ATOM * (TILE / 8)));
+    const uint32_t smem = fixed + p.nst * p.nch * ATOM * (TILE / 8);
+    kda_latent_decode_kernel<FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, split ? map_r : map_c);
     const int rc = launch_result("kda_latent_decode_kernel launch");
     if (rc != KDA_OK) return rc;
-    kda_latent_combine_kernel<NR, FP16><<<dim3(a.H * a.max_tokens, q.slots_meta), CW * 32, 0, st>>>(p);
+    kda_latent_combine_kernel<FP16><<<dim3(a.H * a.max_tokens, q.slots_meta), CW * 32, 0, st>>>(p);
     return launch_result("kda_latent_combine_kernel launch");
 }
 
@@ -725,13 +730,7 @@ size_t latent_decode_workspace_bytes(int rank, int H, int n, int max_tokens) {
 int launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st) {
     using namespace latent;
     const Plan q = plan(a.c.rank, a.H, a.n, a.max_tokens);
-    if (a.c.fp16)
-        return q.NR == 16   ? launch<16, true>(a, q, st)
-               : q.NR == 32 ? launch<32, true>(a, q, st)
-                            : launch<64, true>(a, q, st);
-    return q.NR == 16   ? launch<16, false>(a, q, st)
-           : q.NR == 32 ? launch<32, false>(a, q, st)
-                        : launch<64, false>(a, q, st);
+    return a.c.fp16 ? launch<true>(a, q, st) : launch<false>(a, q, st);
 }
 
 }  // namespace kda

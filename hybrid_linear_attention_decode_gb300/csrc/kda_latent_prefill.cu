@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(PNT, 1)
         for (int j = 0; j < ntile && ok; ++j) {
             const int v0 = after(u, kc), v1 = vc == 2 ? after(v0, 1) : v0;  // values of tile j
             u = after(v0, vc);                                             // keys of tile j + 1
-            const uint64_t dv = sdesc_mn(smem_addr(R + (uint32_t)min(v0, v1) * UNIT), (uint32_t)abs(v1 - v0) * UNIT);
+            const uint64_t dv =
+                sdesc_at(smem_addr(R + (uint32_t)min(v0, v1) * UNIT), (uint32_t)abs(v1 - v0) * UNIT, 1024);
             ok = j < jf ? warp_wait(v_full + (j & 3), (uint32_t)(j >> 2) & 1u)
                         : warp_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
             bool k_in = false;
