@@ -19,7 +19,7 @@
 //            (The transposed product O^T += C^T P^T would leave no row of M unused, but an MN-major A operand
 //            of M 128, N 32 took 187 cycles an instruction; as B it takes 128 for N 256.)
 //   warps 6-9  the queries of the next sequence into tensor memory, as soon as the last S of this one is done
-//   warps 0-3  softmax of S (16 rows a warp, a quad of threads a row), P to shared memory, and at the end O out.
+//   warps 0-3  softmax of S (8 or 16 rows a warp, a quad of threads a row), P to shared memory, and at the end O out.
 // S of a tile is issued before P V of the one before, so the softmax overlaps the products.
 // The running maximum is raised only by more than 2^8 (kRaise); then its warp rescales the rows of O in place.
 // Weights P are rounded to the element type for the second product (its operands are 16-bit); their sum is
@@ -33,7 +33,9 @@ namespace latent {
 
 constexpr int TILE = 64;             // tokens per tile
 constexpr int NR = 64;               // rows (query, head) per CTA
-constexpr int NT = 320;              // threads of the main kernel
+// Threads of the main kernel: 12 warps, the last two idle (registers come in warpgroups).  Launched with 168 registers a
+// thread (64,512 of 65,536); the softmax warpgroup takes 240, the others give down to 128: 63,488 in all.
+constexpr int NT = 384;
 constexpr int SW = 4;                // softmax warps
 constexpr int QW = 4;                // query warps, one for each quarter of the lanes
 constexpr uint32_t ATOM = 1024;      // bytes of 8 tokens x 64 channels
@@ -42,8 +44,9 @@ constexpr uint32_t SMEM_MAX = 227 * 1024;
 constexpr uint32_t MISC = 1536;      // barriers and small arrays
 constexpr int CW = 8;                // warps of a combine CTA
 
-struct Meta {
-    int32_t pieces, group, second, seq;  // parts of a cut sequence: first group, whether its part there is the second
+struct Meta {  // a cut sequence: its parts, the first group, whether its part there is the group's second, its output rows
+    int32_t pieces, group, second, rows;
+    int64_t row0;
 };
 
 struct DecodeP {
@@ -83,6 +86,9 @@ __device__ __forceinline__ Seq seq_of(const LatentDecodeArgs &a, int b) {
     s.tiles = s.nq > 0 ? (s.len + TILE - 1) / TILE : 0;
     return s;
 }
+
+// Rows of a row tile go to the four softmax warps by 8 where that holds them all, else by 16.
+__device__ __forceinline__ int rows_per_warp(int rows) { return rows <= 32 ? 8 : 16; }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SW * 32) : "memory"); }
 // The group's part of the list of tiles: `f(b, s, first tile, tiles, place in the list)` for each sequence in it;
@@ -198,6 +204,7 @@ __global__ void __launch_bounds__(NT, 1)
     bool ok = true;
     auto read = [&](int b) { return seq_of(a, b); };
 
+    if (warp >= SW) asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
     if (warp == 4) {
         // ================================ producer ================================
         // A box is 8 tokens with all their channels: 8 (rank + rope) 2 bytes in a row in the cache, whatever the page
@@ -324,14 +331,16 @@ __global__ void __launch_bounds__(NT, 1)
             if (elect_one()) umma::commit(drain);
             mbar_wait(drain, 0, 10000000ull);
         }
+    } else if (warp >= 10) {
+        __syncthreads_or(false);
     } else if (warp >= 6) {
         // ================================ queries ================================
         const int w4 = warp & 3;                                 // quarter of the lanes
         const uint32_t tq = tmem + ((uint32_t)(32 * w4) << 16);
-        const int i0 = 16 * w4 + (lane >> 2);                    // this thread's rows: i0 and i0 + 8
         uint32_t pieces = 0;
         walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &s, int32_t, int32_t, int64_t) {
             const int rows = min(NR, s.nq * H - rt * NR);
+            const int rw = rows_per_warp(rows), i0 = rw * w4 + (lane >> 2);  // this thread's rows: i0 and, if rw 16, i0 + 8
             const uint2 *src[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint2 x = make_uint2(0, 0);
-                        if (i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
+                        if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
                         v[4 * n + 2 * k] = x.x;
                         v[4 * n + 2 * k + 1] = x.y;
                     }
@@ -368,6 +377,7 @@ __global__ void __launch_bounds__(NT, 1)
         __syncthreads_or(!ok);
     } else {
         // ================================ softmax ================================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
         // These warps meet at named barriers, so they take every decision alike: one thread reads each sequence
         // for all, and a wait that gives up leads on through the same barriers (without further waits) to the end.
         auto read_once = [&](int b) {
@@ -380,7 +390,6 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t quad = tmem + ((uint32_t)(32 * warp) << 16);
         const float c = a.scale * kLog2e, raise = kRaise / c;
         const int nw = d / 8;
-        const int i0 = 16 * warp + (lane >> 2);  // this thread's rows of the row tile: i0 and i0 + 8
         int it = 0;
         int st_prev = 0;          // stage and parity of the empty barrier of tile it - 1
         uint32_t ph_prev = 0;
@@ -388,7 +397,10 @@ __global__ void __launch_bounds__(NT, 1)
         uint32_t ph = 0;
         walk(p, b_start, off_start, g0, g1, rt, read_once, [&](int b, const Seq &s, int32_t off, int32_t nt, int64_t at) {
             const int rows = min(NR, s.nq * H - rt * NR);
-            const bool act = 16 * warp < rows;
+            // this thread's rows of the row tile, i0 and (where a warp has 16) i0 + 8, are rows i0p, i0p + 8 of the products
+            const int rw = rows_per_warp(rows), i0 = rw * warp + (lane >> 2), i0p = 16 * warp + (lane >> 2);
+            const int nk = rw / 8;
+            const bool act = rw * warp < rows;
             const int64_t orow = s.c0 * H + rt * NR;  // output row of the row tile's first row
             if (rt == 0 && tid == 0 && off == 0) {
                 const int64_t last = (at + s.tiles - 1) / per;
@@ -396,7 +408,8 @@ __global__ void __launch_bounds__(NT, 1)
                 m.pieces = (int32_t)(last - g) + 1;
                 m.group = g;
                 m.second = at != g0;
-                m.seq = b;
+                m.rows = s.nq * H;
+                m.row0 = s.c0 * H;
                 if (p.by_seq)
                     p.meta[b] = m;
                 else if (m.pieces > 1)
@@ -466,6 +479,7 @@ __global__ void __launch_bounds__(NT, 1)
                     float mx[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
+                        if (k >= nk) break;
                         float y[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
@@ -480,6 +494,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
+                        if (k >= nk) break;
                         mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
                         mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
                         if (j == 0) {
@@ -510,9 +525,10 @@ __global__ void __launch_bounds__(NT, 1)
                 if (act) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
+                        if (k >= nk) break;
                         const float mc = m[k] == -INFINITY ? 0.f : m[k] * c;
                         const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
-                        const int i = i0 + 8 * k;
+                        const int i = i0p + 8 * k;
                         uint8_t *prow = P + i * 128 + 4 * (lane & 3);
                         uint64_t sum = 0;
 #pragma unroll
@@ -548,9 +564,11 @@ __global__ void __launch_bounds__(NT, 1)
                 float inv[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
+                    inv[k] = 0.f;
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
                     const int i = i0 + 8 * k;
+                    if (k >= nk) break;
                     inv[k] = l[k] == 0.f ? 0.f : 1.f / l[k];
                     if ((lane & 3) == 0) {
                         const float l2 = l[k] == 0.f ? -INFINITY : m[k] * c + __log2f(l[k]);
@@ -562,13 +580,10 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 uint16_t *out = a.out + (orow + i0) * rank + 2 * (lane & 3);
                 float *part = p.part + (slot * NR + i0) * rank + 2 * (lane & 3);
-                for (int ch = 0; ch < rank; ch += 64) {
-                    uint32_t o[32];
-                    ld16x64_issue(quad + T_O + ch, o);
-                    umma::wait_ld(o);
+                auto put = [&](const uint32_t *o, int ch) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        if (i0 + 8 * k >= rows) continue;
+                        if (k >= nk || i0 + 8 * k >= rows) break;
 #pragma unroll
                         for (int n = 0; n < 8; ++n) {
                             const float v0 = __uint_as_float(o[4 * n + 2 * k]) * inv[k];
@@ -580,6 +595,15 @@ __global__ void __launch_bounds__(NT, 1)
                                 *reinterpret_cast<float2 *>(part + at8) = make_float2(v0, v1);
                         }
                     }
+                };
+                for (int ch = 0; ch < rank; ch += 128) {  // two loads in flight
+                    uint32_t o0[32], o1[32];
+                    ld16x64_issue(quad + T_O + ch, o0);
+                    ld16x64_issue(quad + T_O + ch + 64, o1);
+                    umma::wait_ld(o0);
+                    umma::wait_ld(o1);
+                    put(o0, ch);
+                    put(o1, ch + 64);
                 }
             }
             umma::fence_before();
@@ -593,23 +617,21 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp == 5) umma::dealloc(tmem, 512);
 }
 
-// Joins the parts of cut sequences: one CTA per row and cut sequence; its warps take parts in turn.
-template <bool FP16>
+// Joins the parts of cut sequences.  WIDE: a CTA per row, its warps take parts in turn and meet in shared memory; for
+// sequences cut into more parts than a CTA has warps.  Otherwise a warp per row.
+template <bool FP16, bool WIDE>
 __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const DecodeP p) {
-    __shared__ float acc_s[CW][512];
-    __shared__ float ml[CW][2];
     const LatentDecodeArgs &a = p.a;
-    const Meta mt = p.meta[blockIdx.y];
-    if (mt.pieces < 2) return;
-    const Seq s = seq_of(a, mt.seq);
-    const int r = blockIdx.x, rt = r / NR, i = r - rt * NR;
-    if (r >= s.nq * a.H) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.c.rank, nv = rank / 128;
+    const int r = WIDE ? blockIdx.x : blockIdx.x * CW + warp, rt = r / NR, i = r - rt * NR;
+    const Meta mt = p.meta[blockIdx.y];
+    if (mt.pieces < 2 || r >= mt.rows) return;
     float m = -INFINITY, l = 0.f;
     float4 acc[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = warp; k < mt.pieces; k += CW) {
+#pragma unroll 2
+    for (int k = WIDE ? warp : 0; k < mt.pieces; k += WIDE ? CW : 1) {
         const int64_t slot = ((int64_t)(mt.group + k) * 2 + (k == 0 ? mt.second : 0)) * p.nrt + rt;
         const float lk = p.part_l[slot * NR + i];
         const float4 *o = reinterpret_cast<const float4 *>(p.part + (slot * NR + i) * rank);
@@ -630,34 +652,46 @@ __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const Decod
                 acc[v].w = acc[v].w * f + w * x[v].w;
             }
     }
+    const int64_t orow = mt.row0 + r;
+    if constexpr (WIDE) {
+        __shared__ float acc_s[CW][512];
+        __shared__ float ml[CW][2];
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-        if (v < nv) *reinterpret_cast<float4 *>(&acc_s[warp][(v * 32 + lane) * 4]) = acc[v];
-    if (lane == 0) {
-        ml[warp][0] = m;
-        ml[warp][1] = l;
-    }
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.f, f[CW];
+        for (int v = 0; v < 4; ++v)
+            if (v < nv) *reinterpret_cast<float4 *>(&acc_s[warp][(v * 32 + lane) * 4]) = acc[v];
+        if (lane == 0) {
+            ml[warp][0] = m;
+            ml[warp][1] = l;
+        }
+        __syncthreads();
+        float mm = -INFINITY, ll = 0.f, f[CW];
 #pragma unroll
-    for (int w = 0; w < CW; ++w) mm = fmaxf(mm, ml[w][0]);
-#pragma unroll
-    for (int w = 0; w < CW; ++w) {
-        f[w] = ml[w][0] == -INFINITY ? 0.f : exp2_(ml[w][0] - mm);
-        ll += f[w] * ml[w][1];
-    }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int64_t orow = s.c0 * a.H + r;
-    for (int ch = threadIdx.x * 2; ch < rank; ch += CW * 64) {
-        float o0 = 0.f, o1 = 0.f;
+        for (int w = 0; w < CW; ++w) mm = fmaxf(mm, ml[w][0]);
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
-            o0 += f[w] * acc_s[w][ch];
-            o1 += f[w] * acc_s[w][ch + 1];
+            f[w] = ml[w][0] == -INFINITY ? 0.f : exp2_(ml[w][0] - mm);
+            ll += f[w] * ml[w][1];
         }
-        *reinterpret_cast<uint32_t *>(a.out + orow * rank + ch) = pack2<FP16>(o0 * inv, o1 * inv);
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        for (int ch = threadIdx.x * 2; ch < rank; ch += CW * 64) {
+            float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < CW; ++w) {
+                o0 += f[w] * acc_s[w][ch];
+                o1 += f[w] * acc_s[w][ch + 1];
+            }
+            *reinterpret_cast<uint32_t *>(a.out + orow * rank + ch) = pack2<FP16>(o0 * inv, o1 * inv);
+        }
+        if (a.lse && threadIdx.x == 0) a.lse[orow] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
+    } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (v < nv)
+                *reinterpret_cast<uint2 *>(a.out + orow * rank + (v * 32 + lane) * 4) =
+                    make_uint2(pack2<FP16>(acc[v].x * inv, acc[v].y * inv), pack2<FP16>(acc[v].z * inv, acc[v].w * inv));
+        if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[orow] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
 }
 
 struct Plan {
@@ -717,7 +751,11 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     kda_latent_decode_kernel<FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, split ? map_r : map_c);
     const int rc = launch_result("kda_latent_decode_kernel launch");
     if (rc != KDA_OK) return rc;
-    kda_latent_combine_kernel<FP16><<<dim3(a.H * a.max_tokens, q.slots_meta), CW * 32, 0, st>>>(p);
+    const int rows = a.H * a.max_tokens;
+    if (q.groups > CW * a.n)  // a sequence is cut into about groups / n parts
+        kda_latent_combine_kernel<FP16, true><<<dim3(rows, q.slots_meta), CW * 32, 0, st>>>(p);
+    else
+        kda_latent_combine_kernel<FP16, false><<<dim3((rows + CW - 1) / CW, q.slots_meta), CW * 32, 0, st>>>(p);
     return launch_result("kda_latent_combine_kernel launch");
 }
 
