@@ -15,7 +15,6 @@ a paged cache (:class:`LatentCache`, :class:`PageTable`): ``kda_latent_append``,
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -379,53 +378,80 @@ def _need(ok, what: str) -> None:
         raise ValueError(what)
 
 
-def _on_device(fn):
-    """Runs a latent / page call on the CUDA device of its tensors (current or not), with that device's current
-    stream unless one is given; tensors on different devices, or on the CPU, raise ValueError."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        device = None
-        for x in list(args) + list(kw.values()):
-            for t in ((x.pages,) if isinstance(x, LatentCache) else (x.table, x.lens, x.refcount)
-                      if isinstance(x, PageTable) else (x,)):
-                if isinstance(t, torch.Tensor):
-                    _need(t.is_cuda, f"{fn.__name__}: tensors must be on a CUDA device")
-                    _need(device is None or t.device == device, f"{fn.__name__}: tensors are on different devices")
-                    device = t.device
-        if stream is not None:
-            _need(stream.device == device, f"{fn.__name__}: the stream belongs to another device")
-        with torch.cuda.device(device):
-            return fn(*args, stream=torch.cuda.current_stream() if stream is None else stream, **kw)
-    return call
+def _raise(what: str):
+    raise ValueError(what)
+
+
+def _device_of(name: str, tensors) -> int:
+    """The one CUDA device that the tensors (None among them skipped) live on."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    _raise(f"{name}: tensors must be on a CUDA device")
+                if dev is not None:
+                    _raise(f"{name}: tensors are on different devices")
+                dev = d
+    return dev
+
+
+def _launch(fn, name: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) on device `dev`, current or not, on its current stream unless one is given."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        _raise(f"{name}: the stream belongs to another device")
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != KDA_OK:
+        raise KdaError(rc, name, kda_last_error_string())
 
 
 def _int32(t, what: str, n: int | None = None):
-    """A contiguous int32 tensor of n elements (or None), as a pointer."""
+    """The address of a contiguous int32 tensor of n elements (None for None)."""
     if t is None:
         return None
-    _need(t.dtype == torch.int32 and t.dim() == 1 and (n is None or t.shape[0] == n),
-          f"{what} must be an int32 vector" + ("" if n is None else f" of {n} elements"))
-    return _ptr(t)
+    if t.dtype is not torch.int32 or t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
+        _raise(f"{what} must be a contiguous int32 vector" + ("" if n is None else f" of {n} elements"))
+    return t.data_ptr()
 
 
 def _rows_of(t, what: str, dtype, shape):
-    """A tensor of that type and shape whose last axis is contiguous: its pointer and its other strides."""
-    _need(isinstance(t, torch.Tensor), f"{what} must be a tensor")
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what} must be {dtype} of shape {tuple(shape)}")
-    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{what}: the last axis must be contiguous")
-    # the stride of an axis of one element is free in torch: give one that holds a row
-    st, least = [], int(t.shape[-1])
-    for k in range(t.dim() - 2, -1, -1):
-        st.append(least if t.shape[k] <= 1 else int(t.stride(k)))
-        least = max(least, st[-1] * int(t.shape[k]))
-    return (ctypes.c_void_p(t.data_ptr()), *reversed(st))
+    """A tensor of that type and shape whose last axis is contiguous: its address and its other strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        _raise(f"{what} must be a tensor of {dtype} and shape {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        _raise(f"{what}: the last axis must be contiguous")
+    if 0 in shape or 1 in shape:  # the stride of an axis of one element is free in torch: give one that holds a row
+        out, least = [], shape[-1]
+        for k in range(len(shape) - 2, -1, -1):
+            out.append(least if shape[k] <= 1 else st[k])
+            least = max(least, out[-1] * shape[k])
+        return (t.data_ptr(), *reversed(out))
+    return (t.data_ptr(), *st[:-1])
 
 
 def _out(t, what: str, dtype, shape):
     if t is None:
         return None
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what} must be {dtype} of shape {tuple(shape)}")
-    return _ptr(t)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _raise(f"{what} must be a contiguous tensor of {dtype} and shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _bytes(t):
+    """Address and size of a workspace (0 for None)."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        _raise("the workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 @dataclass
@@ -445,13 +471,20 @@ class LatentCache:
         return int(self.pages.shape[3]) - self.rank
 
     def c(self) -> _LatentCache:
+        """The C struct of the pages as they are now (kept while tensor, address and rank stay the same)."""
         p = self.pages
+        key = (p, p.data_ptr(), self.rank)
+        kept = self.__dict__.get("_kept")
+        if kept is not None and kept[0][0] is p and kept[0][1:] == key[1:]:
+            return kept[1]
         if p.dtype not in _ELEM:
             raise TypeError("latent cache dtype must be bfloat16 or float16")
         layers, num, size, d = p.shape
         _need(p.stride(3) == 1 and (size == 1 or p.stride(2) == d), "latent cache: a page must be contiguous")
-        return _LatentCache(self.rank, d - self.rank, size, layers, _ELEM[p.dtype], 0, num, p.stride(0), p.stride(1),
-                            ctypes.c_void_p(p.data_ptr()))
+        c = _LatentCache(self.rank, d - self.rank, size, layers, _ELEM[p.dtype], 0, num, p.stride(0), p.stride(1),
+                         ctypes.c_void_p(p.data_ptr()))
+        self.__dict__["_kept"] = (key, c)
+        return c
 
 
 @dataclass
@@ -470,135 +503,140 @@ class PageTable:
                          torch.zeros(num_pages, **i32), page_size)
 
     def c(self) -> _PageTable:
-        t = self.table
-        _need(t.dtype == torch.int32 and t.dim() == 2, "page table: table must be int32 [max_seqs, max_pages]")
-        return _PageTable(t.shape[0], t.shape[1], self.page_size, 0, self.refcount.shape[0], _ptr(t),
-                          _int32(self.lens, "page table: lens", int(t.shape[0])),
-                          _int32(self.refcount, "page table: refcount"))
+        """The C struct of the tensors as they are now (kept while they and their addresses stay the same)."""
+        t, n, r = self.table, self.lens, self.refcount
+        key = (t.data_ptr(), n.data_ptr(), r.data_ptr(), self.page_size)
+        kept = self.__dict__.get("_kept")
+        if kept is not None and kept[0] == key and kept[1] is t and kept[2] is n and kept[3] is r:
+            return kept[4]
+        _need(t.dtype == torch.int32 and t.dim() == 2 and t.is_contiguous(),
+              "page table: table must be contiguous int32 [max_seqs, max_pages]")
+        c = _PageTable(t.shape[0], t.shape[1], self.page_size, 0, r.shape[0], t.data_ptr(),
+                       _int32(n, "page table: lens", int(t.shape[0])), _int32(r, "page table: refcount"))
+        self.__dict__["_kept"] = (key, t, n, r, c)
+        return c
 
 
-@_on_device
 def kda_latent_append(cache: LatentCache, layer: int, pt: PageTable, rows, cu_tokens, latent, rope, dev_status,
                       stream=None) -> None:
     """Cache rows of new tokens into one layer; see include/kda.h.  rows int32 [n] or None (row b for sequence b),
     cu_tokens int32 [n+1], latent [T, rank] and rope [T, rope] of the cache's type (rows may be strided; rope None
     when the cache has none).  The tokens become the last ones of their rows, which pt.lens already counts."""
-    cc, pc = cache.c(), pt.c()
-    n, T = int(cu_tokens.shape[0]) - 1, int(latent.shape[0])
-    lp, ls = _rows_of(latent, "latent", cache.pages.dtype, (T, cache.rank))
-    rp, rs = (None, 0) if cache.rope == 0 else _rows_of(rope, "rope", cache.pages.dtype, (T, cache.rope))
-    rc = load_library().kda_latent_append(ctypes.byref(cc), int(layer), ctypes.byref(pc), n, _int32(rows, "rows", n),
-                                          _int32(cu_tokens, "cu_tokens"), T, lp, ls, rp, rs,
-                                          _int32(dev_status, "dev_status", 1), _stream(stream))
-    _check(rc, "kda_latent_append")
+    name = "kda_latent_append"
+    dev = _device_of(name, (cache.pages, pt.table, pt.lens, rows, cu_tokens, latent, rope, dev_status))
+    cc, dtype = cache.c(), cache.pages.dtype
+    n, T = cu_tokens.shape[0] - 1, latent.shape[0]
+    lp, ls = _rows_of(latent, "latent", dtype, (T, cc.rank))
+    rp, rs = (None, 0) if cc.rope == 0 else _rows_of(rope, "rope", dtype, (T, cc.rope))
+    _launch(load_library().kda_latent_append, name, dev, stream, cc, layer, pt.c(), n, _int32(rows, "rows", n),
+            _int32(cu_tokens, "cu_tokens"), T, lp, ls, rp, rs, _int32(dev_status, "dev_status", 1))
 
 
 def kda_latent_decode_workspace_bytes(cache: LatentCache, H: int, n: int, max_tokens: int) -> int:
+    """Bytes of workspace kda_latent_decode needs on the cache's device (0 for unsupported sizes)."""
     with torch.cuda.device(cache.pages.device if cache.pages.is_cuda else -1):
-        cc = cache.c()
-        return int(load_library().kda_latent_decode_workspace_bytes(ctypes.byref(cc), int(H), int(n), int(max_tokens)))
+        return int(load_library().kda_latent_decode_workspace_bytes(cache.c(), int(H), int(n), int(max_tokens)))
 
 
-@_on_device
 def kda_latent_decode(cache: LatentCache, layer: int, pt: PageTable, rows, cu_tokens, max_tokens: int, q, out, lse,
                       scale: float, workspace, dev_status, tree_mask=None, stream=None) -> None:
     """Absorbed latent attention of the newest tokens over the paged cache; see include/kda.h.  q [T, H, rank+rope]
     (token and head axes may be strided), out [T, H, rank], lse fp32 [T, H] or None; rows int32 [n] or None; cu_tokens int32
     [n+1], or None for max_tokens queries each of n = len(rows) (or all table rows); tree_mask int64 [T] (bit i: the query
     sees drafted token i of its sequence) or None; workspace uint8, kda_latent_decode_workspace_bytes() bytes."""
-    cc, pc = cache.c(), pt.c()
-    T, H, d = int(q.shape[0]), int(q.shape[1]), cache.rank + cache.rope
-    n = (int(cu_tokens.shape[0]) - 1 if cu_tokens is not None else
-         int(rows.shape[0]) if rows is not None else int(pt.table.shape[0]))
-    _need(rows is not None or n <= pt.table.shape[0], "kda_latent_decode: more sequences than table rows")
-    qp, qt, qh = _rows_of(q, "q", cache.pages.dtype, (T, H, d))
-    if tree_mask is not None:
-        _need(tree_mask.dtype == torch.int64 and tuple(tree_mask.shape) == (T,), f"tree_mask must be int64 [{T}]")
-    rc = load_library().kda_latent_decode(
-        ctypes.byref(cc), int(layer), ctypes.byref(pc), n, _int32(rows, "rows", n),
-        _int32(cu_tokens, "cu_tokens", n + 1), T, int(max_tokens), H, qp, qt, qh, _ptr(tree_mask), float(scale),
-        _out(out, "out", cache.pages.dtype, (T, H, cache.rank)), _out(lse, "lse", torch.float32, (T, H)),
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _int32(dev_status, "dev_status", 1), _stream(stream))
-    _check(rc, "kda_latent_decode")
+    name = "kda_latent_decode"
+    dev = _device_of(name, (cache.pages, pt.table, pt.lens, rows, cu_tokens, q, out, lse, workspace, dev_status, tree_mask))
+    cc, pc, dtype = cache.c(), pt.c(), cache.pages.dtype
+    if q.dim() != 3:
+        _raise("q must be [T, H, rank+rope]")
+    T, H, d = q.shape
+    n = (cu_tokens.shape[0] - 1 if cu_tokens is not None else rows.shape[0] if rows is not None else pc.max_seqs)
+    if rows is None and n > pc.max_seqs:
+        _raise(f"{name}: more sequences than table rows")
+    qp, qt, qh = _rows_of(q, "q", dtype, (T, H, cc.rank + cc.rope))
+    if tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.shape != (T,)
+                                  or not tree_mask.is_contiguous()):
+        _raise(f"tree_mask must be a contiguous int64 vector of {T} elements")
+    if out is None:
+        _raise("out must be a tensor")
+    ws, nbytes = _bytes(workspace)
+    _launch(load_library().kda_latent_decode, name, dev, stream, cc, layer, pc, n, _int32(rows, "rows", n),
+            _int32(cu_tokens, "cu_tokens", n + 1), T, max_tokens, H, qp, qt, qh,
+            None if tree_mask is None else tree_mask.data_ptr(), scale, _out(out, "out", dtype, (T, H, cc.rank)),
+            _out(lse, "lse", torch.float32, (T, H)), ws, nbytes, _int32(dev_status, "dev_status", 1))
 
 
-@_on_device
 def kda_latent_prefill(cu_q, cu_k, max_q: int, q, k_nope, k_rope, v, out, lse, scale: float, dev_status,
                        causal: bool = True, stream=None) -> None:
     """Expanded latent attention for prompts; see include/kda.h.  q [Tq, H, nope+rope], k_nope [Tk, H, nope],
     k_rope [Tk, rope], v [Tk, H, dv], one type, token and head axes may be strided (k_nope and v as halves of one
     tensor); out [Tq, H, dv], lse fp32 [Tq, H] or None; cu_q, cu_k int32 [nseq+1]."""
-    _need(q.dtype in _ELEM, "q must be bfloat16 or float16")
-    n = int(cu_q.shape[0]) - 1
+    name = "kda_latent_prefill"
+    dev = _device_of(name, (cu_q, cu_k, q, k_nope, k_rope, v, out, lse, dev_status))
+    dtype = q.dtype
+    if dtype not in _ELEM:
+        _raise("q must be bfloat16 or float16")
+    if q.dim() != 3 or k_nope.dim() != 3 or k_rope.dim() != 2 or v.dim() != 3:
+        _raise("q, k_nope and v must have three axes, k_rope two")
+    n = cu_q.shape[0] - 1
     Tq, H, dq = q.shape
     Tk, _, nope = k_nope.shape
-    rope, dv = int(k_rope.shape[-1]), int(v.shape[-1])
-    _need(dq == nope + rope, "q's last axis must be that of k_nope and k_rope together")
-    qp, qt, qh = _rows_of(q, "q", q.dtype, (Tq, H, dq))
-    kp, kt, kh = _rows_of(k_nope, "k_nope", q.dtype, (Tk, H, nope))
-    rp, rt = _rows_of(k_rope, "k_rope", q.dtype, (Tk, rope))
-    vp, vt, vh = _rows_of(v, "v", q.dtype, (Tk, H, dv))
-    rc = load_library().kda_latent_prefill(
-        _ELEM[q.dtype], H, nope, rope, dv, n, _int32(cu_q, "cu_q"), _int32(cu_k, "cu_k", n + 1), Tq, Tk, int(max_q),
-        int(bool(causal)), qp, qt, qh, kp, kt, kh, rp, rt, vp, vt, vh, float(scale),
-        _out(out, "out", q.dtype, (Tq, H, dv)), _out(lse, "lse", torch.float32, (Tq, H)),
-        _int32(dev_status, "dev_status", 1), _stream(stream))
-    _check(rc, "kda_latent_prefill")
+    rope, dv = k_rope.shape[1], v.shape[2]
+    if dq != nope + rope:
+        _raise("q's last axis must be that of k_nope and k_rope together")
+    if out is None:
+        _raise("out must be a tensor")
+    _launch(load_library().kda_latent_prefill, name, dev, stream, _ELEM[dtype], H, nope, rope, dv, n,
+            _int32(cu_q, "cu_q"), _int32(cu_k, "cu_k", n + 1), Tq, Tk, max_q, bool(causal),
+            *_rows_of(q, "q", dtype, (Tq, H, dq)), *_rows_of(k_nope, "k_nope", dtype, (Tk, H, nope)),
+            *_rows_of(k_rope, "k_rope", dtype, (Tk, rope)), *_rows_of(v, "v", dtype, (Tk, H, dv)), scale,
+            _out(out, "out", dtype, (Tq, H, dv)), _out(lse, "lse", torch.float32, (Tq, H)),
+            _int32(dev_status, "dev_status", 1))
 
 
 def kda_pages_workspace_bytes(pt: PageTable, n: int) -> int:
-    pc = pt.c()
-    return int(load_library().kda_pages_workspace_bytes(ctypes.byref(pc), int(n)))
+    """Bytes of workspace a kda_pages_* call of n items needs."""
+    return int(load_library().kda_pages_workspace_bytes(pt.c(), int(n)))
 
 
 def _pages_call(name: str, pt: PageTable, cache, arrays, workspace, dev_status, stream) -> None:
-    pc = pt.c()
-    head = [ctypes.byref(pc)]
-    if cache is not None:
-        cc = cache.c()
-        head.append(ctypes.byref(cc))
+    dev = _device_of(name, (pt.table, pt.lens, pt.refcount, workspace, dev_status, *arrays)
+                     + ((cache.pages,) if cache is not None else ()))
+    args = [pt.c()] if cache is None else [pt.c(), cache.c()]
     if arrays:
-        n = int(arrays[0].shape[0])
-        head += [n] + [_int32(x, f"{name}: items", n) for x in arrays]
-    rc = getattr(load_library(), name)(*head, _ptr(workspace),
-                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                       _int32(dev_status, "dev_status", 1), _stream(stream))
-    _check(rc, name)
+        n = arrays[0].shape[0]
+        args += [n, _int32(arrays[0], f"{name}: items"), _int32(arrays[1], f"{name}: items", n)]
+    _launch(getattr(load_library(), name), name, dev, stream, *args, *_bytes(workspace),
+            _int32(dev_status, "dev_status", 1))
 
 
-@_on_device
 def kda_pages_reserve(pt: PageTable, cache: LatentCache, rows, new_lens, workspace, dev_status, stream=None) -> None:
     """Rows grow to new_lens tokens: pages from the lowest free ones, a shared partly filled last page copied first
     (rows, new_lens int32 [n]; row -1 = padding).  See include/kda.h."""
     _pages_call("kda_pages_reserve", pt, cache, (rows, new_lens), workspace, dev_status, stream)
 
 
-@_on_device
 def kda_pages_truncate(pt: PageTable, rows, keep_lens, workspace, dev_status, stream=None) -> None:
     """Rows keep their first keep_lens tokens (0 ends them); pages behind lose a reference.  See include/kda.h."""
     _pages_call("kda_pages_truncate", pt, None, (rows, keep_lens), workspace, dev_status, stream)
 
 
-@_on_device
 def kda_pages_fork(pt: PageTable, cache: LatentCache, parents, children, workspace, dev_status, stream=None) -> None:
     """The empty rows children become copies of rows parents: full pages shared, a partly filled last one copied."""
     _pages_call("kda_pages_fork", pt, cache, (parents, children), workspace, dev_status, stream)
 
 
-@_on_device
 def kda_pages_compact(pt: PageTable, cache: LatentCache, workspace, dev_status, stream=None) -> None:
     """Moves the used pages into the lowest places; tables and refcounts follow.  See include/kda.h."""
     _pages_call("kda_pages_compact", pt, cache, (), workspace, dev_status, stream)
 
 
-@_on_device
 def kda_pages_copy(cache: LatentCache, src, dst, dev_status, stream=None) -> None:
     """Contents of pages src into pages dst in every layer (int32 [n]; -1 = skip), no bookkeeping."""
-    cc, n = cache.c(), int(src.shape[0])
-    rc = load_library().kda_pages_copy(ctypes.byref(cc), n, _int32(src, "src"), _int32(dst, "dst", n),
-                                       _int32(dev_status, "dev_status", 1), _stream(stream))
-    _check(rc, "kda_pages_copy")
+    name = "kda_pages_copy"
+    dev, n = _device_of(name, (cache.pages, src, dst, dev_status)), src.shape[0]
+    _launch(load_library().kda_pages_copy, name, dev, stream, cache.c(), n, _int32(src, "src"), _int32(dst, "dst", n),
+            _int32(dev_status, "dev_status", 1))
 
 
 @dataclass

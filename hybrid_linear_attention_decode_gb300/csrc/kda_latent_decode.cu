@@ -134,6 +134,10 @@ __global__ void __launch_bounds__(NT, 1)
     // tensor memory: Q (288 columns) and two S buffers of 64 in lanes 0-15 of each quarter, O in lanes 16-31
     constexpr uint32_t T_S = 384, T_O = 16u << 16;
 
+    if (tid == 32 * 4) {
+        prefetch_map(&map_c);
+        if (p.split_rope) prefetch_map(&map_r);
+    }
     if (warp == 5) umma::alloc(tmem_s, 512);
     if (tid == 0) {
         start[1] = a.n;
@@ -199,6 +203,7 @@ __global__ void __launch_bounds__(NT, 1)
     __syncthreads();
     umma::fence_after();
     const uint32_t tmem = *tmem_s;
+    allow_dependent_launch();
     const int b_start = g0 < g1 ? (int)start[1] : 0;
     const int32_t off_start = g0 < g1 ? (int32_t)start[2] : 0;
     bool ok = true;
@@ -624,6 +629,7 @@ __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const Decod
     const LatentDecodeArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.c.rank, nv = rank / 128;
     const int r = WIDE ? blockIdx.x : blockIdx.x * CW + warp, rt = r / NR, i = r - rt * NR;
+    wait_for_previous();
     const Meta mt = p.meta[blockIdx.y];
     if (mt.pieces < 2 || r >= mt.rows) return;
     float m = -INFINITY, l = 0.f;
@@ -753,9 +759,10 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     if (rc != KDA_OK) return rc;
     const int rows = a.H * a.max_tokens;
     if (q.groups > CW * a.n)  // a sequence is cut into about groups / n parts
-        kda_latent_combine_kernel<FP16, true><<<dim3(rows, q.slots_meta), CW * 32, 0, st>>>(p);
+        dependent_launch(kda_latent_combine_kernel<FP16, true>, dim3(rows, q.slots_meta), CW * 32, st, p);
     else
-        kda_latent_combine_kernel<FP16, false><<<dim3((rows + CW - 1) / CW, q.slots_meta), CW * 32, 0, st>>>(p);
+        dependent_launch(kda_latent_combine_kernel<FP16, false>, dim3((rows + CW - 1) / CW, q.slots_meta), CW * 32, st,
+                         p);
     return launch_result("kda_latent_combine_kernel launch");
 }
 
