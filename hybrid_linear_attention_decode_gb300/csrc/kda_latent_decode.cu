@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(NT, 1)
     uint64_t *p_ready = s_full + 2;
     uint64_t *q_ready = p_ready + 1;
     uint64_t *q_free = q_ready + 1;
-    uint64_t *drain = q_free + 1;
+    uint64_t *q_sent = q_free + 1;
+    uint64_t *drain = q_sent + 1;
     int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [NT / 32]
     int64_t *start = scan + NT / 32;                                   // total, first sequence, first tile in it
     uint32_t *poison = reinterpret_cast<uint32_t *>(start + 4);  // [64] tile rows that are not finite
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(p_ready, SW);
         mbar_init(q_ready, QW);
         mbar_init(q_free, 1);
+        mbar_init(q_sent, QW);
         mbar_init(drain, 1);
         fence_mbar_init();
     }
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(NT, 1)
                     else
                         set_status(a.status, KDA_DEV_BAD_PAGE);
                 }
-                ok = it < nst || warp_wait(empty + st, ph);
+                ok = it == 0 ? warp_wait(q_sent, 0) : it < nst || warp_wait(empty + st, ph);
                 if (!ok) return false;
                 if (lane == 0) mbar_arrive_expect_tx(full + st, STAGE);
                 __syncwarp();
@@ -352,25 +354,42 @@ __global__ void __launch_bounds__(NT, 1)
                 const int r = rt * NR + i0 + 8 * k, t = r / H, h = r - t * H;
                 src[k] = reinterpret_cast<const uint2 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs) + (lane & 3);
             }
-            bool first = true;
-            for (int ch = 0; ch < d; ch += 128) {  // 64 columns: this thread's 8-byte words 4n + lane % 4 of the 128 channels
-                uint32_t v[32];
+            // Rounds of 128 channels (64 columns; this thread's 8-byte words 4n + lane % 4 of them), three rounds of loads in
+            // flight.  The first of them are sent before the first tile's copies: those fill the memory system's queues for
+            // microseconds, and no product can begin without the queries.
+            constexpr int RB = 3;
+            for (int ch0 = 0; ch0 < d; ch0 += 128 * RB) {
+                uint32_t v[RB][32];
 #pragma unroll
-                for (int n = 0; n < 8; ++n)
+                for (int u = 0; u < RB; ++u)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint2 x = make_uint2(0, 0);
-                        if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
-                        v[4 * n + 2 * k] = x.x;
-                        v[4 * n + 2 * k + 1] = x.y;
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int ch = ch0 + 128 * u;
+                            uint2 x = make_uint2(0, 0);
+                            if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
+                            v[u][4 * n + 2 * k] = x.x;
+                            v[u][4 * n + 2 * k + 1] = x.y;
+                        }
+                if (ch0 == 0) {
+                    if (pieces == 0) {
+                        for (int ch = 128 * RB; ch < d; ch += 64)  // a line of each row in 16 lanes
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                if ((lane & 3) == 0 && 8 * k < rw && i0 + 8 * k < rows)
+                                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src[k] + ch / 4));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(q_sent);
+                    } else {
+                        ok = warp_wait(q_free, (pieces - 1) & 1u);
+                        if (!ok) return false;
+                        umma::fence_after();
                     }
-                if (first && pieces > 0) {
-                    ok = warp_wait(q_free, (pieces - 1) & 1u);
-                    if (!ok) return false;
-                    umma::fence_after();
                 }
-                first = false;
-                st16x64_issue(tq + ch / 2, v);
+#pragma unroll
+                for (int u = 0; u < RB; ++u)
+                    if (ch0 + 128 * u < d) st16x64_issue(tq + (ch0 + 128 * u) / 2, v[u]);
             }
             ++pieces;
             umma::wait_st();
