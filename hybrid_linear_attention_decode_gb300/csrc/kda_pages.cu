@@ -10,8 +10,7 @@
 //          the page copies of all layers in 16-KiB pieces, four 16-byte loads of a thread in flight.
 // The plan reads the pool as it was before the call and the apply launch writes it, so no item sees another's
 // effect.  Copies are bandwidth-bound.
-#include "kda_device.cuh"
-#include "kda_internal.h"
+#include "kda_latent.cuh"
 
 namespace kda {
 namespace pages {
@@ -101,6 +100,7 @@ __global__ void __launch_bounds__(PT) kda_pages_plan_kernel(const PagesArgs a) {
     const PageTableArgs &t = a.t;
     const Ws w = layout(a.ws, t.max_seqs, t.num_pages, a.n);
     const int tid = threadIdx.x;
+    latent::allow_dependent_launch();
 
     if constexpr (OP == PAGES_COMPACT) {
         const int64_t used = select_pages(t.refcount, 0, t.num_pages, false, nullptr, part);
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(AT) kda_pages_apply_kernel(const PagesArgs a) 
     const Ws w = layout(a.ws, t.max_seqs, t.num_pages, a.n);
     const int ps = t.page_size;
     const int tid = threadIdx.x;
+    latent::wait_for_previous();  // for the plan
     if constexpr (OP == PAGES_COMPACT) {
         for (int s = blockIdx.x; s < t.max_seqs; s += gridDim.x) {
             const int64_t len = t.lens[s], have = (len + ps - 1) / ps;
@@ -299,6 +300,16 @@ __global__ void __launch_bounds__(AT) kda_latent_append_kernel(const AppendArgs 
     const int lane = threadIdx.x & 31;
     const int64_t tok = (int64_t)blockIdx.x * (AT / 32) + (threadIdx.x >> 5);
     if (tok >= a.num_tokens) return;
+    // the row itself first: it does not depend on where it goes
+    const int rw = a.c.rank / 8, w = rw + a.c.rope / 8;  // 16-byte words
+    const uint4 *l = reinterpret_cast<const uint4 *>(a.latent + tok * a.latent_stride);
+    const uint4 *r = reinterpret_cast<const uint4 *>(a.rope + tok * a.rope_stride);
+    uint4 v[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int j = lane + 32 * k;
+        if (j < w) v[k] = j < rw ? __ldcs(l + j) : __ldcs(r + j - rw);
+    }
     // the last b with cu[b] <= tok: [lo, hi) narrows to one entry, 32 ways a step
     int lo = 0, hi = a.n + 1;
     while (hi - lo > 1) {
@@ -337,17 +348,8 @@ __global__ void __launch_bounds__(AT) kda_latent_append_kernel(const AppendArgs 
         if (lane == 0) set_status(a.status, bits);
         return;
     }
-    const int rw = a.c.rank / 8, w = rw + a.c.rope / 8;  // 16-byte words
     uint4 *to = reinterpret_cast<uint4 *>(a.c.pages + page * a.c.page_stride +
                                           (pos % a.t.page_size) * (a.c.rank + a.c.rope));
-    const uint4 *l = reinterpret_cast<const uint4 *>(a.latent + tok * a.latent_stride);
-    const uint4 *r = reinterpret_cast<const uint4 *>(a.rope + tok * a.rope_stride);
-    uint4 v[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const int j = lane + 32 * k;
-        if (j < w) v[k] = j < rw ? __ldg(l + j) : __ldg(r + j - rw);
-    }
 #pragma unroll
     for (int k = 0; k < 3; ++k)
         if (lane + 32 * k < w) to[lane + 32 * k] = v[k];
@@ -368,7 +370,7 @@ static int launch_pages_op(const PagesArgs &a, cudaStream_t st) {
     const int rc = launch_result("kda_pages_plan_kernel launch");
     if (rc != KDA_OK) return rc;
     // eight CTAs a multiprocessor are resident; how much there is to copy is known on the device alone
-    kda_pages_apply_kernel<OP><<<(unsigned)current_device_sms() * 8, AT, 0, st>>>(a);
+    latent::dependent_launch(kda_pages_apply_kernel<OP>, dim3((unsigned)current_device_sms() * 8), AT, st, a);
     return launch_result("kda_pages_apply_kernel launch");
 }
 
