@@ -97,7 +97,8 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" 
 // The group's part [at, end) of the list, which begins `off` places into sequence b: `f(b, s, first tile, tiles, n, v)`
 // for each sequence that has tiles in it, the n-th of the group, with v its place in the list; `get(b)` reads the sequence.
 template <class G, class F>
-__device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64_t at, int64_t end, int rt, G get, F f) {
+__device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64_t at, int64_t end, int64_t row0, G get,
+                                     F f) {
     int piece = 0;
     for (; at < end && b < p.a.n; ++b, off = 0) {
         const Seq s = get(b);
@@ -105,11 +106,131 @@ __device__ __forceinline__ void walk(const DecodeP &p, int b, int32_t off, int64
         const int32_t take = (int32_t)min((int64_t)(s.tiles + START - off), end - at);
         const int32_t first = max(off - START, 0), nt = max(off + take - START, 0) - first;
         if (nt > 0) {
-            if (rt * NR < s.nq * p.a.H && !f(b, s, first, nt, piece, at - off)) return;
+            if (row0 < s.nq * p.a.H && !f(b, s, first, nt, piece, at - off)) return;
             ++piece;
         }
         at += take;
     }
+}
+
+// A group's part of the list: places [lo, hi), beginning `off` places into sequence b; per: places of a whole part.
+struct Range {
+    int32_t b, off;
+    int64_t lo, hi, per;
+};
+
+struct Scratch {  // shared memory of group_range()
+    int64_t scan[NT / 32];
+    int64_t b, off;
+};
+
+// Prefix sums of the sequences' places, each thread a run of sequences.  Called by all NT threads; also writes zeros for the
+// queries of empty (or bad) sequences.  `leader`: the CTA of the group that keeps its meta record.
+__device__ __forceinline__ Range group_range(const DecodeP &p, int g, bool leader, Scratch *sh) {
+    const LatentDecodeArgs &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = a.c.rank, H = a.H;
+    const int run = (a.n + NT - 1) / NT;
+    const int r0 = min(a.n, tid * run), r1 = min(a.n, r0 + run);
+    int64_t mine = 0;
+    for (int b = r0; b < r1; ++b) {
+        const int32_t t = seq_of(a, b).tiles;
+        mine += t ? t + START : 0;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) sh->scan[warp] = incl;
+    if (tid == 0) {
+        sh->b = a.n;
+        sh->off = 0;
+    }
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sh->scan[w];
+        total += sh->scan[w];
+    }
+    Range R;
+    R.per = (total + p.groups - 1) / p.groups;
+    R.lo = min(total, g * R.per);
+    R.hi = min(total, R.lo + R.per);
+    if (mine > 0 && R.lo >= before && R.lo < before + mine) {
+        int64_t at = before;
+        for (int b = r0; b < r1; ++b) {
+            int32_t t = seq_of(a, b).tiles;
+            t += t ? START : 0;
+            if (R.lo < at + t) {
+                sh->b = b;
+                sh->off = R.lo - at;
+                break;
+            }
+            at += t;
+        }
+    }
+    if (!p.by_seq && leader && tid == 0) p.meta[g].pieces = 0;
+    for (int b = blockIdx.x; b < a.n; b += gridDim.x) {
+        const Seq s = seq_of(a, b);
+        if (s.bits && tid == 0) set_status(a.status, s.bits);
+        if (s.tiles > 0) continue;
+        if (p.by_seq && tid == 0) p.meta[b].pieces = 0;
+        uint4 *o = reinterpret_cast<uint4 *>(a.out + s.c0 * H * rank);
+        for (int64_t i = tid; i < (int64_t)s.nq * H * rank / 8; i += NT) o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int i = tid; i < s.nq * H; i += NT) a.lse[s.c0 * H + i] = -INFINITY;
+    }
+    __syncthreads();
+    R.b = (int32_t)sh->b;
+    R.off = (int32_t)sh->off;
+    return R;
+}
+
+// The record of a cut sequence, by the leader of the group in which it begins (places v .. v + START + tiles of the list).
+__device__ __forceinline__ void record(const DecodeP &p, const Range &R, int g, int b, const Seq &s, int piece, int64_t v) {
+    Meta m;
+    m.pieces = (int32_t)((v + START + s.tiles - 1) / R.per - g) + 1;
+    m.group = g;
+    m.second = piece > 0;
+    m.rows = s.nq * p.a.H;
+    m.row0 = s.c0 * p.a.H;
+    if (p.by_seq)
+        p.meta[b] = m;
+    else if (m.pieces > 1)
+        p.meta[g] = m;
+}
+
+// Bits of the drafted tokens that the query token t of a sequence sees.
+__device__ __forceinline__ uint64_t drafts_seen(const LatentDecodeArgs &a, const Seq &s, int t) {
+    const uint64_t chain = t >= 63 ? ~0ull : (2ull << t) - 1, all = s.nq >= 64 ? ~0ull : (1ull << s.nq) - 1;
+    return (a.tree ? a.tree[s.c0 + t] : chain) & all;
+}
+
+// Rows [lo, hi) of a tile made ready for the second product by the four warps of a warpgroup (warp index w4): a row
+// behind the sequence becomes zeros (a zero weight times NaN is NaN), and so does a drafted row that is not finite, which
+// `poison` marks.  valid: rows of the sequence; drafts: first drafted row that is looked over (valid: none).  nl, nw: 16-byte
+// words of a row's latents and of all its channels here.
+template <bool FP16>
+__device__ __forceinline__ void fix_tile(uint8_t *x, uint32_t group, int w4, int lane, int valid, int drafts, int nl, int nw,
+                                         uint32_t *poison) {
+    for (int r = valid + w4; r < TILE; r += 4)
+        for (int w = lane; w < nl; w += 32)
+            *reinterpret_cast<uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+    for (int r = drafts + w4; r < valid; r += 4) {
+        bool bad = false;
+        for (int w = lane; w < nw; w += 32)
+            bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 +
+                                                                     (((w ^ r) & 7) << 4)));
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad)
+            for (int w = lane; w < nl; w += 32)
+                *reinterpret_cast<uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
+                    make_uint4(0, 0, 0, 0);
+        if (lane == 0) poison[r] = bad;
+    }
+    fence_proxy_async_smem();
 }
 
 template <bool FP16>
@@ -131,9 +252,8 @@ __global__ void __launch_bounds__(NT, 1)
     uint64_t *q_free = q_ready + 1;
     uint64_t *q_sent = q_free + 1;
     uint64_t *drain = q_sent + 1;
-    int64_t *scan = reinterpret_cast<int64_t *>(drain + 1);      // [NT / 32]
-    int64_t *start = scan + NT / 32;                                   // total, first sequence, first tile in it
-    uint32_t *poison = reinterpret_cast<uint32_t *>(start + 4);  // [64] tile rows that are not finite
+    Scratch *scratch = reinterpret_cast<Scratch *>(drain + 1);
+    uint32_t *poison = reinterpret_cast<uint32_t *>(scratch + 1);  // [64] tile rows that are not finite
     Seq *seq_s = reinterpret_cast<Seq *>(poison + 64);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(seq_s + 1);
 
@@ -148,8 +268,6 @@ __global__ void __launch_bounds__(NT, 1)
     }
     if (warp == 5) umma::alloc(tmem_s, 512);
     if (tid == 0) {
-        start[1] = a.n;
-        start[2] = 0;
         for (int s = 0; s < MAX_STAGES; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
@@ -164,61 +282,11 @@ __global__ void __launch_bounds__(NT, 1)
         fence_mbar_init();
     }
 
-    // ---- this group's part of the list: prefix sums of the sequences' tiles, each thread a run of sequences ----
-    const int run = (a.n + NT - 1) / NT;
-    const int r0 = min(a.n, tid * run), r1 = min(a.n, r0 + run);
-    int64_t mine = 0;
-    for (int b = r0; b < r1; ++b) {
-        const int32_t t = seq_of(a, b).tiles;
-        mine += t ? t + START : 0;
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    const int64_t per = (total + p.groups - 1) / p.groups;
-    const int64_t g0 = min(total, g * per), g1 = min(total, g0 + per);
-    if (mine > 0 && g0 >= before && g0 < before + mine) {
-        int64_t at = before;
-        for (int b = r0; b < r1; ++b) {
-            int32_t t = seq_of(a, b).tiles;
-            t += t ? START : 0;
-            if (g0 < at + t) {
-                start[1] = b;
-                start[2] = g0 - at;
-                break;
-            }
-            at += t;
-        }
-    }
-    if (!p.by_seq && rt == 0 && tid == 0) p.meta[g].pieces = 0;
-    // queries of empty (or bad) sequences: zeros
-    for (int b = blockIdx.x; b < a.n; b += gridDim.x) {
-        const Seq s = seq_of(a, b);
-        if (s.bits && tid == 0) set_status(a.status, s.bits);
-        if (s.tiles > 0) continue;
-        if (p.by_seq && tid == 0) p.meta[b].pieces = 0;
-        uint4 *o = reinterpret_cast<uint4 *>(a.out + s.c0 * H * rank);
-        for (int64_t i = tid; i < (int64_t)s.nq * H * rank / 8; i += NT) o[i] = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-            for (int i = tid; i < s.nq * H; i += NT) a.lse[s.c0 * H + i] = -INFINITY;
-    }
     umma::fence_before();
-    __syncthreads();
+    const Range R = group_range(p, g, rt == 0, scratch);
     umma::fence_after();
     const uint32_t tmem = *tmem_s;
     allow_dependent_launch();
-    const int b_start = g0 < g1 ? (int)start[1] : 0;
-    const int32_t off_start = g0 < g1 ? (int32_t)start[2] : 0;
     bool ok = true;
     auto read = [&](int b) { return seq_of(a, b); };
 
@@ -230,7 +298,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int ps = a.c.page_size;
         int it = 0, st = 0;
         uint32_t ph = 1;  // a fresh ring is empty
-        walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &s, int32_t off, int32_t nt, int, int64_t) {
+        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int, int64_t) {
             const int32_t *trow = a.t.table + (int64_t)s.row * a.t.max_pages;
             for (int j = 0; j < nt; ++j, ++it) {
                 const int key = (off + j) * TILE + (lane & 7) * 8;  // below 2^31: len is
@@ -273,7 +341,7 @@ __global__ void __launch_bounds__(NT, 1)
         uint32_t pieces = 0;
         int it = 0, st = 0;  // tile whose P V comes next, and its stage
         uint32_t ph = 0;     // parity of the stage's full barrier
-        walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &, int32_t, int32_t nt, int, int64_t) {
+        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &, int32_t, int32_t nt, int, int64_t) {
             ok = warp_wait(q_ready, pieces++ & 1u);
             if (!ok) return false;
             umma::fence_after();
@@ -356,7 +424,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int w4 = warp & 3;                                 // quarter of the lanes
         const uint32_t tq = tmem + ((uint32_t)(32 * w4) << 16);
         uint32_t pieces = 0;
-        walk(p, b_start, off_start, g0, g1, rt, read, [&](int, const Seq &s, int32_t, int32_t, int, int64_t) {
+        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &s, int32_t, int32_t, int, int64_t) {
             const int rows = min(NR, s.nq * H - rt * NR);
             const int rw = rows_per_warp(rows), i0 = rw * w4 + (lane >> 2);  // this thread's rows: i0 and, if rw 16, i0 + 8
             const uint2 *src[2];
@@ -430,35 +498,21 @@ __global__ void __launch_bounds__(NT, 1)
         uint32_t ph_prev = 0;
         int st = 0;
         uint32_t ph = 0;
-        walk(p, b_start, off_start, g0, g1, rt, read_once, [&](int b, const Seq &s, int32_t off, int32_t nt, int piece, int64_t v) {
+        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read_once, [&](int b, const Seq &s, int32_t off, int32_t nt, int piece, int64_t v) {
             const int rows = min(NR, s.nq * H - rt * NR);
             // this thread's rows of the row tile, i0 and (where a warp has 16) i0 + 8, are rows i0p, i0p + 8 of the products
             const int rw = rows_per_warp(rows), i0 = rw * warp + (lane >> 2), i0p = 16 * warp + (lane >> 2);
             const int nk = rw / 8;
             const bool act = rw * warp < rows;
             const int64_t orow = s.c0 * H + rt * NR;  // output row of the row tile's first row
-            if (rt == 0 && tid == 0 && off == 0) {
-                const int64_t last = (v + START + s.tiles - 1) / per;
-                Meta m;
-                m.pieces = (int32_t)(last - g) + 1;
-                m.group = g;
-                m.second = piece > 0;
-                m.rows = s.nq * H;
-                m.row0 = s.c0 * H;
-                if (p.by_seq)
-                    p.meta[b] = m;
-                else if (m.pieces > 1)
-                    p.meta[g] = m;
-            }
+            if (rt == 0 && tid == 0 && off == 0) record(p, R, g, b, s, piece, v);
             // what the thread's two rows see among the drafted tokens
             const int base = s.len - s.nq;
             uint64_t see[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int i = i0 + 8 * k;
-                const int t = i < rows ? (rt * NR + i) / H : 0;
-                const uint64_t chain = t >= 63 ? ~0ull : (2ull << t) - 1, all = s.nq >= 64 ? ~0ull : (1ull << s.nq) - 1;
-                see[k] = (a.tree ? a.tree[s.c0 + t] : chain) & all;
+                see[k] = drafts_seen(a, s, i < rows ? (rt * NR + i) / H : 0);
             }
             const bool scan_drafts = s.nq > 1 || a.tree;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -468,29 +522,10 @@ __global__ void __launch_bounds__(NT, 1)
                 umma::fence_after();
                 const bool tail = key0 + TILE > base;
                 if (tail) {
-                    // rows behind the sequence become zeros (a zero weight times NaN is NaN); drafted rows that
-                    // are not finite do too, and count as NaN scores for the queries that see them
                     wait(full + st, ph);
-                    uint8_t *x = KV + (uint32_t)st * STAGE;
                     const int valid = min(TILE, s.len - key0);
-                    for (int r = valid + warp; r < TILE; r += SW)
-                        for (int w = lane; w < rank / 8; w += 32)
-                            *reinterpret_cast<uint4 *>(x + (r >> 3) * GROUP + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
-                                make_uint4(0, 0, 0, 0);
-                    if (scan_drafts)
-                        for (int r = max(0, base - key0) + warp; r < valid; r += SW) {
-                            bool bad = false;
-                            for (int w = lane; w < nw; w += 32)
-                                bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(
-                                    x + (r >> 3) * GROUP + (w >> 3) * ATOM + (r & 7) * 128 + (((w ^ r) & 7) << 4)));
-                            bad = __any_sync(0xffffffffu, bad);
-                            if (bad)
-                                for (int w = lane; w < rank / 8; w += 32)
-                                    *reinterpret_cast<uint4 *>(x + (r >> 3) * GROUP + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
-                                        make_uint4(0, 0, 0, 0);
-                            if (lane == 0) poison[r] = bad;
-                        }
-                    fence_proxy_async_smem();
+                    fix_tile<FP16>(KV + (uint32_t)st * STAGE, GROUP, warp, lane, valid,
+                                   scan_drafts ? max(0, base - key0) : valid, rank / 8, nw, poison);
                     softmax_sync();
                 }
                 uint32_t sr[32];  // 4n + i: row i0 + 8*(i/2), token 8n + 2*(lane%4) + i%2
@@ -737,11 +772,11 @@ struct Plan {
 
 static Plan plan(int rank, int H, int n, int max_tokens) {
     Plan q;
-    const int rows = H * max_tokens;
+    const int rows = H * max_tokens, sms = current_device_sms();
     q.nrt = (rows + NR - 1) / NR;
-    q.groups = std::max(1, current_device_sms() / q.nrt);
+    q.groups = std::max(1, sms / q.nrt);
     q.slots_meta = std::min(n, q.groups);
-    const size_t parts = (size_t)q.groups * 2 * q.nrt * NR;
+    const size_t parts = (size_t)std::max(sms, q.nrt) * 2 * NR;  // whatever the row tiles: groups * nrt is no more
     q.off_part = ((size_t)q.slots_meta * sizeof(Meta) + 255) / 256 * 256;
     q.off_l = q.off_part + parts * rank * 4;
     q.bytes = q.off_l + parts * 4;
@@ -762,14 +797,16 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     const EncodeTiledFn enc = encoder();
     if (!enc) return fail(KDA_ERR_CUDA, "latent decode: cuTensorMapEncodeTiled is not available");
     CUtensorMap map_c, map_r;
-    const int d = a.c.rank + a.c.rope, split = a.c.rope % 64 != 0;
-    const int nc = split ? a.c.rank / 64 : d / 64;  // 64-channel chunks that one box takes
-    const int64_t dims[4] = {64, a.c.page_size, nc, a.c.num_pages}, strides[3] = {d, 64, a.c.page_stride};
-    const int box[4] = {64, 8, nc, 1};
+    const int d = a.c.rank + a.c.rope;
+    const bool split = a.c.rope % 64 != 0;  // one box takes the rotary channels too where they are a whole chunk
+    const int64_t chunks = split ? a.c.rank / 64 : d / 64;
+    const int64_t dims[4] = {64, a.c.page_size, chunks, a.c.num_pages}, strides[3] = {d, 64, a.c.page_stride};
+    const int box[4] = {64, 8, (int)chunks, 1};
     if (!tensor_map(enc, &map_c, FP16, a.c.pages, 4, dims, strides, box) ||
         (split && !map_3d(enc, &map_r, FP16, a.c.pages + a.c.rank, a.c.rope, a.c.page_size, a.c.num_pages, d,
                           a.c.page_stride, 8, 1)))
         return fail(KDA_ERR_CUDA, "latent decode: tensor map encoding failed");
+    if (!split) map_r = map_c;  // not read
     DecodeP p;
     p.a = a;
     p.groups = q.groups;
@@ -781,10 +818,11 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     p.meta = reinterpret_cast<Meta *>(ws);
     p.part = reinterpret_cast<float *>(ws + q.off_part);
     p.part_l = reinterpret_cast<float *>(ws + q.off_l);
+    const uint32_t stage = p.nch * ATOM * (TILE / 8);
     const uint32_t fixed = 1024 + NR * 128 + MISC;
-    p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / (p.nch * ATOM * (TILE / 8)));
-    const uint32_t smem = fixed + p.nst * p.nch * ATOM * (TILE / 8);
-    kda_latent_decode_kernel<FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, split ? map_r : map_c);
+    p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / stage);
+    const uint32_t smem = fixed + p.nst * stage;
+    kda_latent_decode_kernel<FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, map_r);
     const int rc = launch_result("kda_latent_decode_kernel launch");
     if (rc != KDA_OK) return rc;
     const int rows = a.H * a.max_tokens;
