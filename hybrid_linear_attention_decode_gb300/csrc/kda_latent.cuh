@@ -63,15 +63,31 @@ __device__ __forceinline__ uint16_t to_elem(float x) {
     return FP16 ? __half_as_ushort(__float2half_rn(x)) : f2bf(x);
 }
 
-// Whether one of the two elements in a word is infinite or NaN (all exponent bits set).
+// Looks for infinities and NaN, two elements an instruction: acc + x * 0 stays finite as long as every x was.
 template <bool FP16>
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-    constexpr uint32_t e = FP16 ? 0x7c00u : 0x7f80u;
-    return (w & e) == e || ((w >> 16) & e) == e;
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc) {
+    uint32_t r;
+    if constexpr (FP16)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
 }
 template <bool FP16>
-__device__ __forceinline__ bool nonfinite8(uint4 w) {
-    return nonfinite2<FP16>(w.x) || nonfinite2<FP16>(w.y) || nonfinite2<FP16>(w.z) || nonfinite2<FP16>(w.w);
+__device__ __forceinline__ void times_zero4(uint4 x, uint32_t (&acc)[4]) {
+    acc[0] = times_zero<FP16>(x.x, acc[0]);
+    acc[1] = times_zero<FP16>(x.y, acc[1]);
+    acc[2] = times_zero<FP16>(x.z, acc[2]);
+    acc[3] = times_zero<FP16>(x.w, acc[3]);
+}
+// Whether any of the sums is not finite (then it is NaN: all exponent bits set).
+template <bool FP16>
+__device__ __forceinline__ bool nonfinite(const uint32_t (&acc)[4]) {
+    constexpr uint32_t e = FP16 ? 0x7c00u : 0x7f80u;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad |= (acc[k] & e) == e || ((acc[k] >> 16) & e) == e;
+    return bad;
 }
 
 // Instruction descriptor fields on top of umma::idesc(): 16-bit operand format, MN-major ("transposed") A or B.

@@ -219,11 +219,12 @@ __device__ __forceinline__ void fix_tile(uint8_t *x, uint32_t group, int w4, int
             *reinterpret_cast<uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =
                 make_uint4(0, 0, 0, 0);
     for (int r = drafts + w4; r < valid; r += 4) {
-        bool bad = false;
+        uint32_t acc[4] = {0, 0, 0, 0};
         for (int w = lane; w < nw; w += 32)
-            bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 +
-                                                                     (((w ^ r) & 7) << 4)));
-        bad = __any_sync(0xffffffffu, bad);
+            times_zero4<FP16>(*reinterpret_cast<const uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 +
+                                                               (((w ^ r) & 7) << 4)),
+                              acc);
+        const bool bad = __any_sync(0xffffffffu, nonfinite<FP16>(acc));
         if (bad)
             for (int w = lane; w < nl; w += 32)
                 *reinterpret_cast<uint4 *>(x + (r >> 3) * group + (w >> 3) * ATOM + (r & 7) * 128 + ((w & 7) << 4)) =

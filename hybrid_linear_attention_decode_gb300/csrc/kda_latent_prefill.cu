@@ -239,16 +239,16 @@ __global__ void __launch_bounds__(PNT, 1)
             if (!ok) break;
             uint8_t *mk4 = mark + (f & 3) * PK;
             bool found = false;
-            // a lane per group of rows: each row's 64 or 128 channels are 8 or 16 words
-            for (int r0 = 0; r0 < PK; r0 += 32) {
+            for (int r0 = 0; r0 < PK; r0 += 32) {  // a lane per row of 8 or 16 words
                 const int r = r0 + lane;
-                bool bad = false;
+                uint32_t acc[4] = {0, 0, 0, 0};
                 for (int c = 0; c < vc; ++c) {
                     const uint8_t *row = R + (uint32_t)((u + c) % NU) * UNIT + r * 128;
 #pragma unroll
                     for (int w = 0; w < 8; ++w)
-                        bad |= nonfinite8<FP16>(*reinterpret_cast<const uint4 *>(row + (((w ^ lane) & 7) << 4)));
+                        times_zero4<FP16>(*reinterpret_cast<const uint4 *>(row + (((w ^ lane) & 7) << 4)), acc);
                 }
+                const bool bad = nonfinite<FP16>(acc);
                 const bool mine = bad && r < valid;
                 if (bad || r >= valid)
                     for (int c = 0; c < vc; ++c) {
