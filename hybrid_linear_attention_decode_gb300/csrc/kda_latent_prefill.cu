@@ -10,6 +10,8 @@
 //   warp 8   TMA: keys, rotary keys and values as units of 128 rows x 64 channels (16 KiB), one ring
 //   warp 9   MMA: S = Q [K | R]^T (M 128, N 128), then O += P V with P in tensor memory and V as it lies (MN-major).
 //            Order O0(j), S0(j+1), O1(j), S1(j+1): one tile's softmax runs beside the other's two products.
+//            Where 128 queries or fewer are left there is no second query tile: the two then are the same queries over the
+//            even and the odd key tiles, and the first one's warps join the results at the end.
 //   warp 10  value rows that a query of the CTA does not see: those behind the sequence become zeros, and
 //            those that are not finite too (0 x NaN is NaN), with a mark that makes the weights of the queries
 //            that see them NaN.  Only tiles that some query sees in part need it.
@@ -63,8 +65,14 @@ __global__ void __launch_bounds__(PNT, 1)
         nt[t] = last < qt + t * PQ ? 0 : (limit(last) + PK - 1) / PK;
     }
     const int ntile = max(nt[0], nt[1]);
+    const bool split = nt[1] == 0 && ntile > 1 && qt + PQ >= nq;  // one query tile: even and odd key tiles
+    if (split) {
+        nt[0] = (ntile + 1) / 2;
+        nt[1] = ntile / 2;
+    }
+    const int lead = split ? 2 : 1;  // the ring holds K_0 .. K_lead-1, then V_0 K_lead V_1 K_lead+1 ...
     const int jf = limit(qt) / PK;  // from this tile on some query sees a part only
-    const int kc = a.nope / 64 + 1, vc = a.dv / 64, per = kc + vc;  // units of a key tile, of a value tile, of both
+    const int kc = a.nope / 64 + 1, vc = a.dv / 64;  // units of a key tile, of a value tile
     const int NU = p.units;
 
     extern __shared__ uint8_t smem_raw[];
@@ -80,14 +88,17 @@ __global__ void __launch_bounds__(PNT, 1)
     uint64_t *o_done = bars + 28;   // [2] its output
     uint64_t *q_full = bars + 30;
     uint64_t *drain = bars + 31;
-    uint32_t *any = reinterpret_cast<uint32_t *>(drain + 1);  // [4] whether a value tile has marks
+    uint64_t *half_done = bars + 32;  // split: the odd key tiles' maxima and sums are written
+    float *half_ml = reinterpret_cast<float *>(R);  // [2][PQ], over the ring when it is no longer used
+    uint32_t *any = reinterpret_cast<uint32_t *>(bars + 33);  // [4] whether a value tile has marks
     uint32_t *tmem_s = any + 4;
     uint8_t *mark = reinterpret_cast<uint8_t *>(tmem_s + 1);  // [4][PK]
+    uint8_t *tag = mark + 4 * PK;  // [MAX_UNITS] producer's note of what a unit holds: barrier slot, value or key, parity
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 9) umma::alloc(tmem_s, 512);
     if (tid == 0) {
-        for (int i = 0; i < 32; ++i) mbar_init(bars + i, i == 26 || i == 27 ? 4 : 1);  // p_ready: four warps
+        for (int i = 0; i < 33; ++i) mbar_init(bars + i, i == 26 || i == 27 || i == 32 ? 4 : 1);  // p_ready, half_done: four warps
         fence_mbar_init();
     }
     umma::fence_before();
@@ -101,55 +112,60 @@ __global__ void __launch_bounds__(PNT, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 8) {
         // ================================ producer ================================
-        int j = 0;
+        int ki = 0, vi = 0;  // key and value tiles sent for
         if (lane == 0 && ntile > 0) {
             mbar_arrive_expect_tx(q_full, (uint32_t)(2 * kc) * UNIT);
             for (int t = 0; t < 2; ++t)
                 for (int c = 0; c < kc; ++c)
                     tma_load_3d(Q + (uint32_t)(t * kc + c) * UNIT, &mq, c * 64, h, (int)q_lo + qt + t * PQ, q_full);
-            int u = 0, used = 0;     // ring position, units in use up to the whole ring
-            int old = 0, oldc = 0;   // tile and part of the unit that was there before
-            auto next = [&]() {      // waits until the unit at u is free and returns it
+            int u = 0, used = 0;  // ring position, units in use up to the whole ring
+            auto next = [&](bool value, int i) {  // the unit at u, for a part of K_i or V_i, once it is free
                 if (used < NU) {
                     ++used;
                 } else {
-                    ok = ok && mbar_wait((oldc < kc ? k_empty : v_empty) + (old & 3), (uint32_t)(old >> 2) & 1u);
-                    if (++oldc == per) oldc = 0, ++old;
+                    const int g = tag[u];
+                    ok = ok && mbar_wait((g & 4 ? v_empty : k_empty) + (g & 3), (uint32_t)g >> 3);
                 }
+                tag[u] = (uint8_t)((i & 3) | (value ? 4 : 0) | ((i >> 2) & 1) << 3);
                 const int r = u;
                 if (++u == NU) u = 0;
                 return r;
             };
-            for (; j < ntile; ++j) {
-                const int row = (int)k_lo + j * PK;
-                uint64_t *kb = k_full + (j & 3), *vb = j < jf ? v_full + (j & 3) : v_raw + ((j - jf) & 3);
+            auto load_k = [&](int i) {
+                uint64_t *bar = k_full + (i & 3);
                 for (int c = 0; c < kc; ++c) {
-                    uint8_t *dst = R + (uint32_t)next() * UNIT;
-                    if (!ok) break;
-                    if (c == 0) mbar_arrive_expect_tx(kb, (uint32_t)kc * UNIT);
+                    uint8_t *dst = R + (uint32_t)next(false, i) * UNIT;
+                    if (!ok) return;
+                    if (c == 0) {
+                        mbar_arrive_expect_tx(bar, (uint32_t)kc * UNIT);
+                        ++ki;
+                    }
                     if (c < kc - 1)
-                        tma_load_3d(dst, &mk, c * 64, h, row, kb);
+                        tma_load_3d(dst, &mk, c * 64, h, (int)k_lo + i * PK, bar);
                     else
-                        tma_load_3d(dst, &mr, 0, 0, row, kb);
+                        tma_load_3d(dst, &mr, 0, 0, (int)k_lo + i * PK, bar);
                 }
+            };
+            for (int i = 0; i < min(lead, ntile) && ok; ++i) load_k(i);
+            for (; vi < ntile && ok; ++vi) {
+                uint64_t *bar = vi < jf ? v_full + (vi & 3) : v_raw + ((vi - jf) & 3);
+                const int u0 = next(true, vi), u1 = vc == 2 ? next(true, vi) : u0, row = (int)k_lo + vi * PK;
                 if (!ok) break;
-                const int u0 = next(), u1 = vc == 2 ? next() : u0;
-                if (!ok) break;
-                mbar_arrive_expect_tx(vb, (uint32_t)vc * UNIT);
-                tma_load_3d(R + (uint32_t)min(u0, u1) * UNIT, &mv, 0, h, row, vb);
-                if (vc == 2) tma_load_3d(R + (uint32_t)max(u0, u1) * UNIT, &mv, 64, h, row, vb);
+                mbar_arrive_expect_tx(bar, (uint32_t)vc * UNIT);
+                tma_load_3d(R + (uint32_t)min(u0, u1) * UNIT, &mv, 0, h, row, bar);
+                if (vc == 2) tma_load_3d(R + (uint32_t)max(u0, u1) * UNIT, &mv, 64, h, row, bar);
+                if (vi + lead < ntile) load_k(vi + lead);
             }
         }
         if (__syncthreads_or(!ok) && lane == 0 && ntile > 0) {  // copies still in flight land before the CTA ends
             constexpr uint64_t kDrainNs = 10000000ull;
             mbar_wait(q_full, 0, kDrainNs);
-            for (int i = max(0, j - 3); i <= min(j, ntile - 1); ++i) {
-                mbar_wait(k_full + (i & 3), (uint32_t)(i >> 2) & 1u, kDrainNs);
+            for (int i = max(0, ki - 4); i < ki; ++i) mbar_wait(k_full + (i & 3), (uint32_t)(i >> 2) & 1u, kDrainNs);
+            for (int i = max(0, vi - 4); i < vi; ++i)
                 if (i < jf)
                     mbar_wait(v_full + (i & 3), (uint32_t)(i >> 2) & 1u, kDrainNs);
                 else
                     mbar_wait(v_raw + ((i - jf) & 3), (uint32_t)((i - jf) >> 2) & 1u, kDrainNs);
-            }
         }
     } else if (warp == 9) {
         // ================================ MMA issuer ================================
@@ -158,11 +174,11 @@ __global__ void __launch_bounds__(PNT, 1)
         const uint64_t dq0 = umma::sdesc(smem_addr(Q)), dr0 = umma::sdesc(smem_addr(R));
         const int kr = a.rope / 16;
         constexpr uint32_t UW = UNIT >> 4;  // a unit in descriptor words
-        int u = 0;                          // ring position of the key tile whose scores come next
+        int u = 0;
         auto after = [&](int v, int n) { return v + n < NU ? v + n : v + n - NU; };
         auto scores = [&](int t, int v) {  // one thread: S_t = Q_t [K | R]^T of the key tile at ring position v
             const uint32_t ts = tmem + t * PK;
-            uint64_t dq = dq0 + (uint64_t)(t * kc * UW);
+            uint64_t dq = dq0 + (uint64_t)(split ? 0 : t * kc * UW);
             for (int c = 0; c < kc - 1; ++c) {
                 const uint64_t dk = dr0 + (uint64_t)(v * UW);
 #pragma unroll
@@ -179,51 +195,100 @@ __global__ void __launch_bounds__(PNT, 1)
             }
             umma::commit(s_full + t);
         };
-        if (ntile > 0) {
-            ok = warp_wait(q_full, 0) && warp_wait(k_full, 0);
+        auto weigh = [&](int t, uint64_t dv, bool first, bool last) {  // one thread: O_t += P_t V
+            const uint32_t to = tmem + T_O + t * 128, tp = tmem + t * PK;
+#pragma unroll
+            for (int k = 0; k < PK / 16; ++k)
+                mma_ts(to, tp + k * 8, dv + (uint64_t)(k * 2048 >> 4), id_o, !first || k > 0);
+            if (last) umma::commit(o_done + t);
+        };
+        auto wait_k = [&](int i) {
+            ok = ok && warp_wait(k_full + (i & 3), (uint32_t)(i >> 2) & 1u);
             umma::fence_after();
+        };
+        auto wait_v = [&](int i) {
+            ok = ok && (i < jf ? warp_wait(v_full + (i & 3), (uint32_t)(i >> 2) & 1u)
+                               : warp_wait(fixed + ((i - jf) & 3), (uint32_t)((i - jf) >> 2) & 1u));
+        };
+        // u: ring position of what is used next; the order of use is the ring's
+        auto take_v = [&]() {
+            const int v0 = u, v1 = vc == 2 ? after(v0, 1) : v0;
+            u = after(u, vc);
+            return sdesc_at(smem_addr(R + (uint32_t)min(v0, v1) * UNIT), (uint32_t)abs(v1 - v0) * UNIT, 1024);
+        };
+        if (ntile > 0) {
+            ok = warp_wait(q_full, 0);
+            wait_k(0);
             if (ok && elect_one()) {
-                for (int t = 0; t < 2; ++t)
-                    if (nt[t] > 0) scores(t, 0);
+                scores(0, u);
+                if (!split && nt[1] > 0) scores(1, u);
                 umma::commit(k_empty);
             }
             __syncwarp();
+            u = after(u, kc);
+            if (split) {
+                wait_k(1);
+                if (ok && elect_one()) {
+                    scores(1, u);
+                    umma::commit(k_empty + 1);
+                }
+                __syncwarp();
+                u = after(u, kc);
+            }
         }
-        for (int j = 0; j < ntile && ok; ++j) {
-            const int v0 = after(u, kc), v1 = vc == 2 ? after(v0, 1) : v0;  // values of tile j
-            u = after(v0, vc);                                             // keys of tile j + 1
-            const uint64_t dv =
-                sdesc_at(smem_addr(R + (uint32_t)min(v0, v1) * UNIT), (uint32_t)abs(v1 - v0) * UNIT, 1024);
-            ok = j < jf ? warp_wait(v_full + (j & 3), (uint32_t)(j >> 2) & 1u)
-                        : warp_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u);
-            bool k_in = false;
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (j >= nt[t]) continue;
-                ok = warp_wait(p_ready + t, (uint32_t)j & 1u);
+        if (split) {
+            for (int i = 0; i < ntile && ok; ++i) {
+                const int t = i & 1;
+                const uint64_t dv = take_v();
+                wait_v(i);
+                ok = ok && warp_wait(p_ready + t, (uint32_t)(i >> 1) & 1u);
                 if (!ok) break;
                 umma::fence_after();
                 if (elect_one()) {
-                    const uint32_t to = tmem + T_O + t * 128, tp = tmem + t * PK;
-#pragma unroll
-                    for (int k = 0; k < PK / 16; ++k)
-                        mma_ts(to, tp + k * 8, dv + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
-                    if (j + 1 == nt[t]) umma::commit(o_done + t);
-                    if (t == 1 || j >= nt[1]) umma::commit(v_empty + (j & 3));
+                    weigh(t, dv, i < 2, i + 2 >= ntile);
+                    umma::commit(v_empty + (i & 3));
                 }
                 __syncwarp();
-                if (j + 1 < nt[t]) {
-                    if (!k_in) {
-                        ok = warp_wait(k_full + ((j + 1) & 3), (uint32_t)((j + 1) >> 2) & 1u);
-                        if (!ok) break;
-                        umma::fence_after();
-                        k_in = true;
-                    }
+                if (i + 2 < ntile) {
+                    wait_k(i + 2);
+                    if (!ok) break;
                     if (elect_one()) {
                         scores(t, u);
-                        if (t == 1 || j + 1 >= nt[1]) umma::commit(k_empty + ((j + 1) & 3));
+                        umma::commit(k_empty + ((i + 2) & 3));
                     }
                     __syncwarp();
+                    u = after(u, kc);
                 }
+            }
+        } else {
+            for (int j = 0; j < ntile && ok; ++j) {
+                const uint64_t dv = take_v();
+                wait_v(j);
+                bool k_in = false;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j >= nt[t]) continue;
+                    ok = warp_wait(p_ready + t, (uint32_t)j & 1u);
+                    if (!ok) break;
+                    umma::fence_after();
+                    if (elect_one()) {
+                        weigh(t, dv, j == 0, j + 1 == nt[t]);
+                        if (t == 1 || j >= nt[1]) umma::commit(v_empty + (j & 3));
+                    }
+                    __syncwarp();
+                    if (j + 1 < nt[t]) {
+                        if (!k_in) {
+                            wait_k(j + 1);
+                            if (!ok) break;
+                            k_in = true;
+                        }
+                        if (elect_one()) {
+                            scores(t, u);
+                            if (t == 1 || j + 1 >= nt[1]) umma::commit(k_empty + ((j + 1) & 3));
+                        }
+                        __syncwarp();
+                    }
+                }
+                u = after(u, kc);
             }
         }
         if (__syncthreads_or(!ok)) {
@@ -232,8 +297,10 @@ __global__ void __launch_bounds__(PNT, 1)
         }
     } else if (warp == 10) {
         // ================================ value rows that not every query sees ================================
-        int u = (int)(((int64_t)jf * per + kc) % NU);  // ring position of the tile
-        for (int j = jf; j < ntile && ok; ++j, u = (u + per) % NU) {
+        for (int j = jf; j < ntile && ok; ++j) {
+            // V_j comes behind the first keys, V_0 .. V_j-1, and the keys between those
+            const int u = (int)(((int64_t)min(lead, ntile) * kc + (int64_t)j * vc + (int64_t)max(0, min(j, ntile - lead)) * kc) %
+                                NU);
             const int f = j - jf, valid = min(PK, nk - j * PK);
             ok = __all_sync(0xffffffffu, mbar_wait(v_raw + (f & 3), (uint32_t)(f >> 2) & 1u));
             if (!ok) break;
@@ -276,12 +343,12 @@ __global__ void __launch_bounds__(PNT, 1)
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + t * PK, to = tmem + lanes + T_O + t * 128;
-        const int i = qt + t * PQ + 32 * (warp & 3) + lane;  // this thread's query
+        const int i = qt + (split ? 0 : t * PQ) + 32 * (warp & 3) + lane;  // this thread's query
         const int lim = i < nq ? limit(i) : 0;
         const float c = a.scale * kLog2e, raise = kRaise / c;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < nt[t] && ok; ++j) {
-            ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, (uint32_t)j & 1u));
+            ok = warp_wait(s_full + t, (uint32_t)j & 1u);
             if (!ok) break;
             umma::fence_after();
             uint32_t s[4][32];
@@ -289,18 +356,9 @@ __global__ void __launch_bounds__(PNT, 1)
             for (int g = 0; g < 4; ++g) umma::ld32_issue(ts + 32 * g, s[g]);
 #pragma unroll
             for (int g = 0; g < 4; ++g) umma::wait_ld(s[g]);
-            if (j >= jf) {
-                const int left = lim - j * PK;  // keys of the tile that this query sees
-                ok = __all_sync(0xffffffffu, mbar_wait(fixed + ((j - jf) & 3), (uint32_t)((j - jf) >> 2) & 1u));
-                if (!ok) break;
-                if (any[(j - jf) & 3]) {
-                    const uint8_t *mk4 = mark + ((j - jf) & 3) * PK;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (mk4[32 * g + e]) s[g][e] = 0x7fffffffu;  // NaN
-                }
+            const int kt = split ? 2 * j + t : j;  // the key tile
+            const int left = lim - kt * PK;        // its keys that this query sees
+            if (kt >= jf && __any_sync(0xffffffffu, left < PK)) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -336,6 +394,19 @@ __global__ void __launch_bounds__(PNT, 1)
                 }
                 umma::wait_st();
             }
+            if (kt >= jf) {
+                const int f4 = (kt - jf) & 3;
+                ok = warp_wait(fixed + f4, (uint32_t)((kt - jf) >> 2) & 1u);
+                if (!ok) break;
+                if (any[f4]) {
+                    const uint8_t *mk4 = mark + f4 * PK;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * g + e < left && mk4[32 * g + e]) s[g][e] = 0x7fffffffu;  // NaN
+                }
+            }
             const float mc = m == -INFINITY ? 0.f : m * c;
             const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
             uint64_t sum[2] = {0, 0};
@@ -361,28 +432,56 @@ __global__ void __launch_bounds__(PNT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready + t);
         }
-        if (ok && nt[t] > 0) ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, 0));
+        if (nt[t] > 0) ok = ok && warp_wait(o_done + t, 0);
         umma::fence_after();
-        if (ok && qt + t * PQ + 32 * (warp & 3) < nq) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+        float share = 1.f;  // split: what the even and the odd key tiles' results count for in the whole
+        float other = 0.f;
+        if (split && ok) {
+            // every product is done once both o_done are, and so is every read of the ring
+            ok = warp_wait(o_done + (t ^ 1), 0);
+            umma::fence_after();
+            if (t == 1) {
+                half_ml[i - qt] = m;
+                half_ml[PQ + i - qt] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(half_done);
+            } else if (ok) {
+                ok = warp_wait(half_done, 0);
+                const float m1 = half_ml[i - qt], l1 = half_ml[PQ + i - qt], top = fmaxf(m, m1);
+                share = m == -INFINITY ? 0.f : exp2_((m - top) * c);
+                other = m1 == -INFINITY ? 0.f : exp2_((m1 - top) * c);
+                l = l * share + l1 * other;
+                m = top;
+            }
+        }
+        if (ok && !(split && t == 1) && i - lane < nq) {
+            const float inv = l == 0.f ? 0.f : 1.f / l, w0 = share * inv, w1 = other * inv;
             const int64_t row = (q_lo + i) * a.H + h;
             for (int k = 0; k < a.dv; k += 16) {
+                float v[16];
                 uint32_t o[16];
                 if (nt[t] > 0) {
                     umma::ld16_issue(to + k, o);
                     umma::wait_ld16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * w0;
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0;
+                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                }
+                if (split) {
+                    umma::ld16_issue(to + 128 + k, o);
+                    umma::wait_ld16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(o[e]) * w1;
                 }
                 if (i < nq) {
-                    uint32_t w[8];
+                    uint32_t pk[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = pack2<FP16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    for (int e = 0; e < 8; ++e) pk[e] = pack2<FP16>(v[2 * e], v[2 * e + 1]);
                     uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * a.dv + k);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
             }
             if (a.lse && i < nq) a.lse[row] = l == 0.f ? -INFINITY : (m * c + __log2f(l)) * kLn2;

@@ -512,6 +512,61 @@ def test_prefill_unseen_keys_and_values_may_hold_anything(value):
     assert bool(torch.isnan(p.out[149]).all())
 
 
+@pytest.mark.parametrize("nq,nk,dims", [(1, 129, (128, 64, 128)), (7, 1000, (64, 16, 64)), (100, 600, (128, 64, 128)),
+                                        (128, 128 * 9, (64, 32, 128)), (384, 2048, (128, 48, 64)), (257, 257, (64, 64, 64))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_few_queries_over_many_keys(nq, nk, dims, causal):
+    """A last query tile that stands alone: its even and odd key tiles are joined at the end."""
+    p = Prompt([nq, 3], [nk, 300], H=3, nope=dims[0], rope=dims[1], dv=dims[2], causal=causal, seed=nq + nk, dtype=FP)
+    p.run()
+    p.verify()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_prefill_few_queries_unseen_values_may_hold_anything(value):
+    p = Prompt([100, 50], [700, 333], H=2, seed=38)
+    p.run()
+    clean = p.out.clone()
+    p.v[650, 0, 7] = value           # queries 50.. of the first sequence see key 650
+    p.v[700 + 300, 1] = value        # queries 17.. of the second see its key 300
+    p.run()
+    keep = torch.ones(150, 2, dtype=torch.bool, device="cuda")
+    keep[50:100, 0] = keep[117:, 1] = False
+    assert torch.equal(p.out[keep], clean[keep])
+    assert bool((~torch.isfinite(p.out[50:100, 0, 7])).all()) and bool((~torch.isfinite(p.out[117:, 1])).all())
+
+
+def test_prefill_rising_maximum_over_alternating_key_tiles():
+    """Odd key tiles of 128 score far above the even ones (and the other way round): each half has its own maximum."""
+    for odd in (0, 1):
+        p = Prompt([60], [128 * 6 + 40], H=2, seed=39 + odd)
+        k = p.k.float().view(-1, 2, 128)
+        tile = (torch.arange(k.shape[0], device="cuda") // 128) % 2
+        p.k.copy_((k * torch.where(tile == odd, 6.0, 0.05)[:, None, None]).view_as(p.k))
+        p.run()
+        p.verify()
+
+
+@pytest.mark.parametrize("layout", ["head-major", "odd"])
+def test_prefill_and_decode_of_other_layouts(layout):
+    """[H, T, d] tensors, and strides that are multiples of 8 and of nothing else."""
+    def lay(x):
+        T, H, d = x.shape
+        if layout == "head-major":
+            y = torch.empty(H, T, d, dtype=x.dtype, device="cuda").transpose(0, 1)
+        else:
+            y = torch.empty(T * (H * (d + 8) + 24), dtype=x.dtype, device="cuda").as_strided((T, H, d),
+                                                                                        (H * (d + 8) + 24, d + 8, 1))
+        y.copy_(x)
+        return y
+    p = Prompt([200, 130], [300, 130], H=3, seed=44)
+    p.run(q=lay(p.q), k=lay(p.k), v=lay(p.v))
+    p.verify()
+    d = Problem([300, 41, 129], [2, 1, 4], H=6, rank=256, rope=64, seed=45)
+    d.run(q=lay(d.q))
+    d.verify()
+
+
 def test_prefill_one_bad_query_stays_alone():
     p = Prompt([300], [300], H=2, seed=33)
     p.run()
