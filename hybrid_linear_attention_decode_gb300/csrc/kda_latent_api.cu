@@ -1,7 +1,6 @@
 // kda_latent_api.cu -- the C ABI of the latent attention and page pool calls (include/kda.h): argument
 // validation and dispatch.  No allocation, no host synchronisation, no CUDA call before the checks pass.
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
 #include "../../include/kda.h"
@@ -81,6 +80,9 @@ int check_same(const LatentCacheArgs &c, const PageTableArgs &t) {
     return KDA_OK;
 }
 
+// The kernels work with scale * log2(e) and 8 / that; a NaN fails both comparisons.
+bool good_scale(float s) { return s > 0.f && s <= 1e30f; }
+
 bool bad_stride(int64_t s, int64_t least) { return s < least || s > kMaxStride || s % 8; }
 
 }  // namespace
@@ -146,12 +148,10 @@ int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, const kda_pa
     if (n < 0 || n > 65535 || num_tokens < 0 || max_tokens < 1 || max_tokens > KDA_LATENT_MAX_TOKENS || H < 1 ||
         H > KDA_LATENT_MAX_HEADS)
         return fail(KDA_ERR_INVALID_ARG, "latent decode: n, num_tokens, max_tokens or H out of range");
-    if (num_tokens > (int64_t)n * max_tokens && !cu_tokens)
-        return fail(KDA_ERR_INVALID_ARG, "latent decode: num_tokens differs from n * max_tokens without cu_tokens");
     if (!cu_tokens && num_tokens != (int64_t)n * max_tokens)
         return fail(KDA_ERR_INVALID_ARG, "latent decode: num_tokens differs from n * max_tokens without cu_tokens");
     if (num_tokens >= kMaxCount) return fail(KDA_ERR_INVALID_ARG, "latent decode: num_tokens out of range");
-    if (!(scale > 0.f) || !isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "latent decode: scale must be finite and > 0");
+    if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent decode: scale must be > 0 and at most 1e30");
     if (n == 0 || num_tokens == 0) return KDA_OK;
     if (!q || !out) return fail(KDA_ERR_INVALID_ARG, "latent decode: q or out is NULL");
     if (!al(q, 16) || !al(out, 16) || (lse && !al(lse, 4)) || (rows && !al(rows, 4)) ||
@@ -197,9 +197,9 @@ int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int
         return fail(KDA_ERR_UNSUPPORTED_SHAPE, "latent prefill: nope and dv must be 64 or 128 and rope a multiple of 16 "
                                                "up to 64");
     if (H < 1 || H > KDA_LATENT_MAX_HEADS || nseq < 0 || nseq > 65535 || num_q < 0 || num_q >= kMaxCount || num_k < 0 ||
-        num_k >= kMaxCount || max_q < 0)
+        num_k >= kMaxCount || max_q < 0 || max_q > 65535 * 256)
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: H, nseq, num_q, num_k or max_q out of range");
-    if (!(scale > 0.f) || !isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "latent prefill: scale must be finite and > 0");
+    if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent prefill: scale must be > 0 and at most 1e30");
     if (nseq == 0 || num_q == 0 || max_q == 0) return KDA_OK;
     if (!cu_q || !cu_k || !q || !out || (num_k > 0 && (!k_nope || !k_rope || !v)))
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: a required pointer is NULL");

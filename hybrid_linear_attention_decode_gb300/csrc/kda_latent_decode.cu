@@ -778,7 +778,7 @@ static Plan plan(int rank, int H, int n, int max_tokens) {
     q.groups = std::max(1, sms / q.nrt);
     q.slots_meta = std::min(n, q.groups);
     const size_t parts = (size_t)std::max(sms, q.nrt) * 2 * NR;  // whatever the row tiles: groups * nrt is no more
-    q.off_part = ((size_t)q.slots_meta * sizeof(Meta) + 255) / 256 * 256;
+    q.off_part = ((size_t)sms * sizeof(Meta) + 255) / 256 * 256;
     q.off_l = q.off_part + parts * rank * 4;
     q.bytes = q.off_l + parts * 4;
     return q;

@@ -307,7 +307,8 @@ KDA_API int kda_latent_append(const kda_latent_cache *cache, int32_t layer, cons
 #define KDA_LATENT_MAX_TOKENS 64
 #define KDA_LATENT_MAX_HEADS 128
 
-/* Bytes of device workspace kda_latent_decode needs on the current device for these sizes (0 for unsupported ones). */
+/* Bytes of device workspace kda_latent_decode needs on the current device for these sizes (0 for unsupported ones);
+ * what is enough for some n and max_tokens is enough for smaller ones, too. */
 KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, int32_t H, int32_t n,
                                                  int32_t max_tokens);
 
@@ -324,17 +325,20 @@ KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, 
  *   q          device [num_tokens][H][rank+rope], the cache's type, at the given token and head strides
  *              (elements, multiples of 8), 16-byte aligned
  *   tree_mask  device [num_tokens] uint64, or NULL
- *   scale      finite and > 0
+ *   scale      > 0 and at most 1e30
  *   out        device [num_tokens][H][rank] contiguous, the cache's type, 16-byte aligned
  *   lse        device [num_tokens][H] fp32: the natural logarithm of the sum of exp(s); or NULL
  * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so
  * do the queries of a sequence with a bad row or length (flagged; a bad page's tokens read as zero rows).  Sequences with
- * bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  What a cache row that no query of
- * its sequence sees holds (even NaN) does not matter; a query that sees a non-finite row gets NaN.
+ * bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Cache rows that a query does not see
+ * do not matter to it, whatever they hold (NaN too); a query that sees a non-finite row gets non-finite outputs,
+ * all NaN where that row is one of the nq tokens.
  * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product, outputs at
  * the end.  Results do not depend on the other sequences' contents, but a sequence's split over CTAs (and so
- * its last bits) depends on all lengths of the call.  The workspace keeps nothing between calls; calls that overlap on the GPU
- * need one each.  1 <= H <= KDA_LATENT_MAX_HEADS, max_tokens <= KDA_LATENT_MAX_TOKENS, n <= 65535.
+ * its last bits) depends on all lengths of the call and on the GPU's number of multiprocessors.  The workspace
+ * need not be initialised and keeps nothing between calls; calls that overlap on the GPU need one each.
+ * 1 <= H <= KDA_LATENT_MAX_HEADS, max_tokens <= KDA_LATENT_MAX_TOKENS, n <= 65535.  A wait that gives up sets
+ * KDA_DEV_TIMEOUT (outputs then are undefined).
  */
 KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, const kda_page_table *pt, int32_t n,
                               const int32_t *rows, const int32_t *cu_tokens, int64_t num_tokens, int32_t max_tokens,
@@ -345,7 +349,8 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
 /*
  * Expanded latent attention of nseq sequences' queries over their own keys: s = scale (q_nope . k_nope +
  * q_rope . r), o = softmax(s) v, per head, with one rotary key r for all heads.
- *   cu_q, cu_k  device [nseq+1] int32, non-decreasing from 0 to at most num_q / num_k; max_q bounds the queries of one sequence
+ *   cu_q, cu_k  device [nseq+1] int32, non-decreasing from 0 to at most num_q / num_k; max_q bounds the
+ *               queries of one sequence
  *   causal      1: query i of nq sees keys j <= i + nk - nq (the queries are the last nq tokens of nk, as when
  *               the beginning of the prompt is in the cache already); 0: all nk
  *   q           device [num_q][H][nope+rope]     k_nope  device [num_k][H][nope]
@@ -354,8 +359,10 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
  *               elements (multiples of 8), so k_nope and v may be the halves of one [num_k][H][nope+dv] tensor
  *   out         device [num_q][H][dv] contiguous, same type        lse  device [num_q][H] fp32, or NULL
  * A query that sees no key gets out 0 and lse -inf; sequences with bad tables (KDA_DEV_BAD_SEQLENS) and rows
- * behind cu_q[nseq] are left as they were.  Keys and values that a query does not see do not matter to it, even
- * NaN.  Supported: nope and dv in {64, 128}; rope a multiple of 16, 16 to 64.
+ * behind cu_q[nseq] are left as they were.  Keys and values that a query does not see do not matter to it,
+ * whatever they hold.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; the result of a query depends on its
+ * sequence alone.  Supported: nope and dv in {64, 128}; rope a multiple of 16, 16 to 64; scale > 0 and at most
+ * 1e30; max_q up to 65535 * 256.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
  */
 KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int32_t dv, int32_t nseq,
                                const int32_t *cu_q, const int32_t *cu_k, int64_t num_q, int64_t num_k, int32_t max_q,
@@ -369,7 +376,8 @@ KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t r
  * order, and new pages are always the lowest free ones of the pool as it was before the call, so that results
  * do not depend on timing.  An item with a bad row index or length, or whose row appears in an earlier item of
  * the call as well, is flagged (KDA_DEV_BAD_SLOT, _SEQLENS) and left out; so is one for which free pages do
- * not suffice (KDA_DEV_NO_PAGES; the demand of items before it counts whether they were served or not).  Row -1 = a padding item.
+ * not suffice (KDA_DEV_NO_PAGES; the demand of items before it counts whether they were served or not).  Row -1
+ * is a padding item.
  * Shared pages (refcount > 1) are never written.  cache (all layers) is what page copies apply to; its
  * page_size and num_pages have to be the table's.
  *
@@ -379,8 +387,8 @@ KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t r
  *                     pages behind them lose a reference, their entries become -1.
  * kda_pages_fork      the empty row children[i] becomes a copy of row parents[i] (a parent may have many
  *                     children): full pages are shared, a partly filled last page is copied into a new one.
- * kda_pages_compact   pages in use move into the lowest places, [0, pages in use): the i-th used page behind them (ascending)
- *                     moves into the i-th free one among them; tables and refcounts follow.
+ * kda_pages_compact   pages in use move into the lowest places, [0, pages in use): the i-th used page behind them
+ *                     (ascending) moves into the i-th free one among them; tables and refcounts follow.
  * kda_pages_copy      contents only, no bookkeeping: page dst[i] of every layer becomes page src[i] (-1 in
  *                     either: skipped; bad indices flagged).  No dst may repeat or be a src.
  *
@@ -460,7 +468,8 @@ KDA_API const char *kda_status_string(int status);
 
 /* What the last failing call of the calling host thread rejected ("decode: q, k, v, a and z must be
  * 16-byte aligned", "prefill launch: <CUDA error text>", ...), or "" when the last call of the thread to
- * kda_decode_step, kda_prefill_chunked(_noalloc), kda_resume_from_slot or kda_check_slots succeeded.  The
+ * kda_decode_step, kda_prefill_chunked(_noalloc), kda_resume_from_slot, kda_check_slots, a kda_latent_* or a
+ * kda_pages_* function succeeded.  The
  * string belongs to the library and stays valid until the thread's next such call.  Library-side record
  * only; nothing in the pages defines it. */
 KDA_API const char *kda_last_error_string(void);

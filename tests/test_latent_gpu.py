@@ -472,6 +472,20 @@ def test_prefill_long_sequence_sampled_heads():
     p.verify(heads=[0, 5])
 
 
+def test_prefill_of_a_sequence_does_not_depend_on_the_others():
+    p = Prompt([300, 90, 700], [300, 400, 1700], H=3, seed=46)
+    p.run()
+    q0 = k0 = 0
+    for n, m in zip(p.nq, p.nk):
+        out = torch.empty(n, 3, 128, dtype=p.dtype, device="cuda")
+        p.kda.kda_latent_prefill(_cu([n]), _cu([m]), n, p.q[q0:q0 + n], p.k[k0:k0 + m], p.r[k0:k0 + m], p.v[k0:k0 + m],
+                                 out, None, p.scale, p.status)
+        torch.cuda.synchronize()
+        assert torch.equal(out, p.out[q0:q0 + n])
+        q0 += n
+        k0 += m
+
+
 def test_prefill_strided_inputs_and_rows_behind_the_last_sequence():
     p = Prompt([140, 77], [240, 177], H=3, seed=31, extra_q=5, extra_k=9)
     Tq, Tk = p.q.shape[0], p.k.shape[0]
