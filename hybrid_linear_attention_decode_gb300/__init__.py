@@ -400,16 +400,19 @@ def _device_of(name: str, tensors) -> int:
 def _launch(fn, name: str, dev: int, stream, *args) -> None:
     """fn(*args, stream) on device `dev`, current or not, on its current stream unless one is given."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = _current_stream(dev)
     elif stream.device.index != dev:
         _raise(f"{name}: the stream belongs to another device")
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = fn(*args, stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, stream.cuda_stream)
-    if rc != KDA_OK:
+    if rc:
         raise KdaError(rc, name, kda_last_error_string())
+
+
+_current_stream, _current_device = torch.cuda.current_stream, torch.cuda.current_device
 
 
 def _int32(t, what: str, n: int | None = None):

@@ -197,7 +197,7 @@ int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int
         return fail(KDA_ERR_UNSUPPORTED_SHAPE, "latent prefill: nope and dv must be 64 or 128 and rope a multiple of 16 "
                                                "up to 64");
     if (H < 1 || H > KDA_LATENT_MAX_HEADS || nseq < 0 || nseq > 65535 || num_q < 0 || num_q >= kMaxCount || num_k < 0 ||
-        num_k >= kMaxCount || max_q < 0 || max_q > 65535 * 256)
+        num_k >= kMaxCount || max_q < 0 || max_q > KDA_LATENT_MAX_QUERIES)
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: H, nseq, num_q, num_k or max_q out of range");
     if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent prefill: scale must be > 0 and at most 1e30");
     if (nseq == 0 || num_q == 0 || max_q == 0) return KDA_OK;

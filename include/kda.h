@@ -346,6 +346,9 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
                               const uint64_t *tree_mask, float scale, void *out, float *lse, void *workspace,
                               size_t workspace_bytes, int32_t *dev_status, kda_stream_t stream);
 
+/* Most queries per sequence of one kda_latent_prefill call. */
+#define KDA_LATENT_MAX_QUERIES (1 << 23)
+
 /*
  * Expanded latent attention of nseq sequences' queries over their own keys: s = scale (q_nope . k_nope +
  * q_rope . r), o = softmax(s) v, per head, with one rotary key r for all heads.
@@ -360,9 +363,9 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
  *   out         device [num_q][H][dv] contiguous, same type        lse  device [num_q][H] fp32, or NULL
  * A query that sees no key gets out 0 and lse -inf; sequences with bad tables (KDA_DEV_BAD_SEQLENS) and rows
  * behind cu_q[nseq] are left as they were.  Keys and values that a query does not see do not matter to it,
- * whatever they hold.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; the result of a query depends on its
- * sequence alone.  Supported: nope and dv in {64, 128}; rope a multiple of 16, 16 to 64; scale > 0 and at most
- * 1e30; max_q up to 65535 * 256.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
+ * whatever they hold.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; a query's result depends on its
+ * sequence alone, its last bits also on H, nseq and max_q (they decide how the work is cut).  Supported: nope and dv in {64, 128}; rope a multiple of 16, 16 to 64; scale > 0 and at most
+ * 1e30; max_q up to KDA_LATENT_MAX_QUERIES.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
  */
 KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int32_t dv, int32_t nseq,
                                const int32_t *cu_q, const int32_t *cu_k, int64_t num_q, int64_t num_k, int32_t max_q,

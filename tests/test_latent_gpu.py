@@ -466,6 +466,59 @@ def test_prefill_matches_64_bits(case):
     p.verify()
 
 
+# The same with so many heads that a CTA has two query tiles (small calls have one)
+WIDE = [
+    # nq, nk, nope, rope, dv, dtype, causal
+    ([1, 2, 63, 64, 65], [1, 2, 63, 64, 65], 128, 64, 128, BF, True),
+    ([127, 128, 129, 255, 256, 257], [127, 128, 129, 255, 256, 257], 128, 64, 128, FP, True),
+    ([300, 511, 512, 513], [300, 511, 512, 513], 64, 32, 64, BF, True),
+    ([300, 140], [300, 900], 128, 48, 64, BF, False),
+    ([200, 10, 0, 290], [600, 0, 5, 20], 64, 16, 128, BF, True),
+    ([400, 385], [1111, 385], 128, 64, 128, FP, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_prefill_two_query_tiles_match_64_bits(case):
+    nq, nk, nope, rope, dv, dt, causal = WIDE[case]
+    p = Prompt(nq, nk, 96, nope, rope, dv, dt, causal, seed=100 + case)
+    p.run()
+    p.verify(heads=[0, 50, 95])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_prefill_two_query_tiles_unseen_keys_and_values_may_hold_anything(value):
+    p = Prompt([150, 100, 260], [150, 130, 460], H=96, seed=132)
+    p.run()
+    clean, clean_l = p.out.clone(), p.lse.clone()
+    p.v[120, 1, 3] = value           # queries 120.. of the first sequence see key 120
+    p.k[279, 7] = value              # only the second sequence's last query sees its last key
+    p.v[280 + 300, 90] = value       # queries 100.. of the third see its key 300
+    p.v[280 + 459, 40, 100] = value  # only its last query sees its last key
+    p.run()
+    keep = torch.ones(510, 96, dtype=torch.bool, device="cuda")
+    keep[120:150, 1] = keep[249, 7] = keep[350:, 90] = keep[509, 40] = False
+    assert torch.equal(p.out[keep], clean[keep]) and torch.equal(p.lse[keep], clean_l[keep])
+    assert bool((~torch.isfinite(p.out[120:150, 1, 3])).all()) and bool(torch.isnan(p.out[249, 7]).all())
+    assert bool((~torch.isfinite(p.out[350:, 90])).all()) and bool((~torch.isfinite(p.out[509, 40, 100])).all())
+
+
+def test_prefill_two_query_tiles_rising_maximum_and_bad_query():
+    p = Prompt([700], [700], H=96, seed=134)
+    ramp = torch.linspace(0.05, 1, 700, device="cuda")
+    p.k.copy_(p.k.float() * ramp[:, None, None])
+    p.r.copy_(p.r.float() * ramp[:, None])
+    p.scale = 1.5
+    p.run()
+    p.verify(heads=[3, 77])
+    clean = p.out.clone()
+    p.q[300, 5, 9] = float("nan")
+    p.run()
+    keep = torch.ones(700, 96, dtype=torch.bool, device="cuda")
+    keep[300, 5] = False
+    assert torch.equal(p.out[keep], clean[keep]) and bool(torch.isnan(p.out[300, 5]).all())
+
+
 def test_prefill_long_sequence_sampled_heads():
     p = Prompt([4500], [5000], H=6, seed=30)
     p.run()
@@ -473,11 +526,12 @@ def test_prefill_long_sequence_sampled_heads():
 
 
 def test_prefill_of_a_sequence_does_not_depend_on_the_others():
-    p = Prompt([300, 90, 700], [300, 400, 1700], H=3, seed=46)
+    """Bit for bit, where the call is cut alike (two query tiles a CTA in all of these, or one that stands alone)."""
+    p = Prompt([300, 90, 700], [300, 400, 1700], H=96, seed=46)
     p.run()
     q0 = k0 = 0
     for n, m in zip(p.nq, p.nk):
-        out = torch.empty(n, 3, 128, dtype=p.dtype, device="cuda")
+        out = torch.empty(n, 96, 128, dtype=p.dtype, device="cuda")
         p.kda.kda_latent_prefill(_cu([n]), _cu([m]), n, p.q[q0:q0 + n], p.k[k0:k0 + m], p.r[k0:k0 + m], p.v[k0:k0 + m],
                                  out, None, p.scale, p.status)
         torch.cuda.synchronize()
