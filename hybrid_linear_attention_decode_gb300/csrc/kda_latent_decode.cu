@@ -34,7 +34,7 @@ namespace latent {
 constexpr int TILE = 64;             // tokens per tile
 constexpr int NR = 64;               // rows (query, head) per CTA
 // Threads of the main kernel: 12 warps, the last two idle (registers come in warpgroups).  Launched with 168 registers a
-// thread (64,512 of 65,536); the softmax warpgroup takes 240, the others give down to 128: 63,488 in all.
+// thread (64,512 of 65,536); the softmax warpgroup takes 184, the others give down to 160: 128 * 184 + 256 * 160 = 64,512, what the launch holds.
 constexpr int NT = 384;
 constexpr int SW = 4;                // softmax warps
 // A sequence counts for this many tiles more where the list is split: ending one and beginning the next on a CTA costs
@@ -291,197 +291,199 @@ __global__ void __launch_bounds__(NT, 1)
     bool ok = true;
     auto read = [&](int b) { return seq_of(a, b); };
 
-    if (warp >= SW) asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
-    if (warp == 4) {
-        // ================================ producer ================================
-        // A box is 8 tokens with all their channels: 8 (rank + rope) 2 bytes in a row in the cache, whatever the page
-        // size.  (Boxes of 64 tokens x 64 channels, which read 128 bytes of each row at a time, reached 4.0 TB/s of DRAM.)
-        const int ps = a.c.page_size;
-        int it = 0, st = 0;
-        uint32_t ph = 1;  // a fresh ring is empty
-        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int, int64_t) {
-            const int32_t *trow = a.t.table + (int64_t)s.row * a.t.max_pages;
-            for (int j = 0; j < nt; ++j, ++it) {
-                const int key = (off + j) * TILE + (lane & 7) * 8;  // below 2^31: len is
-                int page = (int)a.c.num_pages;                      // a box outside the tensor reads as zeros
-                if (lane < 8 && key < s.len) {
-                    const int e = __ldg(trow + key / ps);
-                    if (e >= 0 && e < a.c.num_pages)
-                        page = e;
-                    else
-                        set_status(a.status, KDA_DEV_BAD_PAGE);
-                }
-                ok = it == 0 ? warp_wait(q_sent, 0) : it < nst || warp_wait(empty + st, ph);
-                if (!ok) return false;
-                if (lane == 0) mbar_arrive_expect_tx(full + st, STAGE);
-                __syncwarp();
-                if (lane < 8) {
-                    uint8_t *dst = KV + (uint32_t)st * STAGE + lane * GROUP;
-                    tma_load_4d(dst, &map_c, 0, key % ps, 0, page, full + st);
-                    if (p.split_rope) tma_load_3d(dst + rank / 64 * ATOM, &map_r, 0, key % ps, page, full + st);
-                }
-                if (++st == nst) st = 0, ph ^= 1;
-            }
-            return true;
-        });
-        if (__syncthreads_or(!ok)) {  // copies still in flight land before the CTA ends (short bounded waits)
-            for (int k = 0; k < min(it, nst); ++k) {
-                st = st ? st - 1 : nst - 1;
-                mbar_wait(full + st, (uint32_t)((it - 1 - k) / nst) & 1u, 10000000ull);
-            }
-        }
-    } else if (warp == 5) {
-        // ================================ MMA issuer ================================
-        const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
-        const uint32_t id_o = umma::idesc(kFmt<FP16>, 64, min(rank, 256)) | kBMajorMN;
-        const uint32_t id_o2 = umma::idesc(kFmt<FP16>, 64, max(rank - 256, 128)) | kBMajorMN;  // the rest of rank > 256
-        const uint64_t dp = umma::sdesc(smem_addr(P));
-        const uint64_t dx0 = sdesc_at(smem_addr(KV), 0, GROUP), dc0 = sdesc_at(smem_addr(KV), ATOM, GROUP);
-        const int ncr = rank / 64, kr = a.c.rope / 16;  // full chunks; instructions of the rotary chunk
-        const uint32_t stage_words = STAGE >> 4, k_words = 2 * GROUP >> 4;  // of a stage, of 16 tokens
-        uint32_t pieces = 0;
-        int it = 0, st = 0;  // tile whose P V comes next, and its stage
-        uint32_t ph = 0;     // parity of the stage's full barrier
-        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &, int32_t, int32_t nt, int, int64_t) {
-            ok = warp_wait(q_ready, pieces++ & 1u);
-            if (!ok) return false;
-            umma::fence_after();
-            auto issue_s = [&](int buf, int stage, bool last) {
-                if (!elect_one()) return;
-                const uint32_t ts = tmem + T_S + buf * TILE;
-                uint32_t tq = tmem;
-                uint64_t dx = dx0 + (uint64_t)(stage * stage_words);
-                for (int c = 0; c < ncr; ++c) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, k > 0 || c > 0);
-                    tq += 32;
-                    dx += ATOM >> 4;
-                }
-                if (kr == 4) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, true);
-                } else {
-                    for (int k = 0; k < kr; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, true);
-                }
-                umma::commit(s_full + buf);
-                if (last) umma::commit(q_free);  // this sequence's queries are read
-            };
-            bool issued = false;  // S of tile `it`
-            for (int j = 0; j < nt; ++j, ++it) {
-                if (!issued) {
-                    ok = warp_wait(full + st, ph);
+    if (warp >= SW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 160;");
+        if (warp == 4) {
+            // ================================ producer ================================
+            // A box is 8 tokens with all their channels: 8 (rank + rope) 2 bytes in a row in the cache, whatever the page
+            // size.  (Boxes of 64 tokens x 64 channels, which read 128 bytes of each row at a time, reached 4.0 TB/s of DRAM.)
+            const int ps = a.c.page_size;
+            int it = 0, st = 0;
+            uint32_t ph = 1;  // a fresh ring is empty
+            walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &s, int32_t off, int32_t nt, int, int64_t) {
+                const int32_t *trow = a.t.table + (int64_t)s.row * a.t.max_pages;
+                for (int j = 0; j < nt; ++j, ++it) {
+                    const int key = (off + j) * TILE + (lane & 7) * 8;  // below 2^31: len is
+                    int page = (int)a.c.num_pages;                      // a box outside the tensor reads as zeros
+                    if (lane < 8 && key < s.len) {
+                        const int e = __ldg(trow + key / ps);
+                        if (e >= 0 && e < a.c.num_pages)
+                            page = e;
+                        else
+                            set_status(a.status, KDA_DEV_BAD_PAGE);
+                    }
+                    ok = it == 0 ? warp_wait(q_sent, 0) : it < nst || warp_wait(empty + st, ph);
                     if (!ok) return false;
-                    umma::fence_after();
-                    issue_s(it & 1, st, j + 1 == nt);
-                }
-                const int st1 = st + 1 == nst ? 0 : st + 1;
-                const uint32_t ph1 = st1 ? ph : ph ^ 1u;
-                // whichever comes first: the weights of this tile, or the rows of the next
-                issued = false;
-                uint64_t t0 = 0;
-                for (uint32_t spin = 1; !__all_sync(0xffffffffu, mbar_test(p_ready, it & 1u)); ++spin) {
-                    if (!issued && j + 1 < nt && __all_sync(0xffffffffu, mbar_test(full + st1, ph1))) {
-                        umma::fence_after();
-                        issue_s((it + 1) & 1, st1, j + 2 == nt);
-                        issued = true;
+                    if (lane == 0) mbar_arrive_expect_tx(full + st, STAGE);
+                    __syncwarp();
+                    if (lane < 8) {
+                        uint8_t *dst = KV + (uint32_t)st * STAGE + lane * GROUP;
+                        tma_load_4d(dst, &map_c, 0, key % ps, 0, page, full + st);
+                        if (p.split_rope) tma_load_3d(dst + rank / 64 * ATOM, &map_r, 0, key % ps, page, full + st);
                     }
-                    if ((spin & 255u) == 0) {
-                        const uint64_t t = global_timer_ns();
-                        if (!t0) t0 = t;
-                        if (__any_sync(0xffffffffu, t - t0 > kWaitLimitNs)) {
-                            ok = false;
-                            return false;
-                        }
-                    }
+                    if (++st == nst) st = 0, ph ^= 1;
                 }
+                return true;
+            });
+            if (__syncthreads_or(!ok)) {  // copies still in flight land before the CTA ends (short bounded waits)
+                for (int k = 0; k < min(it, nst); ++k) {
+                    st = st ? st - 1 : nst - 1;
+                    mbar_wait(full + st, (uint32_t)((it - 1 - k) / nst) & 1u, 10000000ull);
+                }
+            }
+        } else if (warp == 5) {
+            // ================================ MMA issuer ================================
+            const uint32_t id_s = umma::idesc(kFmt<FP16>, 64, TILE);
+            const uint32_t id_o = umma::idesc(kFmt<FP16>, 64, min(rank, 256)) | kBMajorMN;
+            const uint32_t id_o2 = umma::idesc(kFmt<FP16>, 64, max(rank - 256, 128)) | kBMajorMN;  // the rest of rank > 256
+            const uint64_t dp = umma::sdesc(smem_addr(P));
+            const uint64_t dx0 = sdesc_at(smem_addr(KV), 0, GROUP), dc0 = sdesc_at(smem_addr(KV), ATOM, GROUP);
+            const int ncr = rank / 64, kr = a.c.rope / 16;  // full chunks; instructions of the rotary chunk
+            const uint32_t stage_words = STAGE >> 4, k_words = 2 * GROUP >> 4;  // of a stage, of 16 tokens
+            uint32_t pieces = 0;
+            int it = 0, st = 0;  // tile whose P V comes next, and its stage
+            uint32_t ph = 0;     // parity of the stage's full barrier
+            walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &, int32_t, int32_t nt, int, int64_t) {
+                ok = warp_wait(q_ready, pieces++ & 1u);
+                if (!ok) return false;
                 umma::fence_after();
-                if (elect_one()) {
-                    const uint64_t dc = dc0 + (uint64_t)(st * stage_words);
+                auto issue_s = [&](int buf, int stage, bool last) {
+                    if (!elect_one()) return;
+                    const uint32_t ts = tmem + T_S + buf * TILE;
+                    uint32_t tq = tmem;
+                    uint64_t dx = dx0 + (uint64_t)(stage * stage_words);
+                    for (int c = 0; c < ncr; ++c) {
 #pragma unroll
-                    for (int k = 0; k < TILE / 16; ++k)
-                        umma::mma_bf16(tmem + T_O, dp + 2 * k, dc + (uint64_t)(k * k_words), id_o, j > 0 || k > 0);
-                    if (rank > 256) {
-#pragma unroll
-                        for (int k = 0; k < TILE / 16; ++k)
-                            umma::mma_bf16(tmem + T_O + 256, dp + 2 * k, dc + (uint64_t)(k * k_words + (4 * ATOM >> 4)), id_o2,
-                                           j > 0 || k > 0);
+                        for (int k = 0; k < 4; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, k > 0 || c > 0);
+                        tq += 32;
+                        dx += ATOM >> 4;
                     }
-                    umma::commit(empty + st);  // O holds this tile, and its stage is free
-                }
-                __syncwarp();
-                st = st1;
-                ph = ph1;
-            }
-            return true;
-        });
-        if (__syncthreads_or(!ok)) {
-            if (elect_one()) umma::commit(drain);
-            mbar_wait(drain, 0, 10000000ull);
-        }
-    } else if (warp >= 10) {
-        __syncthreads_or(false);
-    } else if (warp >= 6) {
-        // ================================ queries ================================
-        const int w4 = warp & 3;                                 // quarter of the lanes
-        const uint32_t tq = tmem + ((uint32_t)(32 * w4) << 16);
-        uint32_t pieces = 0;
-        walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &s, int32_t, int32_t, int, int64_t) {
-            const int rows = min(NR, s.nq * H - rt * NR);
-            const int rw = rows_per_warp(rows), i0 = rw * w4 + (lane >> 2);  // this thread's rows: i0 and, if rw 16, i0 + 8
-            const uint2 *src[2];
+                    if (kr == 4) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = rt * NR + i0 + 8 * k, t = r / H, h = r - t * H;
-                src[k] = reinterpret_cast<const uint2 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs) + (lane & 3);
-            }
-            // Rounds of 128 channels (64 columns; this thread's 8-byte words 4n + lane % 4 of them), three rounds of loads in
-            // flight.  The first of them are sent before the first tile's copies: those fill the memory system's queues for
-            // microseconds, and no product can begin without the queries.
-            constexpr int RB = 3;
-            for (int ch0 = 0; ch0 < d; ch0 += 128 * RB) {
-                uint32_t v[RB][32];
-#pragma unroll
-                for (int u = 0; u < RB; ++u)
-#pragma unroll
-                    for (int n = 0; n < 8; ++n)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int ch = ch0 + 128 * u;
-                            uint2 x = make_uint2(0, 0);
-                            if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
-                            v[u][4 * n + 2 * k] = x.x;
-                            v[u][4 * n + 2 * k + 1] = x.y;
-                        }
-                if (ch0 == 0) {
-                    if (pieces == 0) {
-                        for (int ch = 128 * RB; ch < d; ch += 64)  // a line of each row in 16 lanes
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                if ((lane & 3) == 0 && 8 * k < rw && i0 + 8 * k < rows)
-                                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src[k] + ch / 4));
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(q_sent);
+                        for (int k = 0; k < 4; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, true);
                     } else {
-                        ok = warp_wait(q_free, (pieces - 1) & 1u);
+                        for (int k = 0; k < kr; ++k) mma_ts(ts, tq + 8 * k, dx + 2 * k, id_s, true);
+                    }
+                    umma::commit(s_full + buf);
+                    if (last) umma::commit(q_free);  // this sequence's queries are read
+                };
+                bool issued = false;  // S of tile `it`
+                for (int j = 0; j < nt; ++j, ++it) {
+                    if (!issued) {
+                        ok = warp_wait(full + st, ph);
                         if (!ok) return false;
                         umma::fence_after();
+                        issue_s(it & 1, st, j + 1 == nt);
                     }
-                }
+                    const int st1 = st + 1 == nst ? 0 : st + 1;
+                    const uint32_t ph1 = st1 ? ph : ph ^ 1u;
+                    // whichever comes first: the weights of this tile, or the rows of the next
+                    issued = false;
+                    uint64_t t0 = 0;
+                    for (uint32_t spin = 1; !__all_sync(0xffffffffu, mbar_test(p_ready, it & 1u)); ++spin) {
+                        if (!issued && j + 1 < nt && __all_sync(0xffffffffu, mbar_test(full + st1, ph1))) {
+                            umma::fence_after();
+                            issue_s((it + 1) & 1, st1, j + 2 == nt);
+                            issued = true;
+                        }
+                        if ((spin & 255u) == 0) {
+                            const uint64_t t = global_timer_ns();
+                            if (!t0) t0 = t;
+                            if (__any_sync(0xffffffffu, t - t0 > kWaitLimitNs)) {
+                                ok = false;
+                                return false;
+                            }
+                        }
+                    }
+                    umma::fence_after();
+                    if (elect_one()) {
+                        const uint64_t dc = dc0 + (uint64_t)(st * stage_words);
 #pragma unroll
-                for (int u = 0; u < RB; ++u)
-                    if (ch0 + 128 * u < d) st16x64_issue(tq + (ch0 + 128 * u) / 2, v[u]);
+                        for (int k = 0; k < TILE / 16; ++k)
+                            umma::mma_bf16(tmem + T_O, dp + 2 * k, dc + (uint64_t)(k * k_words), id_o, j > 0 || k > 0);
+                        if (rank > 256) {
+#pragma unroll
+                            for (int k = 0; k < TILE / 16; ++k)
+                                umma::mma_bf16(tmem + T_O + 256, dp + 2 * k, dc + (uint64_t)(k * k_words + (4 * ATOM >> 4)), id_o2,
+                                               j > 0 || k > 0);
+                        }
+                        umma::commit(empty + st);  // O holds this tile, and its stage is free
+                    }
+                    __syncwarp();
+                    st = st1;
+                    ph = ph1;
+                }
+                return true;
+            });
+            if (__syncthreads_or(!ok)) {
+                if (elect_one()) umma::commit(drain);
+                mbar_wait(drain, 0, 10000000ull);
             }
-            ++pieces;
-            umma::wait_st();
-            umma::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
-            return true;
-        });
-        __syncthreads_or(!ok);
+        } else if (warp >= 10) {
+            __syncthreads_or(false);
+        } else if (warp >= 6) {
+            // ================================ queries ================================
+            const int w4 = warp & 3;                                 // quarter of the lanes
+            const uint32_t tq = tmem + ((uint32_t)(32 * w4) << 16);
+            uint32_t pieces = 0;
+            walk(p, R.b, R.off, R.lo, R.hi, rt * NR, read, [&](int, const Seq &s, int32_t, int32_t, int, int64_t) {
+                const int rows = min(NR, s.nq * H - rt * NR);
+                const int rw = rows_per_warp(rows), i0 = rw * w4 + (lane >> 2);  // this thread's rows: i0 and, if rw 16, i0 + 8
+                const uint2 *src[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = rt * NR + i0 + 8 * k, t = r / H, h = r - t * H;
+                    src[k] = reinterpret_cast<const uint2 *>(a.q + (s.c0 + t) * a.q_ts + h * a.q_hs) + (lane & 3);
+                }
+                // Rounds of 128 channels (64 columns; this thread's 8-byte words 4n + lane % 4 of them), three rounds of loads in
+                // flight.  The first of them are sent before the first tile's copies: those fill the memory system's queues for
+                // microseconds, and no product can begin without the queries.
+                constexpr int RB = 3;
+                for (int ch0 = 0; ch0 < d; ch0 += 128 * RB) {
+                    uint32_t v[RB][32];
+#pragma unroll
+                    for (int u = 0; u < RB; ++u)
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int ch = ch0 + 128 * u;
+                                uint2 x = make_uint2(0, 0);
+                                if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
+                                v[u][4 * n + 2 * k] = x.x;
+                                v[u][4 * n + 2 * k + 1] = x.y;
+                            }
+                    if (ch0 == 0) {
+                        if (pieces == 0) {
+                            for (int ch = 128 * RB; ch < d; ch += 64)  // a line of each row in 16 lanes
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    if ((lane & 3) == 0 && 8 * k < rw && i0 + 8 * k < rows)
+                                        asm volatile("prefetch.global.L2 [%0];" ::"l"(src[k] + ch / 4));
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(q_sent);
+                        } else {
+                            ok = warp_wait(q_free, (pieces - 1) & 1u);
+                            if (!ok) return false;
+                            umma::fence_after();
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < RB; ++u)
+                        if (ch0 + 128 * u < d) st16x64_issue(tq + (ch0 + 128 * u) / 2, v[u]);
+                }
+                ++pieces;
+                umma::wait_st();
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
+                return true;
+            });
+            __syncthreads_or(!ok);
+        }
     } else {
         // ================================ softmax ================================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // These warps meet at named barriers, so they take every decision alike: one thread reads each sequence
         // for all, and a wait that gives up leads on through the same barriers (without further waits) to the end.
         auto read_once = [&](int b) {
@@ -539,13 +541,15 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                         for (int e = 0; e < TILE / 2; ++e) {
                             const int col = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), dr = key0 + col - base;
-                            if (dr >= 0) {
-                                if (dr >= 64 || !(see[(e >> 1) & 1] >> dr & 1))
-                                    sr[e] = 0xff800000u;  // -inf
-                                else if (scan_drafts && poison[col])
-                                    sr[e] = 0x7fffffffu;  // NaN
-                            }
+                            if (dr >= 0 && (dr >= 64 || !(see[(e >> 1) & 1] >> dr & 1))) sr[e] = 0xff800000u;  // -inf
                         }
+                        // a marked row that a query sees makes its sum, and so its whole output, NaN
+                        if (scan_drafts)
+                            for (int r = max(0, base - key0); r < min(TILE, s.len - key0); ++r)
+                                if (poison[r])
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k)
+                                        if (see[k] >> (key0 + r - base) & 1) l[k] = NAN;
                     }
                     float mx[2];
 #pragma unroll

@@ -13,7 +13,7 @@
 //            Where a CTA has one query tile (128 queries or fewer are left), the two are the same queries over the
 //            even and the odd key tiles, and the first one's warps join the results at the end.
 //   warp 10  value rows that a query of the CTA does not see: those behind the sequence become zeros, and
-//            those that are not finite too (0 x NaN is NaN), with a mark that makes the weights of the queries
+//            those that are not finite too (0 x NaN is NaN), with a mark that makes the sums of the queries
 //            that see them NaN.  Only tiles that some query sees in part need it.
 // Tensor memory: S0 S1 O0 O1, 128 columns each.  The running maximum is raised only by more than 2^8 (kRaise), by the
 // row's own thread in place.  Weights are rounded to the element type for the second product (its operands are
@@ -399,13 +399,10 @@ __global__ void __launch_bounds__(PNT, 1)
                 const int f4 = (kt - jf) & 3;
                 ok = warp_wait(fixed + f4, (uint32_t)((kt - jf) >> 2) & 1u);
                 if (!ok) break;
-                if (any[f4]) {
+                if (any[f4]) {  // a marked row that this query sees makes its sum, and so its whole output, NaN
                     const uint8_t *mk4 = mark + f4 * PK;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * g + e < left && mk4[32 * g + e]) s[g][e] = 0x7fffffffu;  // NaN
+                    for (int e = 0; e < min(left, PK); ++e)
+                        if (mk4[e]) l = NAN;
                 }
             }
             const float mc = m == -INFINITY ? 0.f : m * c;
