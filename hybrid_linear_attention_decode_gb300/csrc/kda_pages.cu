@@ -71,25 +71,24 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *part, int64_t 
     return before + s - v;
 }
 
-// Indices p in [lo, hi) with (refcount[p] <= 0) == want_free, ascending, into out; returns how many.
-__device__ int64_t select_pages(const int32_t *ref, int64_t lo, int64_t hi, bool want_free, int32_t *out,
-                                int64_t *part) {
-    int64_t have = 0;
-    for (int64_t base = lo; base < hi; base += PT * 4) {
-        const int64_t p0 = base + (int64_t)threadIdx.x * 4;
-        uint32_t m = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (p0 + u < hi && (ref[p0 + u] <= 0) == want_free) m |= 1u << u;
-        int64_t total;
-        int64_t at = have + block_scan(__popc(m), part, total);
-        if (out)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (m >> u & 1u) out[at++] = (int32_t)(p0 + u);
-        have += total;
-    }
-    return have;
+// f(p) for each page of a thread's run: the pages are dealt out in runs, so that one prefix sum over the threads places
+// them all in order.
+template <class F>
+__device__ __forceinline__ void each_page(int64_t num_pages, F f) {
+    const int64_t run = (num_pages + PT - 1) / PT, p0 = (int64_t)threadIdx.x * run, p1 = min(num_pages, p0 + run);
+#pragma unroll 4
+    for (int64_t p = p0; p < p1; ++p) f(p);
+}
+
+// The free pages, ascending, into list; returns how many.
+__device__ int64_t free_pages(const PageTableArgs &t, int32_t *list, int64_t *part) {
+    int64_t mine = 0, total;
+    each_page(t.num_pages, [&](int64_t p) { mine += t.refcount[p] <= 0; });
+    int64_t at = block_scan(mine, part, total);
+    each_page(t.num_pages, [&](int64_t p) {
+        if (t.refcount[p] <= 0) list[at++] = (int32_t)p;
+    });
+    return total;
 }
 
 __device__ __forceinline__ bool page_ok(const PageTableArgs &t, int32_t p) { return p >= 0 && p < t.num_pages; }
@@ -103,10 +102,23 @@ __global__ void __launch_bounds__(PT) kda_pages_plan_kernel(const PagesArgs a) {
     latent::allow_dependent_launch();
 
     if constexpr (OP == PAGES_COMPACT) {
-        const int64_t used = select_pages(t.refcount, 0, t.num_pages, false, nullptr, part);
-        const int64_t moves = select_pages(t.refcount, used, t.num_pages, false, w.src, part);
-        select_pages(t.refcount, 0, used, true, w.dst, part);  // as many: the used pages fill [0, used)
-        for (int64_t p = tid; p < t.num_pages; p += PT) w.list[p] = (int32_t)p;
+        int64_t mine = 0, used, moves;
+        each_page(t.num_pages, [&](int64_t p) { mine += t.refcount[p] > 0; });
+        block_scan(mine, part, used);
+        // used pages behind the first `used` places, and free ones among these: as many
+        mine = 0;
+        each_page(t.num_pages, [&](int64_t p) {
+            if (p >= used && t.refcount[p] > 0) ++mine;
+            if (p < used && t.refcount[p] <= 0) mine += (int64_t)1 << 32;
+        });
+        const int64_t at = block_scan(mine, part, moves);
+        moves &= 0xffffffff;
+        int64_t from = at & 0xffffffff, to = at >> 32;
+        each_page(t.num_pages, [&](int64_t p) {
+            w.list[p] = (int32_t)p;
+            if (p >= used && t.refcount[p] > 0) w.src[from++] = (int32_t)p;
+            if (p < used && t.refcount[p] <= 0) w.dst[to++] = (int32_t)p;
+        });
         __syncthreads();
         for (int64_t j = tid; j < moves; j += PT) {
             const int32_t s = __ldcg(w.src + j), d = __ldcg(w.dst + j);
@@ -126,7 +138,7 @@ __global__ void __launch_bounds__(PT) kda_pages_plan_kernel(const PagesArgs a) {
         const int32_t r = named[i];
         if (r >= 0 && r < t.max_seqs) atomicMin(w.claim + r, i);
     }
-    const int64_t nfree = OP == PAGES_TRUNCATE ? 0 : select_pages(t.refcount, 0, t.num_pages, true, w.list, part);
+    const int64_t nfree = OP == PAGES_TRUNCATE ? 0 : free_pages(t, w.list, part);
     __syncthreads();
     int64_t taken = 0;
     for (int base = 0; base < a.n; base += PT) {
