@@ -701,7 +701,10 @@ __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const Decod
     const int r = WIDE ? blockIdx.x : blockIdx.x * CW + warp, rt = r / NR, i = r - rt * NR;
     wait_for_previous();
     const Meta mt = p.meta[blockIdx.y];
-    if (mt.pieces < 2 || r >= mt.rows) return;
+    // A call whose waits gave up may leave records unwritten: nothing outside the workspace and the output is touched then.
+    if (mt.pieces < 2 || mt.group < 0 || mt.pieces > p.groups - mt.group || (mt.second | 1) != 1 || r >= mt.rows ||
+        mt.rows > p.nrt * NR || mt.row0 < 0 || mt.row0 > a.num_tokens * a.H - mt.rows)
+        return;
     float m = -INFINITY, l = 0.f;
     float4 acc[4];
 #pragma unroll

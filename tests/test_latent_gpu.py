@@ -526,13 +526,13 @@ def test_prefill_long_sequence_sampled_heads():
 
 
 def test_prefill_of_a_sequence_does_not_depend_on_the_others():
-    """Bit for bit, where the call is cut alike (two query tiles a CTA in all of these, or one that stands alone)."""
+    """Bit for bit, where the calls are cut alike (the same bound of 700 queries: two query tiles a CTA)."""
     p = Prompt([300, 90, 700], [300, 400, 1700], H=96, seed=46)
     p.run()
     q0 = k0 = 0
     for n, m in zip(p.nq, p.nk):
         out = torch.empty(n, 96, 128, dtype=p.dtype, device="cuda")
-        p.kda.kda_latent_prefill(_cu([n]), _cu([m]), n, p.q[q0:q0 + n], p.k[k0:k0 + m], p.r[k0:k0 + m], p.v[k0:k0 + m],
+        p.kda.kda_latent_prefill(_cu([n]), _cu([m]), 700, p.q[q0:q0 + n], p.k[k0:k0 + m], p.r[k0:k0 + m], p.v[k0:k0 + m],
                                  out, None, p.scale, p.status)
         torch.cuda.synchronize()
         assert torch.equal(out, p.out[q0:q0 + n])
