@@ -58,11 +58,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-template <bool FP16>
-__device__ __forceinline__ uint16_t to_elem(float x) {
-    return FP16 ? __half_as_ushort(__float2half_rn(x)) : f2bf(x);
-}
-
 // Looks for infinities and NaN, two elements an instruction: acc + x * 0 stays finite as long as every x was.
 template <bool FP16>
 __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc) {
@@ -90,10 +85,9 @@ __device__ __forceinline__ bool nonfinite(const uint32_t (&acc)[4]) {
     return bad;
 }
 
-// Instruction descriptor fields on top of umma::idesc(): 16-bit operand format, MN-major ("transposed") A or B.
+// Instruction descriptor fields on top of umma::idesc(): 16-bit operand format, MN-major ("transposed") B.
 template <bool FP16>
 constexpr int kFmt = FP16 ? 0 : umma::kBF16;
-constexpr uint32_t kAMajorMN = 1u << 15;
 constexpr uint32_t kBMajorMN = 1u << 16;
 
 // Descriptor of an operand in the 128-byte swizzle, whose atoms are 8 rows of 128 bytes.  K-major (rows = M or N, k
@@ -198,12 +192,6 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
         : "memory");
 }
-
-// 16 bytes global -> shared by this thread, asynchronously; cp_async_wait() waits for all it issued.
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");

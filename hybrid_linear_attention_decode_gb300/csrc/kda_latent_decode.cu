@@ -11,11 +11,11 @@
 // them from L2.  A sequence that a group holds whole is written at once; one that is cut
 // leaves normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
-// A tile, by one CTA of 10 warps (one CTA per SM, ring of tiles in shared memory):
+// A tile, by one CTA of 12 warps (one CTA per SM, ring of tiles in shared memory):
 //   warp 4   TMA: boxes of 8 tokens with all their channels, into K-major 128-byte-swizzled rows
 //   warp 5   S = Q X^T (M 64 rows, N 64 tokens, k = channel) and O += P C (M 64 rows, N 256 or 128 channels,
 //            k = token; C is the same shared memory, read MN-major).  With M 64 an accumulator has half of the
-//            tensor-memory lanes: O, rank columns wide, takes lanes 0-15 of each warp's quarter and S lanes 16-31.
+//            tensor-memory lanes: O, rank columns wide, takes lanes 16-31 of each warp's quarter, Q and S lanes 0-15.
 //            (The transposed product O^T += C^T P^T would leave no row of M unused, but an MN-major A operand
 //            of M 128, N 32 took 187 cycles an instruction; as B it takes 128 for N 256.)
 //   warps 6-9  the queries of the next sequence into tensor memory, as soon as the last S of this one is done
@@ -34,11 +34,12 @@ namespace latent {
 constexpr int TILE = 64;             // tokens per tile
 constexpr int NR = 64;               // rows (query, head) per CTA
 // Threads of the main kernel: 12 warps, the last two idle (registers come in warpgroups).  Launched with 168 registers a
-// thread (64,512 of 65,536); the softmax warpgroup takes 184, the others give down to 160: 128 * 184 + 256 * 160 = 64,512, what the launch holds.
+// thread (64,512 of 65,536); the softmax warpgroup takes 184, the others give down to 160: 128 * 184 + 256 * 160 = 64,512, what
+// the launch holds.  (With the roles unsplit the softmax spilled: 64 sequences 73.7 us instead of 71.0.)
 constexpr int NT = 384;
 constexpr int SW = 4;                // softmax warps
 // A sequence counts for this many tiles more where the list is split: ending one and beginning the next on a CTA costs
-// about as much time (64 sequences of 500 to 8192 tokens, 32 heads: 80.4 us without, 75.3 with 3, 72.7 with 5, 73.8 with 8).
+// about as much time (64 sequences of 500 to 8192 tokens, 32 heads, as measured then: 80.4 us without, 75.3 with 3, 72.7 with 5, 73.8 with 8).
 constexpr int START = 5;
 constexpr int QW = 4;                // query warps, one for each quarter of the lanes
 constexpr uint32_t ATOM = 1024;      // bytes of 8 tokens x 64 channels
@@ -254,8 +255,8 @@ __global__ void __launch_bounds__(NT, 1)
     uint64_t *q_sent = q_free + 1;
     uint64_t *drain = q_sent + 1;
     Scratch *scratch = reinterpret_cast<Scratch *>(drain + 1);
-    uint32_t *poison = reinterpret_cast<uint32_t *>(scratch + 1);  // [64] tile rows that are not finite
-    Seq *seq_s = reinterpret_cast<Seq *>(poison + 64);
+    uint32_t *poison = reinterpret_cast<uint32_t *>(scratch + 1);  // [2][TILE] rows that are not finite, by tile parity
+    Seq *seq_s = reinterpret_cast<Seq *>(poison + 2 * TILE);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(seq_s + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -525,10 +526,12 @@ __global__ void __launch_bounds__(NT, 1)
                 umma::fence_after();
                 const bool tail = key0 + TILE > base;
                 if (tail) {
+                    // marks of two tiles: a warp may be here while another still reads those of the tile before, but not
+                    // two tiles ahead, because P needs the products of the tile before, which need all warps' weights
                     wait(full + st, ph);
                     const int valid = min(TILE, s.len - key0);
                     fix_tile<FP16>(KV + (uint32_t)st * STAGE, GROUP, warp, lane, valid,
-                                   scan_drafts ? max(0, base - key0) : valid, rank / 8, nw, poison);
+                                   scan_drafts ? max(0, base - key0) : valid, rank / 8, nw, poison + (it & 1) * TILE);
                     softmax_sync();
                 }
                 uint32_t sr[32];  // 4n + i: row i0 + 8*(i/2), token 8n + 2*(lane%4) + i%2
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(NT, 1)
                         // a marked row that a query sees makes its sum, and so its whole output, NaN
                         if (scan_drafts)
                             for (int r = max(0, base - key0); r < min(TILE, s.len - key0); ++r)
-                                if (poison[r])
+                                if (poison[(it & 1) * TILE + r])
 #pragma unroll
                                     for (int k = 0; k < 2; ++k)
                                         if (see[k] >> (key0 + r - base) & 1) l[k] = NAN;

@@ -210,6 +210,29 @@ def test_decode_unseen_rows_may_hold_anything(value, page):
     assert bool(torch.isnan(p.out[last]).all())
 
 
+@pytest.mark.parametrize("before", [0, 7, 35, 64, 100])
+def test_decode_marks_of_drafts_in_two_tiles(before):
+    """60 drafted tokens over two tiles, each of which holds a row that is not finite; queries see both, one or none."""
+    p = Problem([before + 60], [60], H=48, rank=128, page=16, seed=before)
+    bad = (3, 59)
+    free = [j for j in range(60) if j not in bad]
+    masks = [sum(1 << j for j in free if j <= t or t in bad) | sum(1 << bad[i] for i in range(2) if t % 4 >> i & 1)
+             for t in range(60)]
+    tree = torch.tensor(masks, dtype=torch.int64, device="cuda")
+    none = torch.tensor([m & ~(1 << 3) & ~(1 << 59) for m in masks], dtype=torch.int64, device="cuda")
+    p.run(tree=none)
+    clean = p.out.clone()
+    for j in bad:
+        p.pages[0, int(p.pt.table[0, (before + j) // 16]), (before + j) % 16, 2] = float("nan")
+    for _ in range(20):
+        p.run(tree=tree)
+        for t in range(60):
+            if t % 4:
+                assert bool(torch.isnan(p.out[t]).all()), t
+            else:
+                assert torch.equal(p.out[t], clean[t]), t
+
+
 def test_decode_one_bad_query_stays_alone():
     p = Problem([150, 90], [2, 2], H=20, rank=128, seed=12)
     p.run()
