@@ -474,11 +474,11 @@ class LatentCache:
         return int(self.pages.shape[3]) - self.rank
 
     def c(self) -> _LatentCache:
-        """The C struct of the pages as they are now (kept while tensor, address and rank stay the same)."""
+        """The C struct of the pages as they are now (made again when anything that goes into it has changed)."""
         p = self.pages
-        key = (p, p.data_ptr(), self.rank)
+        key = (p.data_ptr(), p.shape, p.stride(), p.dtype, self.rank)
         kept = self.__dict__.get("_kept")
-        if kept is not None and kept[0][0] is p and kept[0][1:] == key[1:]:
+        if kept is not None and kept[0] == key:
             return kept[1]
         if p.dtype not in _ELEM:
             raise TypeError("latent cache dtype must be bfloat16 or float16")
@@ -506,17 +506,18 @@ class PageTable:
                          torch.zeros(num_pages, **i32), page_size)
 
     def c(self) -> _PageTable:
-        """The C struct of the tensors as they are now (kept while they and their addresses stay the same)."""
+        """The C struct of the tensors as they are now (made again when anything that goes into it has changed)."""
         t, n, r = self.table, self.lens, self.refcount
-        key = (t.data_ptr(), n.data_ptr(), r.data_ptr(), self.page_size)
+        key = (t.data_ptr(), t.shape, t.stride(), t.dtype, n.data_ptr(), n.shape, n.stride(), n.dtype, r.data_ptr(),
+               r.shape, r.stride(), r.dtype, self.page_size)
         kept = self.__dict__.get("_kept")
-        if kept is not None and kept[0] == key and kept[1] is t and kept[2] is n and kept[3] is r:
-            return kept[4]
+        if kept is not None and kept[0] == key:
+            return kept[1]
         _need(t.dtype == torch.int32 and t.dim() == 2 and t.is_contiguous(),
               "page table: table must be contiguous int32 [max_seqs, max_pages]")
         c = _PageTable(t.shape[0], t.shape[1], self.page_size, 0, r.shape[0], t.data_ptr(),
                        _int32(n, "page table: lens", int(t.shape[0])), _int32(r, "page table: refcount"))
-        self.__dict__["_kept"] = (key, t, n, r, c)
+        self.__dict__["_kept"] = (key, c)
         return c
 
 

@@ -62,8 +62,8 @@ int check_table(const kda_page_table *p, bool counts, PageTableArgs *o) {
     if (p->max_seqs < 1 || p->max_pages < 1 || p->page_size < 1 || p->page_size > 1024 || p->num_pages < 1 ||
         p->num_pages >= kMaxCount)
         return fail(KDA_ERR_INVALID_ARG, "page table: sizes out of range");
-    if ((int64_t)p->max_pages * p->page_size >= kMaxCount)
-        return fail(KDA_ERR_INVALID_ARG, "page table: max_pages * page_size must stay below 2^31 tokens");
+    if ((int64_t)p->max_pages * p->page_size > kMaxCount - 64)  // whole tiles of 64 tokens stay below 2^31
+        return fail(KDA_ERR_INVALID_ARG, "page table: max_pages * page_size must be at most 2^31 - 64 tokens");
     o->max_seqs = p->max_seqs;
     o->max_pages = p->max_pages;
     o->page_size = p->page_size;
@@ -80,8 +80,8 @@ int check_same(const LatentCacheArgs &c, const PageTableArgs &t) {
     return KDA_OK;
 }
 
-// The kernels work with scale * log2(e) and 8 / that; a NaN fails both comparisons.
-bool good_scale(float s) { return s > 0.f && s <= 1e30f; }
+// The kernels work with scale * log2(e) and 8 / that, both of which have to be normal numbers; a NaN fails both comparisons.
+bool good_scale(float s) { return s >= 1e-30f && s <= 1e30f; }
 
 bool bad_stride(int64_t s, int64_t least) { return s < least || s > kMaxStride || s % 8; }
 
@@ -151,7 +151,7 @@ int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, const kda_pa
     if (!cu_tokens && num_tokens != (int64_t)n * max_tokens)
         return fail(KDA_ERR_INVALID_ARG, "latent decode: num_tokens differs from n * max_tokens without cu_tokens");
     if (num_tokens >= kMaxCount) return fail(KDA_ERR_INVALID_ARG, "latent decode: num_tokens out of range");
-    if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent decode: scale must be > 0 and at most 1e30");
+    if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent decode: scale must be from 1e-30 to 1e30");
     if (n == 0 || num_tokens == 0) return KDA_OK;
     if (!q || !out) return fail(KDA_ERR_INVALID_ARG, "latent decode: q or out is NULL");
     if (!al(q, 16) || !al(out, 16) || (lse && !al(lse, 4)) || (rows && !al(rows, 4)) ||
@@ -197,9 +197,9 @@ int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int
         return fail(KDA_ERR_UNSUPPORTED_SHAPE, "latent prefill: nope and dv must be 64 or 128 and rope a multiple of 16 "
                                                "up to 64");
     if (H < 1 || H > KDA_LATENT_MAX_HEADS || nseq < 0 || nseq > 65535 || num_q < 0 || num_q >= kMaxCount || num_k < 0 ||
-        num_k >= kMaxCount || max_q < 0 || max_q > KDA_LATENT_MAX_QUERIES)
+        num_k > kMaxCount - 256 || max_q < 0 || max_q > KDA_LATENT_MAX_QUERIES)
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: H, nseq, num_q, num_k or max_q out of range");
-    if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent prefill: scale must be > 0 and at most 1e30");
+    if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent prefill: scale must be from 1e-30 to 1e30");
     if (nseq == 0 || num_q == 0 || max_q == 0) return KDA_OK;
     if (!cu_q || !cu_k || !q || !out || (num_k > 0 && (!k_nope || !k_rope || !v)))
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: a required pointer is NULL");

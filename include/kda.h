@@ -276,6 +276,7 @@ typedef struct kda_latent_cache {
  * Which pages hold which sequence: token j of table row s is row j % page_size of page
  * table[s][j / page_size], for j < lens[s].  refcount[p] counts the table rows that page p serves (0 = free);
  * only the kda_pages_* calls use it (it may be NULL for the others).  Entries behind a row's last page are not read.
+ * max_pages * page_size is at most 2^31 - 64 tokens.
  */
 typedef struct kda_page_table {
     int32_t max_seqs, max_pages;  /* rows, and entries of a row */
@@ -325,7 +326,7 @@ KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, 
  *   q          device [num_tokens][H][rank+rope], the cache's type, at the given token and head strides
  *              (elements, multiples of 8), 16-byte aligned
  *   tree_mask  device [num_tokens] uint64, or NULL
- *   scale      > 0 and at most 1e30
+ *   scale      from 1e-30 to 1e30
  *   out        device [num_tokens][H][rank] contiguous, the cache's type, 16-byte aligned
  *   lse        device [num_tokens][H] fp32: the natural logarithm of the sum of exp(s); or NULL
  * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so
@@ -352,8 +353,8 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
 /*
  * Expanded latent attention of nseq sequences' queries over their own keys: s = scale (q_nope . k_nope +
  * q_rope . r), o = softmax(s) v, per head, with one rotary key r for all heads.
- *   cu_q, cu_k  device [nseq+1] int32, non-decreasing from 0 to at most num_q / num_k; max_q bounds the
- *               queries of one sequence
+ *   cu_q, cu_k  device [nseq+1] int32, non-decreasing from 0 to at most num_q / num_k (num_k at most 2^31 - 256);
+ *               max_q bounds the queries of one sequence
  *   causal      1: query i of nq sees keys j <= i + nk - nq (the queries are the last nq tokens of nk, as when
  *               the beginning of the prompt is in the cache already); 0: all nk
  *   q           device [num_q][H][nope+rope]     k_nope  device [num_k][H][nope]
@@ -364,8 +365,9 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
  * A query that sees no key gets out 0 and lse -inf; sequences with bad tables (KDA_DEV_BAD_SEQLENS) and rows
  * behind cu_q[nseq] are left as they were.  Keys and values that a query does not see do not matter to it,
  * whatever they hold.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; a query's result depends on its
- * sequence alone, its last bits also on H, nseq and max_q (they decide how the work is cut).  Supported: nope and dv in {64, 128}; rope a multiple of 16, 16 to 64; scale > 0 and at most
- * 1e30; max_q up to KDA_LATENT_MAX_QUERIES.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
+ * sequence alone, its last bits also on H, nseq and max_q (they decide how the work is cut).  Supported: nope and
+ * dv in {64, 128}; rope a multiple of 16, 16 to 64; scale from 1e-30 to 1e30; max_q up to KDA_LATENT_MAX_QUERIES.
+ * A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
  */
 KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int32_t dv, int32_t nseq,
                                const int32_t *cu_q, const int32_t *cu_k, int64_t num_q, int64_t num_k, int32_t max_q,

@@ -149,3 +149,31 @@ def test_binding_refuses_cpu_tensors_types_and_shapes(lib):
     x = torch.zeros(5, 2, 8)[:, :1, :4]
     assert kda._rows_of(x, "x", torch.float32, (5, 1, 4))[1:] == (16, 4)
     assert kda._rows_of(x[:1], "x", torch.float32, (1, 1, 4))[1:] == (4, 4)
+
+
+def test_limits_of_scales_tokens_and_keys(lib):
+    for bad in (1e-31, 1e-45, 2e30):
+        assert decode(lib, scale=bad) == 1 and prefill(lib, scale=bad) == 1
+    # a table of 2^31 - 64 tokens at most, whatever the page size; too small a workspace is looked at after it
+    for size, most in ((16, (1 << 27) - 4), (64, (1 << 25) - 1), (1024, (1 << 21) - 1)):
+        c = cache(page_size=size, page_stride=size * 576, layer_stride=100 * size * 576)
+        assert decode(lib, c, table(page_size=size, max_pages=most), nbytes=0) == 3
+        assert decode(lib, c, table(page_size=size, max_pages=most + 1), nbytes=0) == 1
+    assert prefill(lib, num_k=(1 << 31) - 255) == 1 and "num_k" in kda.kda_last_error_string()
+
+
+def test_structs_follow_tensors_changed_in_place():
+    c = kda.LatentCache(torch.zeros(2, 4, 16, 144, dtype=torch.bfloat16), 128)
+    assert (c.c().layers, c.c().num_pages, c.c().layer_stride) == (2, 4, 4 * 16 * 144)
+    c.pages.transpose_(0, 1)
+    assert (c.c().layers, c.c().num_pages, c.c().layer_stride) == (4, 2, 16 * 144)
+    c.rank = 112
+    assert (c.c().rank, c.c().rope) == (112, 32)
+    t = kda.PageTable.empty(4, 6, 9, 16, device="cpu")
+    assert (t.c().max_seqs, t.c().max_pages) == (4, 6)
+    t.table.resize_(3, 8)
+    t.lens.resize_(3)
+    assert (t.c().max_seqs, t.c().max_pages) == (3, 8)
+    t.table.resize_(2, 8)
+    with pytest.raises(ValueError):
+        t.c()
