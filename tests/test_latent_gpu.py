@@ -338,6 +338,57 @@ def test_decode_on_a_side_stream_and_in_a_replayed_graph():
         p.verify()
 
 
+def test_decode_thousands_of_entries_mostly_padding():
+    """6000 entries, of which 37 have a sequence (some the same), of 0 to 900 tokens."""
+    lens = [0, 1, 900, 64, 129, 500, 65]
+    p = Problem(lens, [1] * len(lens), H=8, rank=128, seed=21)
+    n = 6000
+    at = list(range(0, n, 167)) + [n - 1]
+    rows = np.full(n, -1, np.int32)
+    rows[at] = np.arange(len(at)) % len(lens)
+    q = torch.zeros(n, 8, p.d, dtype=p.dtype, device="cuda")
+    q[at] = torch.randn(len(at), 8, p.d, device="cuda").to(p.dtype)
+    out, lse = torch.full((n, 8, 128), -7.0, dtype=p.dtype, device="cuda"), torch.full((n, 8), -7.0, device="cuda")
+    ws = torch.empty(p.kda.kda_latent_decode_workspace_bytes(p.cache, 8, n, 1), dtype=torch.uint8, device="cuda")
+    p.kda.kda_latent_decode(p.cache, 0, p.pt, _i32(rows), None, 1, q, out, lse, p.scale, ws, p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    for i in at:
+        kv = p.rows64(int(rows[i]))
+        seen = torch.ones(8, kv.shape[0], dtype=torch.bool, device="cuda")
+        o, l, to, tl = attend(q[i].to(F64), kv, kv[:, :128], seen, p.scale, p.dtype)
+        check(out[i], o, to, f"out of entry {i}")
+        check(lse[i], l, tl, f"lse of entry {i}")
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert bool((out[rest] == 0).all()) and bool((lse[rest] == -math.inf).all())
+
+
+def test_calls_on_two_streams_at_once():
+    """Decode, prefill and a second decode with its own workspace, queued on three streams, give what they give alone."""
+    a = Problem([3000, 70, 900], [2, 1, 4], H=32, rank=512, seed=22)
+    b = Problem([1200] * 9, [1] * 9, H=64, rank=256, seed=23)
+    c = Prompt([700, 90], [1500, 90], H=16, seed=24)
+    for x in (a, b, c):
+        x.run()
+    want = [(x.out.clone(), x.lse.clone()) for x in (a, b, c)]
+    ws = [torch.empty(x.kda.kda_latent_decode_workspace_bytes(x.cache, x.H, len(x.nq), max(x.nq)), dtype=torch.uint8,
+                      device="cuda") for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for x in (a, b, c):
+        x.out.fill_(-7)
+        x.lse.fill_(-7)
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for x, w, s in zip((a, b), ws, streams):
+            x.kda.kda_latent_decode(x.cache, 0, x.pt, None, x.cu, max(x.nq), x.q, x.out, x.lse, x.scale, w, x.status, stream=s)
+        c.kda.kda_latent_prefill(c.cu_q, c.cu_k, 700, c.q, c.k, c.r, c.v, c.out, c.lse, c.scale, c.status, stream=streams[2])
+    torch.cuda.synchronize()
+    for x, (out, lse) in zip((a, b, c), want):
+        assert int(x.status.item()) == 0
+        assert torch.equal(x.out, out) and torch.equal(x.lse, lse)
+
+
 def test_decode_rows_at_offsets_past_32_bits():
     """A cache of more than 2^32 bytes and 2^31 elements, read at its far end."""
     kda = _kda()
