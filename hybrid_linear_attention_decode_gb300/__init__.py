@@ -400,19 +400,24 @@ def _device_of(name: str, tensors) -> int:
 def _launch(fn, name: str, dev: int, stream, *args) -> None:
     """fn(*args, stream) on device `dev`, current or not, on its current stream unless one is given."""
     if stream is None:
-        stream = _current_stream(dev)
-    elif stream.device.index != dev:
+        handle = _raw_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
         _raise(f"{name}: the stream belongs to another device")
-    if _current_device() == dev:
-        rc = fn(*args, stream.cuda_stream)
+    if _get_device() == dev:
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, handle)
     if rc:
         raise KdaError(rc, name, kda_last_error_string())
 
 
-_current_stream, _current_device = torch.cuda.current_stream, torch.cuda.current_device
+# Handle of a device's current stream, and the current device: torch.cuda's functions of these names make objects of them, at
+# 1.0 and 0.25 us a call (0.1 both here); CUDA is running by then, because the call's tensors are on it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _int32(t, what: str, n: int | None = None):
