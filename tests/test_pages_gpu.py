@@ -100,7 +100,7 @@ def test_shared_last_page_is_copied_before_it_grows():
 
 
 def test_sizes_beyond_one_plan_sweep():
-    """More pages than one sweep of the plan CTA (4096) and more items than its threads."""
+    """Several pages and more than one item for each thread of the plan CTA (1024)."""
     b = Both(1500, 12, 9000, 16, layers=1, rank=128, rope=0, items=1500)
     rng = np.random.default_rng(0)
     lens = rng.integers(0, 100, 1500).tolist()
