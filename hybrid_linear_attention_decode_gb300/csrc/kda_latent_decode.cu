@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(NT, 1)
     }
 
     umma::fence_before();
+    wait_for_previous();
     const Range R = group_range(p, g, rt == 0, scratch);
     umma::fence_after();
     const uint32_t tmem = *tmem_s;
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(CW * 32) kda_latent_combine_kernel(const Decod
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.c.rank, nv = rank / 128;
     const int r = WIDE ? blockIdx.x : blockIdx.x * CW + warp, rt = r / NR, i = r - rt * NR;
     wait_for_previous();
+    allow_dependent_launch();
     const Meta mt = p.meta[blockIdx.y];
     // A call whose waits gave up may leave records unwritten: nothing outside the workspace and the output is touched then.
     if (mt.pieces < 2 || mt.group < 0 || mt.pieces > p.groups - mt.group || (mt.second | 1) != 1 || r >= mt.rows ||
@@ -833,15 +835,15 @@ static int launch(const LatentDecodeArgs &a, const Plan &q, cudaStream_t st) {
     const uint32_t fixed = 1024 + NR * 128 + MISC;
     p.nst = std::min<int>(MAX_STAGES, (SMEM_MAX - fixed) / stage);
     const uint32_t smem = fixed + p.nst * stage;
-    kda_latent_decode_kernel<FP16><<<q.groups * q.nrt, NT, smem, st>>>(p, map_c, map_r);
+    dependent_launch(kda_latent_decode_kernel<FP16>, dim3(q.groups * q.nrt), NT, smem, st, p, map_c, map_r);
     const int rc = launch_result("kda_latent_decode_kernel launch");
     if (rc != KDA_OK) return rc;
     const int rows = a.H * a.max_tokens;
     if (q.groups > CW * a.n)  // a sequence is cut into about groups / n parts
-        dependent_launch(kda_latent_combine_kernel<FP16, true>, dim3(rows, q.slots_meta), CW * 32, st, p);
+        dependent_launch(kda_latent_combine_kernel<FP16, true>, dim3(rows, q.slots_meta), CW * 32, 0, st, p);
     else
-        dependent_launch(kda_latent_combine_kernel<FP16, false>, dim3((rows + CW - 1) / CW, q.slots_meta), CW * 32, st,
-                         p);
+        dependent_launch(kda_latent_combine_kernel<FP16, false>, dim3((rows + CW - 1) / CW, q.slots_meta), CW * 32, 0,
+                         st, p);
     return launch_result("kda_latent_combine_kernel launch");
 }
 

@@ -45,6 +45,8 @@ __global__ void __launch_bounds__(PNT, 1)
     kda_latent_prefill_kernel(const PrefillP p, const __grid_constant__ CUtensorMap mq,
                               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
                               const __grid_constant__ CUtensorMap mv) {
+    wait_for_previous();
+    allow_dependent_launch();
     const LatentPrefillArgs &a = p.a;
     const int h = blockIdx.x, b = blockIdx.y;
     const int64_t q_lo = a.cu_q[b], q_hi = a.cu_q[b + 1], k_lo = a.cu_k[b], k_hi = a.cu_k[b + 1];
@@ -520,7 +522,7 @@ static int launch(const LatentPrefillArgs &a, cudaStream_t st) {
     p.units = std::min<int>(MAX_UNITS, (PSMEM_MAX - fixed) / UNIT);
     const int rows = ONE ? PQ : 2 * PQ;
     const dim3 grid(a.H, a.nseq, (a.max_q + rows - 1) / rows);
-    kda_latent_prefill_kernel<FP16, ONE><<<grid, PNT, fixed + p.units * UNIT, st>>>(p, mq, mk, mr, mv);
+    dependent_launch(kda_latent_prefill_kernel<FP16, ONE>, grid, PNT, fixed + p.units * UNIT, st, p, mq, mk, mr, mv);
     return launch_result("kda_latent_prefill_kernel launch");
 }
 

@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(PT) kda_pages_plan_kernel(const PagesArgs a) {
     const PageTableArgs &t = a.t;
     const Ws w = layout(a.ws, t.max_seqs, t.num_pages, a.n);
     const int tid = threadIdx.x;
+    latent::wait_for_previous();
     latent::allow_dependent_launch();
 
     if constexpr (OP == PAGES_COMPACT) {
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(AT) kda_pages_apply_kernel(const PagesArgs a) 
     const int ps = t.page_size;
     const int tid = threadIdx.x;
     latent::wait_for_previous();  // for the plan
+    latent::allow_dependent_launch();
     if constexpr (OP == PAGES_COMPACT) {
         for (int s = blockIdx.x; s < t.max_seqs; s += gridDim.x) {
             const int64_t len = t.lens[s], have = (len + ps - 1) / ps;
@@ -304,11 +306,15 @@ __global__ void __launch_bounds__(AT) kda_pages_apply_kernel(const PagesArgs a) 
 
 __global__ void __launch_bounds__(AT) kda_pages_copy_kernel(const LatentCacheArgs c, int32_t n, const int32_t *src,
                                                             const int32_t *dst, int32_t *status) {
+    latent::wait_for_previous();
+    latent::allow_dependent_launch();
     copy_pages(c, n, src, dst, status);
 }
 
 // One warp a token: its sequence by a 32-way search of cu_tokens, then 16-byte copies of its row.
 __global__ void __launch_bounds__(AT) kda_latent_append_kernel(const AppendArgs a) {
+    latent::wait_for_previous();
+    latent::allow_dependent_launch();
     const int lane = threadIdx.x & 31;
     const int64_t tok = (int64_t)blockIdx.x * (AT / 32) + (threadIdx.x >> 5);
     if (tok >= a.num_tokens) return;
@@ -378,11 +384,11 @@ size_t pages_workspace_bytes(int32_t max_seqs, int64_t num_pages, int32_t n) {
 template <int OP>
 static int launch_pages_op(const PagesArgs &a, cudaStream_t st) {
     using namespace pages;
-    kda_pages_plan_kernel<OP><<<1, PT, 0, st>>>(a);
+    latent::dependent_launch(kda_pages_plan_kernel<OP>, dim3(1), PT, 0, st, a);
     const int rc = launch_result("kda_pages_plan_kernel launch");
     if (rc != KDA_OK) return rc;
     // eight CTAs a multiprocessor are resident; how much there is to copy is known on the device alone
-    latent::dependent_launch(kda_pages_apply_kernel<OP>, dim3((unsigned)current_device_sms() * 8), AT, st, a);
+    latent::dependent_launch(kda_pages_apply_kernel<OP>, dim3((unsigned)current_device_sms() * 8), AT, 0, st, a);
     return launch_result("kda_pages_apply_kernel launch");
 }
 
@@ -398,14 +404,15 @@ int launch_pages(PageOp op, const PagesArgs &a, cudaStream_t st) {
 int launch_pages_copy(const LatentCacheArgs &c, int32_t n, const int32_t *src, const int32_t *dst, int32_t *status,
                       cudaStream_t st) {
     using namespace pages;
-    kda_pages_copy_kernel<<<(unsigned)current_device_sms() * 8, AT, 0, st>>>(c, n, src, dst, status);
+    latent::dependent_launch(kda_pages_copy_kernel, dim3((unsigned)current_device_sms() * 8), AT, 0, st, c, n, src, dst,
+                             status);
     return launch_result("kda_pages_copy_kernel launch");
 }
 
 int launch_latent_append(const AppendArgs &a, cudaStream_t st) {
     using namespace pages;
     const int64_t blocks = (a.num_tokens + AT / 32 - 1) / (AT / 32);
-    kda_latent_append_kernel<<<(unsigned)blocks, AT, 0, st>>>(a);
+    latent::dependent_launch(kda_latent_append_kernel, dim3((unsigned)blocks), AT, 0, st, a);
     return launch_result("kda_latent_append_kernel launch");
 }
 
