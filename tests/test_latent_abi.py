@@ -160,6 +160,9 @@ def test_limits_of_scales_tokens_and_keys(lib):
         assert decode(lib, c, table(page_size=size, max_pages=most), nbytes=0) == 3
         assert decode(lib, c, table(page_size=size, max_pages=most + 1), nbytes=0) == 1
     assert prefill(lib, num_k=(1 << 31) - 255) == 1 and "num_k" in kda.kda_last_error_string()
+    big = dict(H=128, nseq=65535, num_q=1 << 22)
+    assert prefill(lib, max_q=2049, **big) == 1 and "2^26" in kda.kda_last_error_string()
+    assert prefill(lib, max_q=2048, out=None, **big) == 1 and "2^26" not in kda.kda_last_error_string()
 
 
 def test_structs_follow_tensors_changed_in_place():
