@@ -202,10 +202,9 @@ int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int
         num_k > kMaxCount - 256 || max_q < 0 || max_q > KDA_LATENT_MAX_QUERIES)
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: H, nseq, num_q, num_k or max_q out of range");
     if (!good_scale(scale)) return fail(KDA_ERR_INVALID_ARG, "latent prefill: scale must be from 1e-30 to 1e30");
-    max_q = (int32_t)std::min<int64_t>(max_q, num_q);
     // a CTA for each tile of queries that a sequence may have, most of them ended at once where max_q is far above the
     // others' lengths: 250 a microsecond, so a quarter of a second for these
-    if ((int64_t)H * nseq * ((max_q + 255) / 256) > (int64_t)1 << 26)
+    if ((int64_t)H * nseq * ((std::min<int64_t>(max_q, num_q) + 255) / 256) > (int64_t)1 << 26)
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: H * nseq * ceil(max_q / 256) must be at most 2^26");
     if (nseq == 0 || num_q == 0 || max_q == 0) return KDA_OK;
     if (!cu_q || !cu_k || !q || !out || (num_k > 0 && (!k_nope || !k_rope || !v)))

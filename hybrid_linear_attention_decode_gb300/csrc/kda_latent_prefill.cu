@@ -521,7 +521,8 @@ static int launch(const LatentPrefillArgs &a, cudaStream_t st) {
     const uint32_t kc = a.nope / 64 + 1, fixed = 1024 + 2 * kc * UNIT + PMISC;
     p.units = std::min<int>(MAX_UNITS, (PSMEM_MAX - fixed) / UNIT);
     const int rows = ONE ? PQ : 2 * PQ;
-    const dim3 grid(a.H, a.nseq, (a.max_q + rows - 1) / rows);
+    const int most = (int)std::min<int64_t>(a.max_q, a.num_q);  // no sequence has more
+    const dim3 grid(a.H, a.nseq, (most + rows - 1) / rows);
     dependent_launch(kda_latent_prefill_kernel<FP16, ONE>, grid, PNT, fixed + p.units * UNIT, st, p, mq, mk, mr, mv);
     return launch_result("kda_latent_prefill_kernel launch");
 }

@@ -354,7 +354,8 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
  * Expanded latent attention of nseq sequences' queries over their own keys: s = scale (q_nope . k_nope +
  * q_rope . r), o = softmax(s) v, per head, with one rotary key r for all heads.
  *   cu_q, cu_k  device [nseq+1] int32, non-decreasing from 0 to at most num_q / num_k (num_k at most 2^31 - 256);
- *               max_q bounds the queries of one sequence (H * nseq * ceil(max_q / 256) at most 2^26)
+ *               max_q bounds the queries of one sequence (H * nseq * ceil(min(max_q, num_q) / 256) at
+ *               most 2^26)
  *   causal      1: query i of nq sees keys j <= i + nk - nq (the queries are the last nq tokens of nk, as when
  *               the beginning of the prompt is in the cache already); 0: all nk
  *   q           device [num_q][H][nope+rope]     k_nope  device [num_k][H][nope]
