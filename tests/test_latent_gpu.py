@@ -389,6 +389,57 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(x.out, out) and torch.equal(x.lse, lse)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_ordered_by_events_across_streams(captured):
+    """Rows appended on one stream, read by decodes of two layers on two streams, which a third call waits for."""
+    kda = _kda()
+    lens = [700, 64, 1]
+    p = Problem(lens, [1, 1, 1], H=32, rank=512, layers=2, seed=25)
+    old = p.pages.clone()
+    new = torch.randn(2, 3, p.d, device="cuda").to(p.dtype)
+    cu = _cu([1, 1, 1])
+    out = torch.zeros(2, 3, 32, 512, dtype=p.dtype, device="cuda")
+    lse = torch.zeros(2, 3, 32, device="cuda")
+    ws = [torch.empty(kda.kda_latent_decode_workspace_bytes(p.cache, 32, 3, 1), dtype=torch.uint8, device="cuda")
+          for _ in range(2)]
+    last = torch.tensor([int(p.pt.table[b, (n - 1) // 64]) for b, n in enumerate(lens)])
+    src, dst = _i32([int(last[0])]), _i32([min(set(range(p.pages.shape[1])) - p.used)])
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        for layer in range(2):
+            kda.kda_latent_append(p.cache, layer, p.pt, None, cu, new[layer, :, :512], new[layer, :, 512:], p.status)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kda.kda_latent_decode(p.cache, 1, p.pt, None, cu, 1, p.q, out[1], lse[1], p.scale, ws[1], p.status)
+        kda.kda_latent_decode(p.cache, 0, p.pt, None, cu, 1, p.q, out[0], lse[0], p.scale, ws[0], p.status)
+        main.wait_stream(side)
+        kda.kda_pages_copy(p.cache, src, dst, p.status)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    if captured:
+        with torch.cuda.graph(g):
+            step()
+    for k in range(6):
+        p.pages.copy_(old)
+        new.copy_(torch.randn(2, 3, p.d, device="cuda"))
+        out.zero_()
+        g.replay() if captured else step()
+        torch.cuda.synchronize()
+        assert int(p.status.item()) == 0
+        assert torch.equal(p.pages[:, int(dst)], p.pages[:, int(src)])
+        for layer in range(2):
+            p.layer = layer
+            for b, n in enumerate(lens):
+                assert torch.equal(p.pages[layer, int(last[b]), (n - 1) % 64], new[layer, b])
+                o, l, to, tl = p.expect(b)
+                check(out[layer, b:b + 1], o, to, f"step {k}, layer {layer}, sequence {b}")
+                check(lse[layer, b:b + 1], l, tl)
+
+
 def test_decode_rows_at_offsets_past_32_bits():
     """A cache of more than 2^32 bytes and 2^31 elements, read at its far end."""
     kda = _kda()
