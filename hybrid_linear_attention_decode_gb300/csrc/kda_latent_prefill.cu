@@ -46,7 +46,6 @@ __global__ void __launch_bounds__(PNT, 1)
                               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
                               const __grid_constant__ CUtensorMap mv) {
     wait_for_previous();
-    allow_dependent_launch();
     const LatentPrefillArgs &a = p.a;
     const int h = blockIdx.x, b = blockIdx.y;
     const int64_t q_lo = a.cu_q[b], q_hi = a.cu_q[b + 1], k_lo = a.cu_k[b], k_hi = a.cu_k[b + 1];
@@ -106,6 +105,7 @@ __global__ void __launch_bounds__(PNT, 1)
     __syncthreads();
     umma::fence_after();
     const uint32_t tmem = *tmem_s;
+    allow_dependent_launch();  // with its tensor memory in hand: a CTA that waits may hold some itself
     constexpr uint32_t T_O = 2 * PK;
     bool ok = true;
 
