@@ -82,7 +82,7 @@ int check_same(const LatentCacheArgs &c, const PageTableArgs &t) {
     return KDA_OK;
 }
 
-// The kernels work with scale * log2(e) and 8 / that, both of which have to be normal numbers; a NaN fails both comparisons.
+// The kernels work with scale * log2(e) and 6 or 8 / that, which have to be normal numbers; a NaN fails both comparisons.
 bool good_scale(float s) { return s >= 1e-30f && s <= 1e30f; }
 
 bool bad_stride(int64_t s, int64_t least) { return s < least || s > kMaxStride || s % 8; }

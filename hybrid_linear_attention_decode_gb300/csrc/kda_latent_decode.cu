@@ -21,9 +21,9 @@
 //   warps 6-9  the queries of the next sequence into tensor memory, as soon as the last S of this one is done
 //   warps 0-3  softmax of S (8 or 16 rows a warp, a quad of threads a row), P to shared memory, and at the end O out.
 // S of a tile is issued before P V of the one before, so the softmax overlaps the products.
-// The running maximum is raised only by more than 2^8 (kRaise); then its warp rescales the rows of O in place.
-// Weights P are rounded to the element type for the second product (its operands are 16-bit); their sum is
-// kept in fp32 from the unrounded weights.
+// The running maximum is raised only by more than kRaise; then its warp rescales the rows of O in place.
+// Weights P are rounded to the element type for the second product (its operands are 16-bit), in fp16 moved up by
+// 2^kBias; their sum is kept in fp32 from the unrounded weights.
 #include <algorithm>
 
 #include "kda_latent.cuh"
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(NT, 1)
         };
         auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity)); };
         const uint32_t quad = tmem + ((uint32_t)(32 * warp) << 16);
-        const float c = a.scale * kLog2e, raise = kRaise / c;
+        const float c = a.scale * kLog2e, raise = kRaise<FP16> / c;
         const int nw = d / 8;
         int it = 0;
         int st_prev = 0;          // stage and parity of the empty barrier of tile it - 1
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         if (k >= nk) break;
-                        const float mc = m[k] == -INFINITY ? 0.f : m[k] * c;
-                        const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+                        const float up = m[k] == -INFINITY ? 0.f : fmaf(-m[k], c, kBias<FP16>);
+                        const uint64_t c2 = pair(c, c), up2 = pair(up, up);
                         const int i = i0p + 8 * k;
                         uint8_t *prow = P + i * 128 + 4 * (lane & 3);
                         uint64_t sum = 0;
@@ -614,12 +614,12 @@ __global__ void __launch_bounds__(NT, 1)
                         for (int n = 0; n < TILE / 8; ++n) {
                             float p0, p1;
                             unpair(fma2(pair(__uint_as_float(sr[4 * n + 2 * k]), __uint_as_float(sr[4 * n + 2 * k + 1])), c2,
-                                        mc2),
+                                        up2),
                                    p0, p1);
                             p0 = exp2_(p0);
                             p1 = exp2_(p1);
                             sum = add2(sum, pair(p0, p1));
-                            *reinterpret_cast<uint32_t *>(prow + (((n ^ i) & 7) << 4)) = pack2<FP16>(p0, p1);
+                            *reinterpret_cast<uint32_t *>(prow + (((n ^ i) & 7) << 4)) = pack_weights<FP16>(p0, p1);
                         }
                         float s0, s1;
                         unpair(sum, s0, s1);
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (k >= nk) break;
                     inv[k] = l[k] == 0.f ? 0.f : 1.f / l[k];
                     if ((lane & 3) == 0) {
-                        const float l2 = l[k] == 0.f ? -INFINITY : m[k] * c + __log2f(l[k]);
+                        const float l2 = l[k] == 0.f ? -INFINITY : m[k] * c + (__log2f(l[k]) - kBias<FP16>);
                         if (!whole)
                             p.part_l[slot * NR + i] = l2;
                         else if (a.lse && i < rows)

@@ -15,9 +15,9 @@
 //   warp 10  value rows that a query of the CTA does not see: those behind the sequence become zeros, and
 //            those that are not finite too (0 x NaN is NaN), with a mark that makes the sums of the queries
 //            that see them NaN.  Only tiles that some query sees in part need it.
-// Tensor memory: S0 S1 O0 O1, 128 columns each.  The running maximum is raised only by more than 2^8 (kRaise), by the
+// Tensor memory: S0 S1 O0 O1, 128 columns each.  The running maximum is raised only by more than kRaise, by the
 // row's own thread in place.  Weights are rounded to the element type for the second product (its operands are
-// 16-bit); their sum is kept in fp32 from the unrounded weights.
+// 16-bit), in fp16 moved up by 2^kBias; their sum is kept in fp32 from the unrounded weights.
 // Query tiles are dealt out from the last (under a causal mask the longest) to the first.
 #include <algorithm>
 
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(PNT, 1)
         const uint32_t ts = tmem + lanes + t * PK, to = tmem + lanes + T_O + t * 128;
         const int i = qt + (ONE ? 0 : t * PQ) + 32 * (warp & 3) + lane;  // this thread's query
         const int lim = i < nq ? limit(i) : 0;
-        const float c = a.scale * kLog2e, raise = kRaise / c;
+        const float c = a.scale * kLog2e, raise = kRaise<FP16> / c;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < nt[t] && ok; ++j) {
             ok = warp_wait(s_full + t, (uint32_t)j & 1u);
@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(PNT, 1)
                         if (mk4[e]) l = NAN;
                 }
             }
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+            const float up = m == -INFINITY ? 0.f : fmaf(-m, c, kBias<FP16>);
+            const uint64_t c2 = pair(c, c), up2 = pair(up, up);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -415,11 +415,11 @@ __global__ void __launch_bounds__(PNT, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     float x0, x1;
-                    unpair(fma2(pair(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])), c2, mc2), x0, x1);
+                    unpair(fma2(pair(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])), c2, up2), x0, x1);
                     x0 = exp2_(x0);
                     x1 = exp2_(x1);
                     sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(x0, x1));
-                    w[e >> 1] = pack2<FP16>(x0, x1);
+                    w[e >> 1] = pack_weights<FP16>(x0, x1);
                 }
                 st16_issue(ts + 16 * g, w);
             }
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(PNT, 1)
                     dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
             }
-            if (a.lse && i < nq) a.lse[row] = l == 0.f ? -INFINITY : (m * c + __log2f(l)) * kLn2;
+            if (a.lse && i < nq) a.lse[row] = l == 0.f ? -INFINITY : (m * c + (__log2f(l) - kBias<FP16>)) * kLn2;
         }
         __syncthreads_or(!ok);
     }

@@ -334,10 +334,11 @@ KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, 
  * bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Cache rows that a query does not see
  * do not matter to it, whatever they hold (NaN too); a query that sees a non-finite row gets non-finite outputs,
  * all NaN where that row is one of the nq tokens.
- * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product, outputs at
- * the end.  Results do not depend on the other sequences' contents, but a sequence's split over CTAs (and so
- * its last bits) depends on all lengths of the call and on the GPU's number of multiprocessors.  The workspace
- * need not be initialised and keeps nothing between calls; calls that overlap on the GPU need one each.
+ * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 one below
+ * 2^-23 of its row's largest by up to 2^-34 of the largest), outputs at the end.  Results do not depend on the other
+ * sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all lengths of the call and
+ * on the GPU's number of multiprocessors.  The workspace need not be initialised and keeps nothing between calls; calls
+ * that overlap on the GPU need one each.
  * 1 <= H <= KDA_LATENT_MAX_HEADS, max_tokens <= KDA_LATENT_MAX_TOKENS, n <= 65535.  A wait that gives up sets
  * KDA_DEV_TIMEOUT (outputs then are undefined).
  */
