@@ -631,7 +631,8 @@ def kda_pages_truncate(pt: PageTable, rows, keep_lens, workspace, dev_status, st
 
 
 def kda_pages_fork(pt: PageTable, cache: LatentCache, parents, children, workspace, dev_status, stream=None) -> None:
-    """The empty rows children become copies of rows parents: full pages shared, a partly filled last one copied."""
+    """The empty rows children become copies of rows parents: full pages shared, a partly filled last one copied (-1 as
+    parent or child: padding, which names no row)."""
     _pages_call("kda_pages_fork", pt, cache, (parents, children), workspace, dev_status, stream)
 
 

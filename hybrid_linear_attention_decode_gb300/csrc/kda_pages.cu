@@ -23,7 +23,7 @@ constexpr int PIECE = AT * UNROLL; // words of a copy piece (16 KiB)
 // Workspace (int32): header, row claims, per-item records, free list or page map, copy lists.
 struct Ws {
     int32_t *hdr;    // [0] entries of the copy lists
-    int32_t *claim;  // [max_seqs] first item that names the row
+    int32_t *claim;  // [max_seqs] first item, padding aside, that names the row
     int32_t *start;  // [n] first entry of the free list the item takes
     int32_t *flag;   // [n] 0: left out; 1: served; 3: served, with a copied page
     int32_t *len;    // [n] tokens of the row (fork: of the parent) before the call
@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(PT) kda_pages_plan_kernel(const PagesArgs a) {
     __syncthreads();
     for (int i = tid; i < a.n; i += PT) {
         const int32_t r = named[i];
+        if (OP == PAGES_FORK && a.x[i] == -1) continue;  // a padding item, whatever its child
         if (r >= 0 && r < t.max_seqs) atomicMin(w.claim + r, i);
     }
     const int64_t nfree = OP == PAGES_TRUNCATE ? 0 : free_pages(t, w.list, part);

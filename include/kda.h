@@ -384,7 +384,7 @@ KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t r
  * do not depend on timing.  An item with a bad row index or length, or whose row appears in an earlier item of
  * the call as well, is flagged (KDA_DEV_BAD_SLOT, _SEQLENS) and left out; so is one for which free pages do
  * not suffice (KDA_DEV_NO_PAGES; the demand of items before it counts whether they were served or not).  Row -1
- * is a padding item.
+ * (fork: -1 as parent or child) makes a padding item, which does nothing and names no row.
  * Shared pages (refcount > 1) are never written.  cache (all layers) is what page copies apply to; its
  * page_size and num_pages have to be the table's.
  *
