@@ -226,6 +226,15 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 // that other work could see or have written; that returns when the kernel before is done and its writes are visible.  All
 // latent attention and pool kernels are launched so: one call after another takes 0.2 to 1.4 us less (append 2.7 -> 2.35 us,
 // decode over one sequence 11.9 -> 11.65, trees 88.2 -> 86.8).
+// These kernels read global memory with ordinary loads (or streaming ones, or by TMA): a non-coherent load is for memory that
+// nothing writes while the kernel is on the GPU, and here that begins before the kernel ahead has written the last of it.
+// An ordinary load as an instruction of its own, behind the waits ahead of it; many of them stay in flight together (the
+// decode kernel's queries as C++ loads: one sequence 11.9 us instead of 11.5).
+__device__ __forceinline__ uint2 load_ordinary(const uint2 *p) {
+    uint2 r;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
 __device__ __forceinline__ void allow_dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

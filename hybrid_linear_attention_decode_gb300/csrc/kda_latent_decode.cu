@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int key = (off + j) * TILE + (lane & 7) * 8;  // below 2^31: len is
                     int page = (int)a.c.num_pages;                      // a box outside the tensor reads as zeros
                     if (lane < 8 && key < s.len) {
-                        const int e = __ldg(trow + key / ps);
+                        const int e = trow[key / ps];
                         if (e >= 0 && e < a.c.num_pages)
                             page = e;
                         else
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(NT, 1)
                             for (int k = 0; k < 2; ++k) {
                                 const int ch = ch0 + 128 * u;
                                 uint2 x = make_uint2(0, 0);
-                                if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = __ldg(src[k] + ch / 4 + 4 * n);
+                                if (8 * k < rw && i0 + 8 * k < rows && ch + 16 * n < d) x = load_ordinary(src[k] + ch / 4 + 4 * n);
                                 v[u][4 * n + 2 * k] = x.x;
                                 v[u][4 * n + 2 * k + 1] = x.y;
                             }
