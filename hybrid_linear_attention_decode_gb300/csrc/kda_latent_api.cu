@@ -14,9 +14,16 @@ namespace {
 
 bool al(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Tokens, pages and strides beyond these are refused, so that no product below overflows 64 bits.
+// Tokens, pages, strides and the elements from a tensor's first index to its last beyond these are refused, so that no
+// product here or in the kernels overflows 64 bits; sequences, table rows and items beyond kMaxItems, so that 32-bit
+// indices that step past the last one by a grid or a block do not wrap around.
 constexpr int64_t kMaxCount = (int64_t)1 << 31;
 constexpr int64_t kMaxStride = (int64_t)1 << 36;
+constexpr int64_t kMaxExtent = (int64_t)1 << 44;
+constexpr int32_t kMaxItems = 1 << 30;
+
+// Whether `count` indices at that stride reach past kMaxExtent (both checked before: not negative).
+bool too_far(int64_t count, int64_t stride) { return count > 1 && stride > kMaxExtent / (count - 1); }
 
 int check_cache(const kda_latent_cache *c, LatentCacheArgs *o) {
     if (!c || !c->pages) return fail(KDA_ERR_INVALID_ARG, "latent cache: cache or pages is NULL");
@@ -33,7 +40,8 @@ int check_cache(const kda_latent_cache *c, LatentCacheArgs *o) {
     if (!al(c->pages, 16) || c->layer_stride % 8 || c->page_stride % 8)
         return fail(KDA_ERR_INVALID_ARG, "latent cache: pages and strides must be 16-byte aligned");
     const int64_t page = (int64_t)c->page_size * (c->rank + c->rope);
-    if (c->layer_stride < 0 || c->page_stride < 0 || c->layer_stride > kMaxStride || c->page_stride > kMaxStride)
+    if (c->layer_stride < 0 || c->page_stride < 0 || c->layer_stride > kMaxStride || c->page_stride > kMaxStride ||
+        too_far(c->layers, c->layer_stride) || too_far(c->num_pages, c->page_stride))
         return fail(KDA_ERR_INVALID_ARG, "latent cache: stride out of range");
     const bool pages_inside = c->num_pages == 1 || c->page_stride >= page;
     const bool layers_inside = c->layers == 1 || c->layer_stride >= page;
@@ -61,7 +69,7 @@ int check_table(const kda_page_table *p, bool counts, PageTableArgs *o) {
         return fail(KDA_ERR_INVALID_ARG, "page table: table, lens or refcount is NULL");
     if (!al(p->table, 4) || !al(p->lens, 4) || (p->refcount && !al(p->refcount, 4)))
         return fail(KDA_ERR_INVALID_ARG, "page table: table, lens or refcount misaligned");
-    if (p->max_seqs < 1 || p->max_pages < 1 || p->page_size < 1 || p->page_size > 1024 || p->num_pages < 1 ||
+    if (p->max_seqs < 1 || p->max_seqs > kMaxItems || p->max_pages < 1 || p->page_size < 1 || p->page_size > 1024 || p->num_pages < 1 ||
         p->num_pages >= kMaxCount)
         return fail(KDA_ERR_INVALID_ARG, "page table: sizes out of range");
     if ((int64_t)p->max_pages * p->page_size > kMaxCount - 64)  // whole tiles of 64 tokens stay below 2^31
@@ -85,7 +93,10 @@ int check_same(const LatentCacheArgs &c, const PageTableArgs &t) {
 // The kernels work with scale * log2(e) and 6 or 8 / that, which have to be normal numbers; a NaN fails both comparisons.
 bool good_scale(float s) { return s >= 1e-30f && s <= 1e30f; }
 
-bool bad_stride(int64_t s, int64_t least) { return s < least || s > kMaxStride || s % 8; }
+// A stride of `count` indices.
+bool bad_stride(int64_t s, int64_t least, int64_t count) {
+    return s < least || s > kMaxStride || s % 8 || too_far(count, s);
+}
 
 }  // namespace
 
@@ -102,7 +113,7 @@ int kda_latent_append(const kda_latent_cache *cache, int32_t layer, const kda_pa
     if (rc == KDA_OK) rc = check_same(a.c, a.t);
     if (rc != KDA_OK) return rc;
     if (layer < 0 || layer >= a.c.layers) return fail(KDA_ERR_INVALID_ARG, "latent append: layer out of range");
-    if (n < 0 || num_tokens < 0 || num_tokens >= kMaxCount)
+    if (n < 0 || n > kMaxItems || num_tokens < 0 || num_tokens >= kMaxCount)
         return fail(KDA_ERR_INVALID_ARG, "latent append: n or num_tokens out of range");
     if (n == 0 || num_tokens == 0) return KDA_OK;
     if (!cu_tokens || !latent || (a.c.rope > 0 && !rope))
@@ -110,8 +121,8 @@ int kda_latent_append(const kda_latent_cache *cache, int32_t layer, const kda_pa
     if (!al(latent, 16) || (a.c.rope > 0 && !al(rope, 16)) || !al(cu_tokens, 4) || (rows && !al(rows, 4)) ||
         (dev_status && !al(dev_status, 4)))
         return fail(KDA_ERR_INVALID_ARG, "latent append: latent and rope must be 16-byte aligned, the others 4-byte");
-    if (bad_stride(latent_stride, num_tokens > 1 ? a.c.rank : 0) ||
-        (a.c.rope > 0 && bad_stride(rope_stride, num_tokens > 1 ? a.c.rope : 0)))
+    if (bad_stride(latent_stride, num_tokens > 1 ? a.c.rank : 0, num_tokens) ||
+        (a.c.rope > 0 && bad_stride(rope_stride, num_tokens > 1 ? a.c.rope : 0, num_tokens)))
         return fail(KDA_ERR_INVALID_ARG, "latent append: row strides must be multiples of 8 that hold a row");
     a.c.pages += layer * a.c.layer_stride;
     a.n = n;
@@ -161,7 +172,7 @@ int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, const kda_pa
         return fail(KDA_ERR_INVALID_ARG, "latent decode: q and out must be 16-byte aligned, tree_mask 8-byte, the "
                                          "others 4-byte");
     const int64_t d = a.c.rank + a.c.rope;
-    if (bad_stride(q_token_stride, num_tokens > 1 ? 8 : 0) || bad_stride(q_head_stride, H > 1 ? d : 0))
+    if (bad_stride(q_token_stride, num_tokens > 1 ? 8 : 0, num_tokens) || bad_stride(q_head_stride, H > 1 ? d : 0, H))
         return fail(KDA_ERR_INVALID_ARG, "latent decode: q strides must be multiples of 8 that hold a row");
     const size_t need = latent_decode_workspace_bytes(a.c.rank, H, n, max_tokens);
     if (!workspace || workspace_bytes < need || !al(workspace, 16))
@@ -213,10 +224,10 @@ int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: q, k_nope, k_rope, v and out must be 16-byte aligned");
     if (!al(cu_q, 4) || !al(cu_k, 4) || (lse && !al(lse, 4)) || (dev_status && !al(dev_status, 4)))
         return fail(KDA_ERR_INVALID_ARG, "latent prefill: tables, lse or status misaligned");
-    if (bad_stride(q_token_stride, 8) || bad_stride(q_head_stride, 8) || bad_stride(k_token_stride, 8) ||
-        bad_stride(k_head_stride, 8) || bad_stride(rope_token_stride, 8) || bad_stride(v_token_stride, 8) ||
-        bad_stride(v_head_stride, 8))
-        return fail(KDA_ERR_INVALID_ARG, "latent prefill: strides must be positive multiples of 8");
+    if (bad_stride(q_token_stride, 8, num_q) || bad_stride(q_head_stride, 8, H) || bad_stride(k_token_stride, 8, num_k) ||
+        bad_stride(k_head_stride, 8, H) || bad_stride(rope_token_stride, 8, num_k) ||
+        bad_stride(v_token_stride, 8, num_k) || bad_stride(v_head_stride, 8, H))
+        return fail(KDA_ERR_INVALID_ARG, "latent prefill: strides must be positive multiples of 8 in range");
     LatentPrefillArgs a;
     a.fp16 = dtype == KDA_ELEM_FP16;
     a.H = H;
@@ -250,7 +261,9 @@ int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int
 
 size_t kda_pages_workspace_bytes(const kda_page_table *pt, int32_t n) {
     clear_error();
-    if (!pt || n < 0 || pt->max_seqs < 1 || pt->num_pages < 1 || pt->num_pages >= kMaxCount) return 0;
+    if (!pt || n < 0 || n > kMaxItems || pt->max_seqs < 1 || pt->max_seqs > kMaxItems || pt->num_pages < 1 ||
+        pt->num_pages >= kMaxCount)
+        return 0;
     return pages_workspace_bytes(pt->max_seqs, pt->num_pages, n);
 }
 
@@ -268,7 +281,7 @@ static int pages_call(PageOp op, const kda_page_table *pt, const kda_latent_cach
     } else {
         a.c = LatentCacheArgs{};
     }
-    if (n < 0) return fail(KDA_ERR_INVALID_ARG, "pages: n < 0");
+    if (n < 0 || n > kMaxItems) return fail(KDA_ERR_INVALID_ARG, "pages: n out of range");
     if (op != PAGES_COMPACT) {
         if (n == 0) return KDA_OK;
         if (!x || !y || !al(x, 4) || !al(y, 4))
@@ -314,7 +327,7 @@ int kda_pages_copy(const kda_latent_cache *cache, int32_t n, const int32_t *src,
     LatentCacheArgs c;
     const int rc = check_cache(cache, &c);
     if (rc != KDA_OK) return rc;
-    if (n < 0) return fail(KDA_ERR_INVALID_ARG, "pages copy: n < 0");
+    if (n < 0 || n > kMaxItems) return fail(KDA_ERR_INVALID_ARG, "pages copy: n out of range");
     if (n == 0) return KDA_OK;
     if (!src || !dst || !al(src, 4) || !al(dst, 4) || (dev_status && !al(dev_status, 4)))
         return fail(KDA_ERR_INVALID_ARG, "pages copy: src, dst or status NULL or misaligned");

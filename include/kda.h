@@ -259,6 +259,8 @@ KDA_API int kda_resume_from_slot(const kda_pool *pool, int32_t n, const int32_t 
  * and pages may have any (16-byte aligned, not overlapping) stride.  One page index holds the same tokens in
  * every layer.  Supported: rank in {128, 256, 384, 512}; rope a multiple of 16, 0 to 64; page_size 16, 32 or a
  * multiple of 64 up to 1024.
+ * In all of these calls a tensor's strides reach at most 2^44 elements from its first index to its last, and n and
+ * max_seqs are at most 2^30 (where no lower limit is given).
  */
 enum kda_elem_type { KDA_ELEM_BF16 = 0, KDA_ELEM_FP16 = 1 };
 
