@@ -334,8 +334,10 @@ KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, 
  * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so
  * do the queries of a sequence with a bad row or length (flagged; a bad page's tokens read as zero rows).  Sequences with
  * bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Cache rows that a query does not see
- * do not matter to it, whatever they hold (NaN too); a query that sees a non-finite row gets non-finite outputs,
- * all NaN where that row is one of the nq tokens.
+ * do not matter to it, whatever they hold (NaN too).  A row with a NaN makes the outputs and lse of the queries that see
+ * it NaN, and so does one with an infinity whose score is +infinity or NaN.  Where its score is -infinity it has weight
+ * 0, and only the channels that are infinite in it may come out NaN; but where it is one of several drafted tokens (nq
+ * above 1, or a tree_mask), all outputs and lse of the queries that see it are NaN.
  * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 one below
  * 2^-23 of its row's largest by up to 2^-34 of the largest), outputs at the end.  Results do not depend on the other
  * sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all lengths of the call and
@@ -368,7 +370,9 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
  *   out         device [num_q][H][dv] contiguous, same type        lse  device [num_q][H] fp32, or NULL
  * A query that sees no key gets out 0 and lse -inf; sequences with bad tables (KDA_DEV_BAD_SEQLENS) and rows
  * behind cu_q[nseq] are left as they were.  Keys and values that a query does not see do not matter to it,
- * whatever they hold.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; a query's result depends on its
+ * whatever they hold.  A seen key with a NaN, or whose score is +infinity, makes a query's outputs and lse NaN (-infinity:
+ * weight 0); a seen value that is not finite makes its channel, and in some calls all of the query's outputs and lse,
+ * NaN or infinite.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; a query's result depends on its
  * sequence alone, its last bits also on H, nseq and max_q (they decide how the work is cut).  Supported: nope and
  * dv in {64, 128}; rope a multiple of 16, 16 to 64; scale from 1e-30 to 1e30; max_q up to KDA_LATENT_MAX_QUERIES.
  * A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
