@@ -7,8 +7,9 @@
 //
 // Split: the 64-token tiles of all sequences form one list, and each group of CTAs takes an equal, contiguous
 // part of it (found on the device from lens, so a captured launch follows its lengths).  A group has one CTA for
-// each 64 rows, side by side in the grid, so that they read the same tiles at the same time and all but one of
-// them from L2.  A sequence that a group holds whole is written at once; one that is cut
+// each 64 of H max_tokens rows, side by side in the grid, so that they read the same tiles at the same time and all but
+// one of them from L2; where a sequence has fewer rows, the CTAs of the others idle (64 sequences of one query, 32 heads:
+// 67 us with max_tokens 1, 171 with 8).  A sequence that a group holds whole is written at once; one that is cut
 // leaves normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
 // A tile, by one CTA of 12 warps (one CTA per SM, ring of tiles in shared memory):
@@ -17,7 +18,7 @@
 //            k = token; C is the same shared memory, read MN-major).  With M 64 an accumulator has half of the
 //            tensor-memory lanes: O, rank columns wide, takes lanes 16-31 of each warp's quarter, Q and S lanes 0-15.
 //            (The transposed product O^T += C^T P^T would leave no row of M unused, but an MN-major A operand
-//            of M 128, N 32 took 187 cycles an instruction; as B it takes 128 for N 256.)
+//            of M 128, N 32 took 187 cycles an instruction; as B of M 64, N 256 it takes 156.)
 //   warps 6-9  the queries of the next sequence into tensor memory, as soon as the last S of this one is done
 //   warps 0-3  softmax of S (8 or 16 rows a warp, a quad of threads a row), P to shared memory, and at the end O out.
 // S of a tile is issued before P V of the one before, so the softmax overlaps the products.
@@ -39,7 +40,10 @@ constexpr int NR = 64;               // rows (query, head) per CTA
 constexpr int NT = 384;
 constexpr int SW = 4;                // softmax warps
 // A sequence counts for this many tiles more where the list is split: ending one and beginning the next on a CTA costs
-// about as much time (64 sequences of 500 to 8192 tokens, 32 heads, as measured then: 80.4 us without, 75.3 with 3, 72.7 with 5, 73.8 with 8).
+// about as much time.  us with 0 / 2 / 5 / 8: 64 sequences of 500 to 8192 tokens, 32 heads, rank 512: 73.3 / 71.5 / 70.8 / 72.4, rank
+// 256: 47.2 / 46.2 / 44.0 / 45.1, rank 128: 40.5 / 38.9 / 36.9 / 38.3; 16 of these with 128 heads, rank 512: 53.5 / 45.8 / 42.8 /
+// 43.5; 200 of up to 3000, 16 heads, rank 128: 49.7 / 46.4 / 45.4 / 46.6; 300 of 100 to 900, 32 heads, rank 128: 38.5 / 34.7 / 33.4 /
+// 34.3, rank 512: 57.5 / 51.0 / 52.6 / 56.4 (the one where 2 would do better).
 constexpr int START = 5;
 constexpr int QW = 4;                // query warps, one for each quarter of the lanes
 constexpr uint32_t ATOM = 1024;      // bytes of 8 tokens x 64 channels

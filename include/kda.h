@@ -328,9 +328,14 @@ KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_cache *cache, 
  *   q          device [num_tokens][H][rank+rope], the cache's type, at the given token and head strides
  *              (elements, multiples of 8), 16-byte aligned
  *   tree_mask  device [num_tokens] uint64, or NULL
- *   scale      from 1e-30 to 1e30
+ *   scale      from 1e-30 to 1e30; scores, scaled by it and by log2 e, have to stay within fp32
  *   out        device [num_tokens][H][rank] contiguous, the cache's type, 16-byte aligned
  *   lse        device [num_tokens][H] fp32: the natural logarithm of the sum of exp(s); or NULL
+ * out, lse and the workspace overlap nothing else that the call reads or writes.
+ * max_tokens decides how the call is cut: ceil(H max_tokens / 64) CTAs share each part of a sequence, of which those past
+ * its own ceil(H nq / 64) idle, so a sequence costs about as much with one query as with max_tokens.  64 sequences of 500 to
+ * 8192 tokens with one query each, rank 512: 32 heads 67 us with max_tokens 1, 171 with 8, 1469 with 64; 128 heads 104
+ * and 678.  Where few sequences have drafts, one call for these and one for the others is faster.
  * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so
  * do the queries of a sequence with a bad row or length (flagged; a bad page's tokens read as zero rows).  Sequences with
  * bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Cache rows that a query does not see
@@ -374,7 +379,8 @@ KDA_API int kda_latent_decode(const kda_latent_cache *cache, int32_t layer, cons
  * weight 0); a seen value that is not finite makes its channel, and in some calls all of the query's outputs and lse,
  * NaN or infinite.  fp32 scores, sums and outputs, roundings as for kda_latent_decode; a query's result depends on its
  * sequence alone, its last bits also on H, nseq and max_q (they decide how the work is cut).  Supported: nope and
- * dv in {64, 128}; rope a multiple of 16, 16 to 64; scale from 1e-30 to 1e30; max_q up to KDA_LATENT_MAX_QUERIES.
+ * dv in {64, 128}; rope a multiple of 16, 16 to 64 (a model without rotary keys gives 16 zeros); scale as for
+ * kda_latent_decode; max_q up to KDA_LATENT_MAX_QUERIES.
  * A wait that gives up sets KDA_DEV_TIMEOUT (outputs then are undefined).
  */
 KDA_API int kda_latent_prefill(int32_t dtype, int32_t H, int32_t nope, int32_t rope, int32_t dv, int32_t nseq,
