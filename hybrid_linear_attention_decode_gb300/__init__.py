@@ -10,7 +10,8 @@ Entry points (same names as the C ABI): ``kda_project_inputs``, ``kda_decode_ste
 ``kda_status_string``; the host prefix index ``kda_prefix_*`` through :class:`PrefixIndex`; latent attention over
 a paged cache (:class:`LatentCache`, :class:`PageTable`): ``kda_latent_append``, ``kda_latent_decode``,
 ``kda_latent_prefill`` and the page pool's ``kda_pages_reserve``, ``kda_pages_truncate``, ``kda_pages_fork``,
-``kda_pages_compact``, ``kda_pages_copy``.
+``kda_pages_compact``, ``kda_pages_copy``; grouped-query attention over the same pool (:class:`KvCache`):
+``kda_kv_append``, ``kda_kv_decode``, ``kda_kv_evict``; rotary positions (:class:`Rope`): ``kda_rope_apply``.
 """
 from __future__ import annotations
 
@@ -39,6 +40,8 @@ class KdaError(RuntimeError):
 KDA_STATE_FP32, KDA_STATE_BF16 = 0, 1
 KDA_ELEM_BF16, KDA_ELEM_FP16 = 0, 1
 LATENT_MAX_TOKENS, LATENT_MAX_HEADS = 64, 128  # KDA_LATENT_MAX_* in kda.h
+KDA_ROPE_PLAIN, KDA_ROPE_LINEAR, KDA_ROPE_NTK, KDA_ROPE_PARTS = 0, 1, 2, 3
+KV_MAX_TOKENS, KV_MAX_HEADS, KV_EVICT_MAX_LEN = 64, 256, 1 << 20  # KDA_KV_* in kda.h
 
 
 class _Pool(ctypes.Structure):
@@ -63,6 +66,18 @@ class _PageTable(ctypes.Structure):
     _fields_ = [("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
                 ("lens", ctypes.c_void_p), ("refcount", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("layers", ctypes.c_int32), ("dtype", ctypes.c_int32), ("stats", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("pages", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("offset", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("turns", ctypes.c_void_p)]
 
 
 class _PrefixPlan(ctypes.Structure):
@@ -130,6 +145,21 @@ def load_library(path: str | None = None):
     lib.kda_pages_compact.restype = ctypes.c_int
     lib.kda_pages_copy.argtypes = [pcache, i32, vp, vp, vp, vp]
     lib.kda_pages_copy.restype = ctypes.c_int
+    pkv, prope, f64 = ctypes.POINTER(_KvCache), ctypes.POINTER(_Rope), ctypes.c_double
+    lib.kda_kv_cache_pages.argtypes = [pkv, pcache]
+    lib.kda_rope_turns.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+    lib.kda_rope_turns_of.argtypes = [i32, vp, vp]
+    lib.kda_rope_apply.argtypes = [prope, i32, i64, i32, i32, vp, i32, vp, i64, i64, vp, i64, i64, vp]
+    lib.kda_kv_append.argtypes = [pkv, i32, ptable, i32, vp, vp, i64, vp, i64, i64, vp, i64, i64, vp, prope, i32, vp, i64,
+                                  i64, vp, vp, vp]
+    lib.kda_kv_decode_workspace_bytes.argtypes = [pkv, i32, i32, i32, i64]
+    lib.kda_kv_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_kv_decode.argtypes = [pkv, i32, ptable, i32, vp, vp, i64, i32, i32, vp, i64, i64, vp, f32, vp, vp, i32, f32,
+                                  i64, vp, ctypes.c_size_t, vp, vp]
+    lib.kda_kv_evict.argtypes = [pkv, ptable, i32, vp, vp, i32, vp, vp, vp, vp]
+    for name in ("kda_kv_cache_pages", "kda_rope_turns", "kda_rope_turns_of", "kda_rope_apply", "kda_kv_append",
+                 "kda_kv_decode", "kda_kv_evict"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.kda_selftest_wait_timeout.argtypes = [i64, vp, vp]
     lib.kda_selftest_wait_timeout.restype = ctypes.c_int
     lib.kda_prefix_index_create.argtypes = [i32, i32, i32, i64]
@@ -646,6 +676,238 @@ def kda_pages_copy(cache: LatentCache, src, dst, dev_status, stream=None) -> Non
     name = "kda_pages_copy"
     dev, n = _device_of(name, (cache.pages, src, dst, dev_status)), src.shape[0]
     _launch(load_library().kda_pages_copy, name, dev, stream, cache.c(), n, _int32(src, "src"), _int32(dst, "dst", n),
+            _int32(dev_status, "dev_status", 1))
+
+
+# ------------------------------------------------------------------------------- grouped-query attention, rotary positions
+@dataclass
+class KvCache:
+    """Pages of keys and values of every layer: data [layers, num_pages, words] bf16 or fp16, a page of page_size tokens
+    holding keys [heads, page_size, head_dim], values of the same shape and, with stats, fp32 sums of attention weights
+    and int32 positions [heads, 2, page_size].  The first two axes of data may be strided.  The kda_pages_* calls take a
+    KvCache as they take a :class:`LatentCache`."""
+    data: torch.Tensor
+    heads: int
+    head_dim: int
+    page_size: int
+    stats: bool = False
+
+    @staticmethod
+    def words(page_size: int, heads: int, head_dim: int, stats: bool = False) -> int:
+        """16-bit words of a page."""
+        return page_size * heads * (2 * head_dim + (4 if stats else 0))
+
+    @staticmethod
+    def empty(layers: int, num_pages: int, page_size: int, heads: int, head_dim: int, stats: bool = False,
+              dtype=torch.bfloat16, device="cuda") -> "KvCache":
+        return KvCache(torch.zeros(layers, num_pages, KvCache.words(page_size, heads, head_dim, stats), dtype=dtype,
+                                   device=device), heads, head_dim, page_size, stats)
+
+    def _rows(self, part: int) -> torch.Tensor:
+        size = self.heads * self.page_size * self.head_dim
+        return self.data[..., part * size:(part + 1) * size].unflatten(-1, (self.heads, self.page_size, self.head_dim))
+
+    @property
+    def keys(self) -> torch.Tensor:
+        """View [layers, num_pages, heads, page_size, head_dim]."""
+        return self._rows(0)
+
+    @property
+    def values(self) -> torch.Tensor:
+        """View [layers, num_pages, heads, page_size, head_dim]."""
+        return self._rows(1)
+
+    def _stats(self, part: int, dtype) -> torch.Tensor:
+        _need(self.stats, "kv cache: it has no stats")
+        at = self.heads * self.page_size * self.head_dim
+        return self.data.view(dtype)[..., at:].unflatten(-1, (self.heads, 2, self.page_size))[..., part, :]
+
+    @property
+    def weights(self) -> torch.Tensor:
+        """View [layers, num_pages, heads, page_size] fp32: each token's accumulated attention weight."""
+        return self._stats(0, torch.float32)
+
+    @property
+    def positions(self) -> torch.Tensor:
+        """View [layers, num_pages, heads, page_size] int32."""
+        return self._stats(1, torch.int32)
+
+    def _key(self):
+        p = self.data
+        return (p.data_ptr(), p.shape, p.stride(), p.dtype, self.heads, self.head_dim, self.page_size, self.stats)
+
+    def kv(self) -> _KvCache:
+        """The C struct of the pages as they are now (made again when anything that goes into it has changed)."""
+        key, kept = self._key(), self.__dict__.get("_kept")
+        if kept is not None and kept[0] == key:
+            return kept[1]
+        p = self.data
+        if p.dtype not in _ELEM:
+            raise TypeError("kv cache dtype must be bfloat16 or float16")
+        _need(p.dim() == 3 and p.shape[2] == self.words(self.page_size, self.heads, self.head_dim, self.stats)
+              and p.stride(2) == 1, "kv cache: data must be [layers, num_pages, words of a page], a page contiguous")
+        c = _KvCache(self.heads, self.head_dim, self.page_size, p.shape[0], _ELEM[p.dtype], int(bool(self.stats)),
+                     p.shape[1], p.stride(0), p.stride(1), ctypes.c_void_p(p.data_ptr()))
+        self.__dict__["_kept"] = (key, c)
+        return c
+
+    def c(self) -> _LatentCache:
+        """The C struct that the kda_pages_* calls take."""
+        key, kept = self._key(), self.__dict__.get("_kept_pages")
+        if kept is not None and kept[0] == key:
+            return kept[1]
+        c = _LatentCache()
+        _check(load_library().kda_kv_cache_pages(self.kv(), c), "kda_kv_cache_pages")
+        self.__dict__["_kept_pages"] = (key, c)
+        return c
+
+    @property
+    def pages(self) -> torch.Tensor:
+        return self.data
+
+
+_SCALING = {"none": KDA_ROPE_PLAIN, "linear": KDA_ROPE_LINEAR, "ntk": KDA_ROPE_NTK, "parts": KDA_ROPE_PARTS}
+
+
+@dataclass
+class Rope:
+    """Rotary positions of the channels offset .. offset + dim - 1 of a head: turns int64 [dim / 2] on the GPU (the bits
+    of kda_rope.turns), pairs as halves or interleaved, rotated values times scale."""
+    turns: torch.Tensor
+    offset: int = 0
+    interleaved: bool = False
+    scale: float = 1.0
+
+    @staticmethod
+    def make(dim: int, base: float = 10000.0, offset: int = 0, interleaved: bool = False, scaling: str = "none",
+             factor: float = 1.0, original: float = 0.0, low: float = 1.0, high: float = 32.0, scale: float = 1.0,
+             device="cuda") -> "Rope":
+        """theta_i = base^(-2i / dim), changed for long contexts as enum kda_rope_scaling in kda.h says: "none", "linear",
+        "ntk" or "parts" (by `low` and `high` turns within the `original` length)."""
+        if scaling not in _SCALING:
+            _raise(f"scaling must be one of {', '.join(_SCALING)}")
+        turns = torch.empty(max(dim // 2, 0), dtype=torch.int64)
+        _check(load_library().kda_rope_turns(dim, base, _SCALING[scaling], factor, original, low, high, turns.data_ptr()),
+               "kda_rope_turns")
+        return Rope(turns.to(device), offset, interleaved, scale)
+
+    @staticmethod
+    def of(theta, offset: int = 0, interleaved: bool = False, scale: float = 1.0, device="cuda") -> "Rope":
+        """Of dim / 2 frequencies in radians a position, given one by one."""
+        theta = torch.as_tensor(theta, dtype=torch.float64, device="cpu").contiguous()
+        turns = torch.empty(theta.shape, dtype=torch.int64)
+        _check(load_library().kda_rope_turns_of(theta.numel(), theta.data_ptr(), turns.data_ptr()), "kda_rope_turns_of")
+        return Rope(turns.to(device), offset, interleaved, scale)
+
+    def c(self) -> _Rope:
+        """The C struct of the tensor as it is now (made again when anything that goes into it has changed)."""
+        t = self.turns
+        key = (t.data_ptr(), t.shape, t.dtype, self.offset, self.interleaved, self.scale)
+        kept = self.__dict__.get("_kept")
+        if kept is not None and kept[0] == key:
+            return kept[1]
+        _need(t.dtype == torch.int64 and t.dim() == 1 and t.is_contiguous(),
+              "rope: turns must be a contiguous int64 vector")
+        c = _Rope(2 * t.shape[0], self.offset, int(bool(self.interleaved)), self.scale, ctypes.c_void_p(t.data_ptr()))
+        self.__dict__["_kept"] = (key, c)
+        return c
+
+
+def kda_rope_apply(rope: Rope, x, positions, out, inverse: bool = False, stream=None) -> None:
+    """x [T, H, D] with the channels that rope names rotated by positions (int32 [T]) into out; see include/kda.h.  Token and
+    head axes may be strided; out may be x.  inverse: by minus the angle, the gradient of the rotation."""
+    name = "kda_rope_apply"
+    dev = _device_of(name, (rope.turns, x, positions, out))
+    if x.dtype not in _ELEM:
+        _raise("x must be bfloat16 or float16")
+    if x.dim() != 3:
+        _raise("x must be [T, H, D]")
+    T, H, D = x.shape
+    _launch(load_library().kda_rope_apply, name, dev, stream, rope.c(), _ELEM[x.dtype], T, H, D,
+            _int32(positions, "positions", T), bool(inverse), *_rows_of(x, "x", x.dtype, x.shape),
+            *_rows_of(out, "out", x.dtype, x.shape))
+
+
+def kda_kv_append(cache: KvCache, layer: int, pt: PageTable, rows, cu_tokens, k, v, positions, dev_status,
+                  rope: Rope | None = None, q=None, q_out=None, stream=None) -> None:
+    """Keys and values of new tokens into one layer's pages; see include/kda.h.  rows int32 [n] or None (row b for
+    sequence b), cu_tokens int32 [n+1], k and v [T, heads, head_dim] and q [T, H, head_dim] of the cache's type (token and
+    head axes may be strided), positions int32 [T].  rope rotates the keys on their way and, into q_out [T, H, head_dim],
+    the queries.  The tokens become the last ones of their rows, which pt.lens already counts."""
+    name = "kda_kv_append"
+    dev = _device_of(name, (cache.data, pt.table, pt.lens, rows, cu_tokens, k, v, positions, dev_status, q, q_out,
+                            None if rope is None else rope.turns))
+    cc, dtype = cache.kv(), cache.data.dtype
+    n, T = cu_tokens.shape[0] - 1, k.shape[0]
+    shape = (T, cc.heads, cc.head_dim)
+    H, qa, qo = 0, (None, 0, 0), None
+    if q is not None:
+        if q.dim() != 3 or q_out is None:
+            _raise("q must be [T, H, head_dim], and q_out given")
+        H = q.shape[1]
+        qa = _rows_of(q, "q", dtype, (T, H, cc.head_dim))
+        qo = _out(q_out, "q_out", dtype, (T, H, cc.head_dim))
+    _launch(load_library().kda_kv_append, name, dev, stream, cc, layer, pt.c(), n, _int32(rows, "rows", n),
+            _int32(cu_tokens, "cu_tokens"), T, *_rows_of(k, "k", dtype, shape), *_rows_of(v, "v", dtype, shape),
+            _int32(positions, "positions", T), None if rope is None else rope.c(), H, *qa, qo,
+            _int32(dev_status, "dev_status", 1))
+
+
+def kda_kv_decode_workspace_bytes(cache: KvCache, H: int, n: int, max_tokens: int, max_slots: int = 0) -> int:
+    """Bytes of workspace kda_kv_decode needs on the cache's device (0 for unsupported sizes); max_slots: a bound on the sum
+    of the call's lens where weights are added up."""
+    with torch.cuda.device(cache.data.device if cache.data.is_cuda else -1):
+        return int(load_library().kda_kv_decode_workspace_bytes(cache.kv(), int(H), int(n), int(max_tokens),
+                                                                int(max_slots)))
+
+
+def kda_kv_decode(cache: KvCache, layer: int, pt: PageTable, rows, cu_tokens, max_tokens: int, q, out, lse, scale: float,
+                  workspace, dev_status, tree_mask=None, weight_decay: float | None = None, max_slots: int | None = None,
+                  stream=None) -> None:
+    """Grouped-query attention of the newest tokens over the paged cache; see include/kda.h.  q [T, H, head_dim] (token and
+    head axes may be strided), out [T, H, head_dim], lse fp32 [T, H] or None; rows, cu_tokens, tree_mask as for
+    kda_latent_decode.  weight_decay: not None adds the call's weights to the cache's sums, after multiplying these
+    with it; max_slots then bounds the sum of the call's lens (None: the pool's pages full once).  workspace uint8,
+    kda_kv_decode_workspace_bytes() bytes for the same max_slots."""
+    name = "kda_kv_decode"
+    adds = weight_decay is not None
+    dev = _device_of(name, (cache.data, pt.table, pt.lens, pt.refcount if adds else None, rows, cu_tokens, q, out, lse,
+                            workspace, dev_status, tree_mask))
+    cc, pc, dtype = cache.kv(), pt.c(), cache.data.dtype
+    if q.dim() != 3:
+        _raise("q must be [T, H, head_dim]")
+    T, H, d = q.shape
+    n = (cu_tokens.shape[0] - 1 if cu_tokens is not None else rows.shape[0] if rows is not None else pc.max_seqs)
+    if rows is None and n > pc.max_seqs:
+        _raise(f"{name}: more sequences than table rows")
+    qp, qt, qh = _rows_of(q, "q", dtype, (T, H, cc.head_dim))
+    if tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.shape != (T,)
+                                  or not tree_mask.is_contiguous()):
+        _raise(f"tree_mask must be a contiguous int64 vector of {T} elements")
+    if out is None:
+        _raise("out must be a tensor")
+    if max_slots is None:
+        max_slots = cc.num_pages * cc.page_size if adds else 0
+    ws, nbytes = _bytes(workspace)
+    _launch(load_library().kda_kv_decode, name, dev, stream, cc, layer, pc, n, _int32(rows, "rows", n),
+            _int32(cu_tokens, "cu_tokens", n + 1), T, max_tokens, H, qp, qt, qh,
+            None if tree_mask is None else tree_mask.data_ptr(), scale, _out(out, "out", dtype, (T, H, d)),
+            _out(lse, "lse", torch.float32, (T, H)), adds, weight_decay if adds else 1.0, max_slots, ws, nbytes,
+            _int32(dev_status, "dev_status", 1))
+
+
+def kda_kv_evict(cache: KvCache, pt: PageTable, rows, keep, new_lens, dev_status, first: int = 0, since=None,
+                 stream=None) -> None:
+    """Each layer and head keeps keep[i] tokens of row rows[i], those with the largest sums, in the row's first slots; see
+    include/kda.h.  rows, keep, new_lens, since int32 [n] (rows and since may be None); kda_pages_truncate(pt, rows,
+    new_lens, ...) then gives the pages behind back."""
+    name = "kda_kv_evict"
+    dev = _device_of(name, (cache.data, pt.table, pt.lens, pt.refcount, rows, keep, new_lens, since, dev_status))
+    n, pc = keep.shape[0], pt.c()
+    if rows is None and n > pc.max_seqs:
+        _raise(f"{name}: more sequences than table rows")
+    _launch(load_library().kda_kv_evict, name, dev, stream, cache.kv(), pc, n, _int32(rows, "rows", n),
+            _int32(keep, "keep"), first, _int32(since, "since", n), _int32(new_lens, "new_lens", n),
             _int32(dev_status, "dev_status", 1))
 
 

@@ -145,6 +145,73 @@ int launch_pages(PageOp op, const PagesArgs &a, cudaStream_t st);
 int launch_pages_copy(const LatentCacheArgs &c, int32_t n, const int32_t *src, const int32_t *dst, int32_t *status,
                       cudaStream_t st);
 
+// Key-value attention over the same pool (kda_kv_api.cu validates, the kda_kv_*.cu files launch).
+struct KvCacheArgs {
+    int32_t heads, d, page_size, layers, fp16, stats;
+    int64_t num_pages, layer_stride, page_stride;  // 16-bit words
+    uint16_t *pages;
+};
+struct RopeArgs {  // dim 0: no rotation
+    int32_t dim, offset, interleaved;
+    float scale;
+    const uint64_t *turns;
+};
+struct RotateArgs {
+    RopeArgs r;
+    int32_t fp16, H, D, inverse, in_place;
+    int64_t num_tokens;
+    const int32_t *positions;
+    const uint16_t *x;
+    uint16_t *out;
+    int64_t x_ts, x_hs, o_ts, o_hs;
+};
+int launch_rotate(const RotateArgs &a, cudaStream_t st);
+
+struct KvAppendArgs {
+    KvCacheArgs c;  // pages already at the layer
+    PageTableArgs t;
+    RopeArgs r;
+    int32_t n, H;   // H 0: no queries
+    const int32_t *rows, *cu, *positions;
+    int64_t num_tokens;
+    const uint16_t *k, *v, *q;
+    uint16_t *q_out;
+    int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
+    int32_t *status;
+};
+int launch_kv_append(const KvAppendArgs &a, cudaStream_t st);
+
+struct KvDecodeArgs {
+    KvCacheArgs c;  // pages already at the layer
+    PageTableArgs t;
+    int32_t n, max_tokens, H;
+    const int32_t *rows, *cu;
+    int64_t num_tokens;
+    const uint16_t *q;
+    int64_t q_ts, q_hs;
+    const uint64_t *tree;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    int32_t add_weights;
+    float decay;
+    int64_t max_slots;
+    void *ws;
+    int32_t *status;
+};
+size_t kv_decode_workspace_bytes(const KvCacheArgs &c, int H, int n, int max_tokens, int64_t max_slots);
+int launch_kv_decode(const KvDecodeArgs &a, cudaStream_t st);
+
+struct KvEvictArgs {
+    KvCacheArgs c;
+    PageTableArgs t;
+    int32_t n, first;
+    const int32_t *rows, *keep, *since;
+    int32_t *new_lens;
+    int32_t *status;
+};
+int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st);
+
 bool prefill_supported(int dk, int dv, int W, int chunk);
 // The host-side argument checks of kda_prefill_chunked (everything but the workspace); KDA_OK or the failure
 // code with the reason recorded.  Makes no CUDA call.

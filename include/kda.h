@@ -267,7 +267,7 @@ enum kda_elem_type { KDA_ELEM_BF16 = 0, KDA_ELEM_FP16 = 1 };
 typedef struct kda_latent_cache {
     int32_t rank, rope, page_size, layers;
     int32_t dtype;             /* enum kda_elem_type */
-    int32_t reserved;          /* 0 */
+    int32_t reserved;          /* 0 (kda_kv_cache_pages() fills in another value, for the kda_pages_* calls alone) */
     int64_t num_pages;
     int64_t layer_stride;      /* elements from a page's copy in one layer to that in the next */
     int64_t page_stride;       /* elements from one page to the next */
@@ -429,6 +429,173 @@ KDA_API int kda_pages_copy(const kda_latent_cache *cache, int32_t n, const int32
                            int32_t *dev_status, kda_stream_t stream);
 
 /*
+ * Grouped-query attention over the same pool of pages, for a hybrid whose other layers are not latent ones: H query heads
+ * share `heads` key-value heads, query head h reading key-value head h / (H / heads).
+ *
+ *     s_j = scale q . k_j ,   o = sum_j softmax(s)_j v_j
+ *
+ * A page holds page_size tokens of one layer in one contiguous piece of 16-bit words:
+ *   keys    [heads][page_size][head_dim]
+ *   values  [heads][page_size][head_dim]
+ *   stats   [heads][2][page_size] (only when `stats` is 1): a fp32 sum of attention weights, and an int32 position, of
+ *           each token and head.  kda_kv_append sets them (0 and the token's position), kda_kv_decode adds to the sums,
+ *           kda_kv_evict decides by them.
+ * so heads page_size (2 head_dim + 4 stats) words, whatever the page_size.  Layers and pages may have any stride (16-byte
+ * aligned, not overlapping).  Supported: head_dim a multiple of 8, 16 to 256; heads 1 to 128; page_size 16, 32 or a
+ * multiple of 64 up to 1024; bf16 and fp16.
+ * Tables, row numbers and reference counts are the page pool's (kda_page_table).  The kda_pages_* calls work on these pages
+ * through kda_kv_cache_pages(), which describes them as a cache of rows that they only copy.
+ */
+typedef struct kda_kv_cache {
+    int32_t heads, head_dim, page_size, layers;
+    int32_t dtype;             /* enum kda_elem_type */
+    int32_t stats;             /* 1: pages have sums and positions */
+    int64_t num_pages;
+    int64_t layer_stride;      /* 16-bit words from a page's copy in one layer to that in the next */
+    int64_t page_stride;       /* 16-bit words from one page to the next */
+    void *pages;               /* device, 16-byte aligned */
+} kda_kv_cache;
+
+/* The cache as the kda_pages_* calls take it (host only, no CUDA call): KDA_OK and *out filled, or why not. */
+KDA_API int kda_kv_cache_pages(const kda_kv_cache *cache, kda_latent_cache *out);
+
+/*
+ * Rotary positions.  Pair i of dim / 2 turns by the angle a = position * theta_i:
+ *     y1 = scale (x1 cos a - x2 sin a),   y2 = scale (x2 cos a + x1 sin a)
+ * The pairs are the channels offset + i and offset + dim/2 + i (interleaved 0: halves), or offset + 2i and offset + 2i + 1
+ * (interleaved 1); the other channels of a head stay as they are.  turns[i] is theta_i as a fraction of a full turn, times
+ * 2^64: position * turns[i] modulo 2^64 is then the exact fraction of a turn at any int32 position, so far positions are
+ * as precise as near ones (the error of theta_i itself, 2^-53 of it, is all that grows).
+ */
+typedef struct kda_rope {
+    int32_t dim, offset;       /* dim even, 2 to 256 */
+    int32_t interleaved;       /* 0 or 1 */
+    float scale;               /* not 0; 1 where a model does not say otherwise */
+    const uint64_t *turns;     /* device [dim / 2] */
+} kda_rope;
+
+/* How theta_i = base^(-2i / dim) is changed for contexts longer than the trained one. */
+enum kda_rope_scaling {
+    KDA_ROPE_PLAIN = 0,
+    KDA_ROPE_LINEAR = 1,       /* theta_i / factor */
+    KDA_ROPE_NTK = 2,          /* base * factor^(dim / (dim - 2)) in the place of base */
+    KDA_ROPE_PARTS = 3         /* with r = original theta_i / 2 pi (turns within the trained length) and
+                                * g = (r - low) / (high - low) clamped to 0..1:  theta_i (g + (1 - g) / factor) */
+};
+
+/* Host only: turns (host [dim / 2]) of a base and a scaling; factor at least 1, 0 < original and 0 <= low < high for
+ * KDA_ROPE_PARTS, ignored elsewhere.  kda_rope_turns_of: of any count frequencies in radians a position, for scalings that
+ * give them one by one (each finite, not negative, below 2^20). */
+KDA_API int kda_rope_turns(int32_t dim, double base, int32_t scaling, double factor, double original, double low,
+                           double high, uint64_t *turns);
+KDA_API int kda_rope_turns_of(int32_t count, const double *theta, uint64_t *turns);
+
+/*
+ * Rotates x [num_tokens][H][D] into out (same shape): the queries or keys of a prompt, the rotary part of latent
+ * attention's queries (offset = nope) or rows (H 1).  inverse 1: by -a, the gradient of the rotation (times scale), and
+ * with scale 1 what brings rotated keys back.
+ *   positions  device [num_tokens] int32, any values
+ *   x, out     device, of one type (dtype, enum kda_elem_type), with token and head strides in elements (multiples of 8),
+ *              16-byte aligned.  out may be x itself (the same address and strides): then only the rotated channels are
+ *              written; else out gets all D channels and may not overlap x.
+ * The angle is exact to 2^-32 of a turn, sine, cosine and products fp32, rounded once to the type.
+ * D a multiple of 8 up to 1024, H 1 to 1024, offset + dim <= D.
+ */
+KDA_API int kda_rope_apply(const kda_rope *rope, int32_t dtype, int64_t num_tokens, int32_t H, int32_t D,
+                           const int32_t *positions, int32_t inverse, const void *x, int64_t x_token_stride,
+                           int64_t x_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride,
+                           kda_stream_t stream);
+
+/*
+ * Writes the keys and values of new tokens of n sequences into one layer, as kda_latent_append does (rows, cu_tokens, lens
+ * and what is flagged are as there).  In the same launch keys are rotated on their way (rope not NULL), sums set to 0 and
+ * positions stored (a cache with stats), and the tokens' queries rotated (q not NULL, which needs rope) from q into q_out.
+ *   k, v       device [num_tokens][heads][head_dim], q [num_tokens][H][head_dim], the cache's type, at the given token and
+ *              head strides (elements, multiples of 8), 16-byte aligned: parts of one projection's output, for example
+ *   positions  device [num_tokens] int32; NULL only without rope and stats
+ *   q_out      device [num_tokens][H][head_dim] contiguous, 16-byte aligned; or q itself (its address, with contiguous
+ *              strides).  Queries of all tokens before cu_tokens[n] are rotated, those of padding entries and of sequences
+ *              with a bad row or page, too; rows behind cu_tokens[n] and those of flagged cu_tokens are left as they were.
+ * rope->offset + rope->dim <= head_dim; H 1 to 1024.  No two tokens of a call may go to the same place.
+ */
+KDA_API int kda_kv_append(const kda_kv_cache *cache, int32_t layer, const kda_page_table *pt, int32_t n,
+                          const int32_t *rows, const int32_t *cu_tokens, int64_t num_tokens, const void *k,
+                          int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                          int64_t v_head_stride, const int32_t *positions, const kda_rope *rope, int32_t H, const void *q,
+                          int64_t q_token_stride, int64_t q_head_stride, void *q_out, int32_t *dev_status,
+                          kda_stream_t stream);
+
+/* Most query tokens per sequence of one kda_kv_decode call, and most query heads. */
+#define KDA_KV_MAX_TOKENS 64
+#define KDA_KV_MAX_HEADS 256
+
+/* Bytes of device workspace kda_kv_decode needs on the current device for these sizes (0 for unsupported ones).  max_slots:
+ * 0 when weights are not added up, else a bound on the sum of lens over the call's sequences.  What is enough for some n,
+ * max_tokens and max_slots is enough for smaller ones, too. */
+KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t H, int32_t n, int32_t max_tokens,
+                                             int64_t max_slots);
+
+/*
+ * Attention of n sequences' newest tokens over one layer of the paged cache: a decode step (one token a sequence) or the
+ * verification of drafted tokens, whose keys and values are in the cache already.  rows, cu_tokens, max_tokens, tree_mask,
+ * scale, lse, who sees what, padding entries, empty rows and flags are kda_latent_decode's.
+ *   q          device [num_tokens][H][head_dim], the cache's type, at the given token and head strides (elements,
+ *              multiples of 8), 16-byte aligned; H a multiple of the cache's heads
+ *   out        device [num_tokens][H][head_dim] contiguous, the cache's type, 16-byte aligned
+ *   add_weights  1 (a cache with stats): each cached token's sum becomes weight_decay * sum + the weights that the
+ *              sequence's queries give it in this call, summed over the query tokens and over the query heads that share
+ *              its key-value head.  weight_decay from 0 to 1; max_slots as the workspace was asked for.  Shared pages
+ *              (refcount above 1) are never written, so their tokens' sums stay; refcount may not be NULL then.  No table
+ *              row may appear twice in such a call.  Sequences whose slots pass max_slots, added up in order, are
+ *              flagged (KDA_DEV_BAD_SEQLENS) and leave their sums as they were, their outputs are as always.  A query
+ *              whose lse is NaN adds nothing.
+ * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so do the
+ * queries of a sequence with a bad row or length (flagged); a bad page's tokens read as zero keys and values (flagged).
+ * Sequences with bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Tokens that a query does not see
+ * do not matter to it, whatever they hold (NaN too).  A seen key whose score is +infinity or NaN makes the query's outputs
+ * and lse NaN (-infinity: weight 0); a seen value that is not finite makes its channel NaN or infinite, and where it is one
+ * of several drafted tokens (nq above 1, or a tree_mask) all outputs and lse of the queries that see it NaN.
+ * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 relative to
+ * themselves down to 2^-29 of the largest of their part of the row, by up to 2^-40 of it below), outputs at the end.  Results
+ * do not depend on the other sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all
+ * lengths of the call and on the GPU's number of multiprocessors.  The workspace need not be initialised and keeps nothing
+ * between calls; calls that overlap on the GPU need one each.
+ * max_tokens <= KDA_KV_MAX_TOKENS, H <= KDA_KV_MAX_HEADS, n <= 65535.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs
+ * then are undefined).
+ */
+KDA_API int kda_kv_decode(const kda_kv_cache *cache, int32_t layer, const kda_page_table *pt, int32_t n,
+                          const int32_t *rows, const int32_t *cu_tokens, int64_t num_tokens, int32_t max_tokens,
+                          int32_t H, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                          const uint64_t *tree_mask, float scale, void *out, float *lse, int32_t add_weights,
+                          float weight_decay, int64_t max_slots, void *workspace, size_t workspace_bytes,
+                          int32_t *dev_status, kda_stream_t stream);
+
+/* Most tokens of a row that kda_kv_evict takes. */
+#define KDA_KV_EVICT_MAX_LEN (1 << 20)
+
+/*
+ * Eviction by accumulated attention weight, for n sequences, in all layers: of the len = lens[rows[i]] tokens of its row
+ * each layer and key-value head keeps keep[i] of its own, in this order:
+ *   1. protected ones: position below `first` (the beginning that most queries look at), position at or above since[i] (the
+ *      newest ones), or on a shared page (refcount above 1: those are never written);
+ *   2. larger sums (a NaN counts as less than anything);
+ *   3. lower slots.
+ * The i-th kept token behind the first keep[i] slots (ascending) moves, with its sum and position, to the i-th slot among
+ * them whose token is dropped (ascending); what is behind keep[i] slots then is no longer needed: kda_pages_truncate with
+ * new_lens ends the call's work.  The order of slots is no longer that of positions, which attention does not mind: keys are
+ * rotated when they are stored.  lens, tables and reference counts are read only.
+ *   rows      device [n] int32 or NULL (row i); -1 = a padding entry
+ *   keep      device [n] int32, not negative; a row of at most keep[i] tokens stays as it is
+ *   since     device [n] int32, or NULL (nothing is newest)
+ *   new_lens  device [n] int32: min(len, keep[i]); 0 for padding entries; len for rows that are flagged and left as they
+ *             are: a bad length or page, a row longer than KDA_KV_EVICT_MAX_LEN (0 for a bad row or length)
+ * Flags: KDA_DEV_BAD_SLOT, _SEQLENS, _PAGE.  No row may appear twice in a call.  n <= 65535.
+ */
+KDA_API int kda_kv_evict(const kda_kv_cache *cache, const kda_page_table *pt, int32_t n, const int32_t *rows,
+                         const int32_t *keep, int32_t first, const int32_t *since, int32_t *new_lens, int32_t *dev_status,
+                         kda_stream_t stream);
+
+/*
  * Host-side prefix index and retention policies ("A Preview of Production-Scale Kimi K3 Support on vLLM",
  * section "The Hardest Part: Prefix Caching for KDA": chained fine-grained hashes, copy-on-write of a
  * cached partial state into a private destination, deferred same-step reuse; "vLLM Kimi K3 Support",
@@ -487,8 +654,8 @@ KDA_API const char *kda_status_string(int status);
 
 /* What the last failing call of the calling host thread rejected ("decode: q, k, v, a and z must be
  * 16-byte aligned", "prefill launch: <CUDA error text>", ...), or "" when the last call of the thread to
- * kda_decode_step, kda_prefill_chunked(_noalloc), kda_resume_from_slot, kda_check_slots, a kda_latent_* or a
- * kda_pages_* function succeeded.  The
+ * kda_decode_step, kda_prefill_chunked(_noalloc), kda_resume_from_slot, kda_check_slots, a kda_latent_*, a kda_kv_*,
+ * a kda_rope_* or a kda_pages_* function succeeded.  The
  * string belongs to the library and stays valid until the thread's next such call.  Library-side record
  * only; nothing in the pages defines it. */
 KDA_API const char *kda_last_error_string(void);
