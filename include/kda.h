@@ -556,7 +556,7 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  * and lse NaN (-infinity: weight 0); a seen value that is not finite makes its channel NaN or infinite, and where it is one
  * of several drafted tokens (nq above 1, or a tree_mask) all outputs and lse of the queries that see it NaN.
  * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 relative to
- * themselves down to 2^-29 of the largest of their part of the row, by up to 2^-40 of it below), outputs at the end.  Results
+ * themselves down to 2^-28 of the largest of their part of the row, by up to 2^-39 of it below), outputs at the end.  Results
  * do not depend on the other sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all
  * lengths of the call and on the GPU's number of multiprocessors.  The workspace need not be initialised and keeps nothing
  * between calls; calls that overlap on the GPU need one each.
