@@ -4,15 +4,19 @@
 // key is all ones if it is protected and else its sum, as 32 bits in the order of the numbers.  Units share nothing, so each
 // is one CTA, or one cluster of CTAs that divide its slots where there are few units.
 //
-//   select  the keep-th largest key by its digits, 11 + 11 + 10 bits: a histogram in shared memory for each (atomics on
-//           counts: their order does not matter), summed over the cluster; ties go to the lowest slots
+//   select  the keep-th largest pair of key and slot (lower slots count as larger) byte by byte: a histogram of 256 bins in
+//           shared memory (four copies, so that lanes with equal bytes meet less; atomics on counts: their order does not
+//           matter), summed over the cluster.  It ends when a bin is taken whole, or when a bin has so few pairs that each
+//           can be compared with all others
 //   mark    one bit a slot, kept or not, in every CTA of the cluster; prefix sums over blocks of 256 slots of the holes (dropped,
-//           below keep) and of the sources (kept, at or behind keep), of which there are as many
-//   move    a warp finds 32 holes and 32 sources at a time by their ranks, and copies the rows, 8 loads a lane in flight
+//           below keep) and of the sources (kept, at or behind keep), of which there are as many; both listed in order, where
+//           the keys were
+//   move    a warp copies the rows of up to 32 pairs from the lists, several loads a lane in flight
 //
 // Filling holes instead of closing them up moves the fewest rows there are (bringing 2,112 tokens back to 2,048 moves 64 at
 // most; closing up would move nearly all), and no row that is read is written, so nothing has to wait for anything.
-// Bound by bytes: 8 a slot to select, twice 4 head_dim + 8 for each row that moves.
+// Bound by bytes: 8 a slot to select, twice 4 head_dim + 8 for each row that moves; with short rows by the latency of a unit's
+// steps, which is why CTAs are small enough for several on a multiprocessor.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -24,12 +28,13 @@ namespace kv {
 
 namespace cg = cooperative_groups;
 
-constexpr int ET = 512;             // threads
-constexpr int EW = ET / 32;
-constexpr int BINS = 2048;
+constexpr int BINS = 256, COPIES = 4;
+constexpr int FEW = 128;            // pairs that are compared with one another
 constexpr int BLOCK = 256;          // slots of a prefix sum's block
-constexpr int KEYS = 12288;         // keys of a CTA that stay in shared memory; more are made again from the pages
+constexpr int KEYS = 16384;         // most keys of a CTA that stay in shared memory; more are made again from the pages
 constexpr int MAX_CLUSTER = 8;
+constexpr int UNROLL = 4;           // 16-byte words of a lane in flight while rows move
+constexpr int AHEAD = 2;            // groups of four slots of a thread in flight while keys are read
 constexpr uint32_t PROTECTED = 0xffffffffu;
 
 // Blocks that `words` words of marks have, rounded up to a multiple of 4.
@@ -49,100 +54,67 @@ __device__ __forceinline__ uint32_t order_of(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Keys of slots j .. j + 3 (j a multiple of 4: one page has them, as pages are multiples of 16); 0 behind the end.
-__device__ __forceinline__ uint4 keys_at(const KvEvictArgs &a, const Unit &u, int j) {
-    const int32_t p = u.trow[j / a.c.page_size];
-    const bool shared = a.t.refcount[p] > 1;
+// Keys of slots j .. j + 3 (j a multiple of 4: one page has them, as pages are multiples of 16) of page p; 0 behind the end.
+struct Four {
+    float4 w;
+    int4 pos;
+    int32_t shared;
+};
+__device__ __forceinline__ Four read_four(const KvEvictArgs &a, const Unit &u, int j, int32_t p) {
     const uint16_t *st = u.base + p * a.c.page_stride + stats_at(a.c, u.head) + 2 * (j % a.c.page_size);
-    const float4 w = *reinterpret_cast<const float4 *>(st);
-    const int4 pos = *reinterpret_cast<const int4 *>(st + 2 * a.c.page_size);
+    Four f;
+    f.w = *reinterpret_cast<const float4 *>(st);
+    f.pos = *reinterpret_cast<const int4 *>(st + 2 * a.c.page_size);
+    f.shared = a.t.refcount[p];
+    return f;
+}
+__device__ __forceinline__ uint4 keys_of(const KvEvictArgs &a, const Unit &u, int j, const Four &f) {
     auto key = [&](int k, float x, int32_t at) {
-        if (j + k >= u.len) return 0u;
-        return shared || at < a.first || at >= u.since ? PROTECTED : order_of(x);
+        if (j + k >= u.len) return 0u;  // as a pair with its slot less than all that exist, and so never kept
+        return f.shared > 1 || at < a.first || at >= u.since ? PROTECTED : order_of(x);
     };
-    return make_uint4(key(0, w.x, pos.x), key(1, w.y, pos.y), key(2, w.z, pos.z), key(3, w.w, pos.w));
+    return make_uint4(key(0, f.w.x, f.pos.x), key(1, f.w.y, f.pos.y), key(2, f.w.z, f.pos.z), key(3, f.w.w, f.pos.w));
 }
 
-// The k-th (from 0) set bit of x.
-__device__ __forceinline__ int nth_bit(uint32_t x, int k) {
-    int at = 0;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-        const int c = __popc(x & ((1u << w) - 1));
-        if (k >= c) {
-            k -= c;
-            x >>= w;
-            at += w;
-        }
-    }
-    return at;
-}
+// The last of the keep-th largest: pairs of key and inverted slot whose bytes under the masks are as large stay.
+struct Border {
+    uint32_t key, key_mask, slot, slot_mask;
+};
 
-// The slot with rank r among the marked ones, by prefix sums of blocks and the words f(w) of marks.
-template <class F>
-__device__ __forceinline__ int slot_of(const int32_t *before, int blocks, int r, F f) {
-    int lo = 0, hi = blocks;  // before[lo] <= r < before[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (before[mid] <= r)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    r -= before[lo];
-    int w = lo * (BLOCK / 32);
-    uint32_t x = f(w);
-    for (int c = __popc(x); r >= c; c = __popc(x)) {
-        r -= c;
-        x = f(++w);
-    }
-    return w * 32 + nth_bit(x, r);
-}
-
-// Exclusive prefix sum over the CTA; total gets the sum.  part: EW + 1 ints that nothing else uses meanwhile.
-__device__ __forceinline__ int cta_scan(int v, int *part, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(FULL, s, o);
-        if (lane >= o) s += t;
-    }
-    if (lane == 31) part[warp] = s;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < EW; ++w) {
-        if (w < warp) before += part[w];
-        total += part[w];
-    }
-    __syncthreads();
-    return before + s - v;
-}
-
-__global__ void __launch_bounds__(ET) kda_kv_evict_kernel(const KvEvictArgs a, int words_max) {
-    // [words_max] marks, holes and sources before each block of them, histogram, keys; each a multiple of 16 bytes
+// keys_max: keys of a CTA that there is room for.
+template <int ET>
+__global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(const KvEvictArgs a, int words_max, int keys_max) {
+    constexpr int EW = ET / 32;
+    // [words_max] marks, holes and sources before each block of them, keys; each a multiple of 16 bytes
     extern __shared__ __align__(16) uint32_t smem[];
-    __shared__ int part[EW];
-    __shared__ int found[4];   // bin, count above it, its own count
-    __shared__ int ties;       // this CTA's tokens whose key is the last one taken
+    __shared__ __align__(16) int32_t hist[2][BINS * COPIES];  // of passes in turn
+    __shared__ int32_t sums[BINS];
+    __shared__ uint64_t few[FEW];
+    __shared__ int found[3];   // bin, count above it, its own count
+    __shared__ int listed;     // pairs in few (of the cluster's first CTA)
+    __shared__ int spoiled;    // this CTA's slots have a bad page
+    __shared__ uint64_t part[EW];
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int blocks_max = blocks_of(words_max);
     uint32_t *marks = smem;
     int32_t *holes = reinterpret_cast<int32_t *>(marks + words_max), *sources = holes + blocks_max;
-    int32_t *hist = sources + blocks_max;
-    uint32_t *kept = reinterpret_cast<uint32_t *>(hist + BINS);
+    uint32_t *kept = reinterpret_cast<uint32_t *>(sources + blocks_max);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto sync_all = [&] {
+        if (C > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+    if (tid == 0) listed = spoiled = 0;
 
     wait_for_previous();
     allow_dependent_launch();
-    int64_t unit = blockIdx.x / C;
+    const uint32_t unit = blockIdx.x / C, above_head = unit / a.c.heads;
     Unit u;
-    u.head = (int)(unit % a.c.heads);
-    unit /= a.c.heads;
-    const int layer = (int)(unit % a.c.layers), i = (int)(unit / a.c.layers);
+    u.head = (int)(unit - above_head * a.c.heads);
+    const int i = (int)(above_head / a.c.layers), layer = (int)(above_head - i * a.c.layers);
     const bool tells = layer == 0 && u.head == 0 && rank == 0 && tid == 0;
     u.base = a.c.pages + layer * a.c.layer_stride;
     const int32_t row = a.rows ? a.rows[i] : i;
@@ -157,7 +129,8 @@ __global__ void __launch_bounds__(ET) kda_kv_evict_kernel(const KvEvictArgs a, i
     u.keep = a.keep[i];
     u.since = a.since ? a.since[i] : INT32_MAX;
     u.trow = a.t.table + (int64_t)row * a.t.max_pages;
-    const bool bad_len = u.len < 0 || u.len > (int64_t)a.t.max_pages * a.c.page_size;
+    const int ps = a.c.page_size;
+    const bool bad_len = u.len < 0 || u.len > (int64_t)a.t.max_pages * ps;
     if (bad_len || u.keep < 0 || u.len <= u.keep || u.len > KDA_KV_EVICT_MAX_LEN) {
         if (tells) {
             a.new_lens[i] = bad_len ? 0 : u.len;
@@ -165,186 +138,325 @@ __global__ void __launch_bounds__(ET) kda_kv_evict_kernel(const KvEvictArgs a, i
         }
         return;
     }
-    // a bad page anywhere leaves the whole row as it is, in every layer and head alike
-    const int pages = (u.len + a.c.page_size - 1) / a.c.page_size;
-    bool bad = false;
-    for (int p = tid; p < pages; p += ET) bad |= !page_ok(a.t, u.trow[p]);
-    if (__syncthreads_or(bad)) {
-        if (tells) {
-            a.new_lens[i] = u.len;
-            set_status(a.status, KDA_DEV_BAD_PAGE);
-        }
-        return;
-    }
-    if (tells) a.new_lens[i] = u.keep;
-    if (u.keep == 0) return;
 
-    // this CTA's slots [s0, s1), whole words of marks
+    // this CTA's slots [s0, s1), whole blocks of marks
     const int per = ((u.len + C - 1) / C + BLOCK - 1) / BLOCK * BLOCK;
     const int s0 = min(u.len, rank * per), s1 = min(u.len, s0 + per);
-    const bool stay = s1 - s0 <= KEYS;
-    for (int j = s0 + 4 * tid; j < s1; j += 4 * ET)
-        if (stay) *reinterpret_cast<uint4 *>(kept + j - s0) = keys_at(a, u, j);
-    auto keys = [&](int j) { return stay ? *reinterpret_cast<const uint4 *>(kept + j - s0) : keys_at(a, u, j); };
+    const bool stay = s1 - s0 <= keys_max;
+    bool bad = false;
+    // f(j, keys of slots j .. j + 3) for this thread's slots, from the pages or from shared memory
+    auto from_pages = [&](auto f) {
+        for (int j0 = s0 + 4 * tid; j0 < s1; j0 += 4 * ET * AHEAD) {
+            int32_t p[AHEAD];
+            Four x[AHEAD];
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e) {
+                const int j = j0 + e * 4 * ET;
+                p[e] = j < s1 ? u.trow[j / ps] : 0;
+            }
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e) {
+                const int j = j0 + e * 4 * ET;
+                if (!page_ok(a.t, p[e])) {
+                    bad = true;
+                    p[e] = 0;
+                }
+                if (j < s1) x[e] = read_four(a, u, j, p[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e) {
+                const int j = j0 + e * 4 * ET;
+                if (j < s1) f(j, keys_of(a, u, j, x[e]));
+            }
+        }
+    };
+    auto each = [&](auto f) {
+        if (!stay) return from_pages(f);
+        for (int j = s0 + 4 * tid; j < s1; j += 4 * ET) f(j, *reinterpret_cast<const uint4 *>(kept + j - s0));
+    };
 
-    // the keep-th largest key, digit by digit: `need` of the keys that begin with `prefix` are among them
-    uint32_t prefix = 0, mask = 0;
-    int need = u.keep, equal = 0;
-    for (int digit = 0; digit < 3; ++digit) {
-        const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bins = digit == 2 ? 1024 : 2048;
-        for (int b = tid; b < BINS; b += ET) hist[b] = 0;
+    // `need` of the pairs that begin as the bytes found so far are among those that stay
+    Border t = {0, 0, 0, 0};
+    int need = max(u.keep, 1);  // (a row that keeps nothing has its pages looked at, too)
+    for (int pass = 0; pass < 7; ++pass) {
+        int32_t *h = hist[pass & 1];
+        if (tid < BINS) reinterpret_cast<int4 *>(h)[tid] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        for (int j = s0 + 4 * tid; j < s1; j += 4 * ET) {
-            const uint4 k = keys(j);
+        const int shift = pass < 4 ? 24 - 8 * pass : 16 - 8 * (pass - 4);
+        int32_t *h_lane = h + (lane & (COPIES - 1));
+        auto count = [&](int, uint4 k) {
             const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (j + e < s1 && (x[e] & mask) == prefix) atomicAdd(hist + ((x[e] >> shift) & (bins - 1)), 1);
-        }
-        cluster.sync();
-        // bins from the top: thread t has bins [4t, 4t + 4) counted from the largest
-        int c[BINS / ET], mine = 0;
+                if ((x[e] & t.key_mask) == t.key) atomicAdd(h_lane + ((x[e] >> shift) & 255) * COPIES, 1);
+        };
+        auto count_slots = [&](int j, uint4 k) {
+            const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-        for (int e = 0; e < BINS / ET; ++e) {
-            const int b = BINS - 1 - (tid * (BINS / ET) + e);
-            c[e] = 0;
-            for (int r = 0; r < C; ++r) c[e] += *cluster.map_shared_rank(hist + b, r);
-            mine += c[e];
-        }
-        int total, above = cta_scan(mine, part, total);
-#pragma unroll
-        for (int e = 0; e < BINS / ET; ++e) {
-            if (above < need && need <= above + c[e]) {
-                found[0] = BINS - 1 - (tid * (BINS / ET) + e);
-                found[1] = above;
-                found[2] = c[e];
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t slot = 0xffffffu - (j + e);
+                if (x[e] == t.key && (slot & t.slot_mask) == t.slot) atomicAdd(h_lane + ((slot >> shift) & 255) * COPIES, 1);
             }
-            above += c[e];
+        };
+        if (pass == 0) {
+            from_pages([&](int j, uint4 k) {
+                if (stay) *reinterpret_cast<uint4 *>(kept + j - s0) = k;
+                count(j, k);
+            });
+            if (bad) spoiled = 1;
+        } else if (pass < 4) {
+            each(count);
+        } else {
+            each(count_slots);
         }
-        cluster.sync();  // all have read the histograms
-        prefix |= (uint32_t)found[0] << shift;
-        mask |= (uint32_t)(bins - 1) << shift;
-        need -= found[1];
-        equal = found[2];
+        sync_all();
+        if (C > 1) {
+            if (tid < BINS) {
+                int c = 0;
+#pragma unroll
+                for (int r = 0; r < MAX_CLUSTER; ++r)
+                    if (r < C) {
+                        const int4 x = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(h + tid * COPIES, r));
+                        c += x.x + x.y + x.z + x.w;
+                    }
+                sums[tid] = c;
+            }
+            __syncthreads();
+        }
+        if (warp == 0) {
+            // a lane has eight bins, counted from the largest
+            int c[BINS / 32], mine = 0;
+#pragma unroll
+            for (int e = 0; e < BINS / 32; ++e) {
+                const int bin = BINS - 1 - (lane * (BINS / 32) + e);
+                if (C > 1) {
+                    c[e] = sums[bin];
+                } else {
+                    const int4 x = reinterpret_cast<const int4 *>(h)[bin];
+                    c[e] = x.x + x.y + x.z + x.w;
+                }
+                mine += c[e];
+            }
+            int above = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(FULL, above, o);
+                if (lane >= o) above += x;
+            }
+            above -= mine;
+#pragma unroll
+            for (int e = 0; e < BINS / 32; ++e) {
+                if (above < need && need <= above + c[e]) {
+                    found[0] = BINS - 1 - (lane * (BINS / 32) + e);
+                    found[1] = above;
+                    found[2] = c[e];
+                }
+                above += c[e];
+            }
+        }
         __syncthreads();
+        if (pass == 0) {
+            const bool wrong = lane < C && *cluster.map_shared_rank(&spoiled, lane);
+            if (__any_sync(FULL, wrong)) {  // the same in all CTAs of the row: it stays as it is, in every layer and head
+                sync_all();
+                if (tells) {
+                    a.new_lens[i] = u.len;
+                    set_status(a.status, KDA_DEV_BAD_PAGE);
+                }
+                return;
+            }
+        }
+        if (pass < 4) {
+            t.key |= (uint32_t)found[0] << shift;
+            t.key_mask |= 255u << shift;
+        } else {
+            t.slot |= (uint32_t)found[0] << shift;
+            t.slot_mask |= 255u << shift;
+        }
+        need -= found[1];
+        const int size = found[2];
+        if (need == size) break;  // all that begin so stay
+        if (size <= FEW) {
+            each([&](int j, uint4 k) {
+                const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t slot = 0xffffffu - (j + e);
+                    if ((x[e] & t.key_mask) == t.key && (slot & t.slot_mask) == t.slot) {
+                        const int at = atomicAdd(cluster.map_shared_rank(&listed, 0), 1);
+                        for (int r = 0; r < C; ++r) cluster.map_shared_rank(few, r)[at] = (uint64_t)x[e] << 32 | slot;
+                    }
+                }
+            });
+            sync_all();
+            if (tid < size) {
+                const uint64_t mine = few[tid];
+                int larger = 0;
+                for (int k = 0; k < size; ++k) larger += few[k] > mine;
+                if (larger == need - 1) {
+                    found[0] = (int)(uint32_t)(mine >> 32);
+                    found[1] = (int)(uint32_t)mine;
+                }
+            }
+            __syncthreads();
+            t = Border{(uint32_t)found[0], 0xffffffffu, (uint32_t)found[1], 0xffffffu};
+            break;
+        }
+    }
+    if (tells) a.new_lens[i] = u.keep;
+    if (u.keep == 0) {
+        sync_all();
+        return;
     }
 
-    // marks of this CTA's slots: larger keys, and the first `need` of the equal ones
-    const bool some = need < equal;  // not all of the equal ones: their order counts
-    int mine = 0, before = 0;
-    if (some) {
-        for (int j = s0 + 4 * tid; j < s1; j += 4 * ET) {
-            const uint4 k = keys(j);
-            mine += (k.x == prefix) + (j + 1 < s1 && k.y == prefix) + (j + 2 < s1 && k.z == prefix) +
-                    (j + 3 < s1 && k.w == prefix);
-        }
-        int total;
-        cta_scan(mine, part, total);
-        if (tid == 0) ties = total;
-        cluster.sync();
-        for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&ties, r);
-    }
+    // marks: larger pairs, and those that begin as the last one does
     for (int j0 = s0; j0 < s1; j0 += 4 * ET) {
         const int j = j0 + 4 * tid;
-        uint32_t bits = 0, same = 0;
-        if (j < s1) {
-            const uint4 k = keys(j);
+        uint32_t word = 0;
+        auto mark = [&](int, uint4 k) {
             const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < s1) {
-                    bits |= (uint32_t)(x[e] > prefix) << e;
-                    same |= (uint32_t)(x[e] == prefix) << e;
-                }
-        }
-        if (some) {
-            int total;
-            int at = before + cta_scan(__popc(same), part, total);
-            before += total;
-            for (int e = 0; e < 4; ++e)
-                if ((same >> e) & 1) bits |= (uint32_t)(at++ < need) << e;
-        } else {
-            bits |= same;
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t key = x[e] & t.key_mask, slot = (0xffffffu - (j + e)) & t.slot_mask;
+                word |= (uint32_t)(key > t.key || (key == t.key && slot >= t.slot)) << e;
+            }
+        };
+        if (j < s1) {
+            if (stay)
+                mark(j, *reinterpret_cast<const uint4 *>(kept + j - s0));
+            else
+                mark(j, keys_of(a, u, j, read_four(a, u, j, u.trow[j / ps])));
         }
         // eight threads' bits are a word, which every CTA of the cluster gets
-        uint32_t word = bits << (4 * (lane & 7));
+        word <<= 4 * (lane & 7);
         word |= __shfl_xor_sync(FULL, word, 1);
         word |= __shfl_xor_sync(FULL, word, 2);
         word |= __shfl_xor_sync(FULL, word, 4);
         if ((j & ~31) < s1)
             for (int r = lane & 7; r < C; r += 8) *cluster.map_shared_rank(marks + j / 32, r) = word;
     }
-    cluster.sync();  // all marks are there, all sums have been read
+    sync_all();  // all marks are there, all sums have been read, nobody reads another CTA's memory any more
 
     const int nb = (u.len + BLOCK - 1) / BLOCK, nw = (u.len + 31) / 32;
     const int kw = u.keep / 32;
     const uint32_t low = (1u << (u.keep % 32)) - 1;  // slots of word kw that lie below keep
     auto hole = [&](int w) { return w < kw ? ~marks[w] : w == kw ? ~marks[w] & low : 0u; };
     auto source = [&](int w) { return w < kw || w >= nw ? 0u : w == kw ? marks[w] & ~low : marks[w]; };
-    int moves = 0, unused = 0;
-    for (int b0 = 0; b0 < nb; b0 += ET) {
-        const int b = b0 + tid;
-        int nh = 0, ns = 0;
-        if (b < nb)
+    // marks of block b: holes in the low 32 bits, sources in the high ones
+    auto marked = [&](int b) {
+        uint32_t nh = 0, ns = 0;
 #pragma unroll
-            for (int w = b * (BLOCK / 32); w < (b + 1) * (BLOCK / 32); ++w) {
-                if (w < nw) {
-                    nh += __popc(hole(w));
-                    ns += __popc(source(w));
-                }
+        for (int q = 0; q < 2; ++q) {
+            const int w = b * (BLOCK / 32) + 4 * q;
+            const uint4 m = *reinterpret_cast<const uint4 *>(marks + w);
+            const uint32_t x[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t is = w + e < nw ? x[e] : 0u;
+                nh += w + e < kw ? 32 - __popc(is) : w + e == kw ? __popc(~is & low) : 0;
+                ns += w + e < kw ? 0 : w + e == kw ? __popc(is & ~low) : __popc(is);
             }
-        int th, ts;
-        const int h = cta_scan(nh, part, th), s = cta_scan(ns, part, ts);
-        if (b < nb) {
-            holes[b] = moves + h;
-            sources[b] = unused + s;
         }
-        moves += th;
-        unused += ts;
+        return (uint64_t)ns << 32 | nh;
+    };
+    uint64_t carry = 0;
+    for (int b0 = 0; b0 < nb; b0 += ET) {  // in warps that have no blocks nothing is added
+        const int b = b0 + tid;
+        const uint64_t mine = b < nb ? marked(b) : 0;
+        uint64_t incl = mine;
+        if (b0 + warp * 32 < nb) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t x = __shfl_up_sync(FULL, incl, o);
+                if (lane >= o) incl += x;
+            }
+        }
+        if (lane == 31) part[warp] = incl;
+        __syncthreads();
+        uint64_t before = carry;
+        for (int v = 0; v < EW && b0 + v * 32 < nb; ++v) {
+            if (v < warp) before += part[v];
+            carry += part[v];
+        }
+        before += incl - mine;
+        if (b < nb) {
+            holes[b] = (int32_t)(uint32_t)before;
+            sources[b] = (int32_t)(before >> 32);
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
-    // moves [m0, m1) are this warp's
-    const int nwarps = C * EW, w = rank * EW + warp;
-    const int share = (moves + nwarps - 1) / nwarps, m0 = min(moves, w * share), m1 = min(moves, m0 + share);
-    const int nv = a.c.d / 8, both = 2 * nv, ps = a.c.page_size;
+    // the pairs with ranks [q0, q1) are this CTA's, in rounds of as many as the lists hold
+    const int moves = (int)(uint32_t)carry, quota = (moves + C - 1) / C, q0 = min(moves, rank * quota), q1 = min(moves, q0 + quota);
+    const int room = keys_max / 2;
+    int32_t *list = reinterpret_cast<int32_t *>(kept);  // [room] sources, [room] holes
+    // A row's key and value are `both` words of 16 bytes: to 32 lanes in turn, or several rows at once where they are 16 or less
+    const int nv = a.c.d / 8, both = 2 * nv;
+    const int width = both > 16 ? 32 : both > 8 ? 16 : both > 4 ? 8 : 4, at_once = 32 / width, sub = lane / width;
     uint16_t *keys0 = u.base + key_at(a.c, u.head);
     const int64_t values = value_at(a.c, u.head) - key_at(a.c, u.head);
-    for (int m = m0; m < m1; m += 32) {
-        const int cnt = min(32, m1 - m);
-        int64_t from = 0, to = 0;  // words before the rows' pages
-        int fs = 0, ts = 0;        // and the slots within these
-        if (lane < cnt) {
-            const int src = slot_of(sources, nb, m + lane, source), dst = slot_of(holes, nb, m + lane, hole);
-            from = u.trow[src / ps] * a.c.page_stride;
-            to = u.trow[dst / ps] * a.c.page_stride;
-            fs = src % ps;
-            ts = dst % ps;
-            const int32_t *f = reinterpret_cast<const int32_t *>(u.base + from + stats_at(a.c, u.head)) + fs;
-            int32_t *t = reinterpret_cast<int32_t *>(u.base + to + stats_at(a.c, u.head)) + ts;
-            const int32_t x = f[0], y = f[ps];
-            t[0] = x;
-            t[ps] = y;
-            from += (int64_t)fs * a.c.d;
-            to += (int64_t)ts * a.c.d;
-        }
-        constexpr int UNROLL = 8;
-        for (int v0 = 0; v0 < cnt * both; v0 += 32 * UNROLL) {
-            uint4 r[UNROLL];
-            int64_t at[UNROLL];
+    for (int r0 = q0; r0 < q1; r0 += room) {
+        const int r1 = min(q1, r0 + room);
+        // a warp has a block, a lane eight slots of it
+        for (int b = warp; b < nb; b += EW) {
+            const int w = b * (BLOCK / 32) + lane / 4, at = 8 * (lane & 3);
+            const uint32_t before = (1u << at) - 1, here = 255u << at;
 #pragma unroll
-            for (int e = 0; e < UNROLL; ++e) {
-                const int v = v0 + e * 32 + lane;
-                const int row_ = min(v / both, 31), k = v - row_ * both;
-                const int64_t f = __shfl_sync(FULL, from, row_), t = __shfl_sync(FULL, to, row_);
-                const int64_t in = (k < nv ? 0 : values) + (k < nv ? k : k - nv) * 8;
-                at[e] = v < cnt * both ? t + in : -1;
-                if (at[e] >= 0) r[e] = __ldcs(reinterpret_cast<const uint4 *>(keys0 + f + in));
+            for (int side = 0; side < 2; ++side) {
+                const int32_t *base = side ? holes : sources;
+                const int first = base[b], next = b + 1 < nb ? base[b + 1] : moves;
+                if (first >= r1 || next <= r0 || first == next) continue;
+                const uint32_t x = side ? hole(w) : source(w);
+                int k = __popc(x);  // marks of the words before, from the lanes that have these
+                k = (lane & 3) == 0 ? k : 0;
+                int incl = k;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(FULL, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                k = __shfl_sync(FULL, incl - k, lane & ~3) + first + __popc(x & before);
+                for (uint32_t mine = x & here; mine; mine &= mine - 1, ++k)
+                    if (k >= r0 && k < r1) list[side * room + k - r0] = w * 32 + __ffs(mine) - 1;
             }
-#pragma unroll
-            for (int e = 0; e < UNROLL; ++e)
-                if (at[e] >= 0) *reinterpret_cast<uint4 *>(keys0 + at[e]) = r[e];
         }
+        __syncthreads();
+        const int share = min(32, (r1 - r0 + EW - 1) / EW);
+        for (int m = r0 + warp * share; m < r1; m += EW * share) {
+            const int cnt = min(share, r1 - m);
+            int64_t from = 0, to = 0;  // words before the rows
+            if (lane < cnt) {
+                const int src = list[m - r0 + lane], dst = list[room + m - r0 + lane];
+                from = u.trow[src / ps] * a.c.page_stride;
+                to = u.trow[dst / ps] * a.c.page_stride;
+                const int32_t *f = reinterpret_cast<const int32_t *>(u.base + from + stats_at(a.c, u.head)) + src % ps;
+                int32_t *g = reinterpret_cast<int32_t *>(u.base + to + stats_at(a.c, u.head)) + dst % ps;
+                const int32_t x = f[0], y = f[ps];
+                g[0] = x;
+                g[ps] = y;
+                from += (int64_t)(src % ps) * a.c.d;
+                to += (int64_t)(dst % ps) * a.c.d;
+            }
+            for (int k = lane & (width - 1); k - (lane & (width - 1)) < both; k += 32) {
+                const int64_t in = k < nv ? k * 8 : values + (k - nv) * 8;
+                for (int n = sub; n - sub < cnt; n += UNROLL * at_once) {
+                    uint4 r[UNROLL];
+#pragma unroll
+                    for (int e = 0; e < UNROLL; ++e) {
+                        const int x = n + e * at_once;
+                        const uint16_t *f = keys0 + __shfl_sync(FULL, from, min(x, 31)) + in;
+                        if (x < cnt && k < both) r[e] = __ldcs(reinterpret_cast<const uint4 *>(f));
+                    }
+#pragma unroll
+                    for (int e = 0; e < UNROLL; ++e) {
+                        const int x = n + e * at_once;
+                        uint16_t *f = keys0 + __shfl_sync(FULL, to, min(x, 31)) + in;
+                        if (x < cnt && k < both) *reinterpret_cast<uint4 *>(f) = r[e];
+                    }
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -355,16 +467,20 @@ int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {
     const int64_t units = (int64_t)a.n * a.c.layers * a.c.heads;
     const int64_t cap = std::min<int64_t>((int64_t)a.t.max_pages * a.t.page_size, KDA_KV_EVICT_MAX_LEN);
     const int words = (int)((cap + BLOCK - 1) / BLOCK * (BLOCK / 32));
-    // CTAs of a unit: as many as there is room for, and as many as have 1,024 slots each
+    // CTAs of a unit: more where there are few units, while each has 1,024 slots or more
     int C = 1;
-    while (C < MAX_CLUSTER && units * C * 2 <= (int64_t)current_device_sms() * 2 && cap > (int64_t)C * 1024) C *= 2;
-    const size_t smem = 4 * ((size_t)words + 2 * blocks_of(words) + BINS + KEYS);
-    auto k = kda_kv_evict_kernel;
-    static std::atomic<uint64_t> prepared{0};
-    if (allow_smem(k, prepared) == cudaSuccess) {
+    while (C < MAX_CLUSTER && units * C < (int64_t)current_device_sms() * 4 && cap > (int64_t)C * 1024) C *= 2;
+    const int other = 4 * (words + 2 * blocks_of(words)), room = (kSmemMax - 12288 - other) / 4 / BLOCK * BLOCK;
+    const int keys = (int)std::min<int64_t>({KEYS, room, ((cap + C - 1) / C + BLOCK - 1) / BLOCK * BLOCK});
+    const size_t smem = (size_t)other + 4 * keys;
+    // where a multiprocessor has one CTA at most, larger ones
+    const bool wide = units * C <= current_device_sms();
+    static std::atomic<uint64_t> prepared[2];
+    auto k = wide ? kda_kv_evict_kernel<1024> : kda_kv_evict_kernel<256>;
+    if (allow_smem(k, prepared[wide]) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(units * C));
-        cfg.blockDim = dim3(ET);
+        cfg.blockDim = dim3(wide ? 1024 : 256);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
         cudaLaunchAttribute attr[2];
@@ -374,7 +490,7 @@ int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {
         attr[1].val.clusterDim = {(unsigned)C, 1, 1};
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        cudaLaunchKernelEx(&cfg, k, a, words);
+        cudaLaunchKernelEx(&cfg, k, a, words, keys);
     }
     return launch_result("kda_kv_evict_kernel launch");
 }
