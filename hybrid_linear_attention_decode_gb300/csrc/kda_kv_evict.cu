@@ -29,12 +29,11 @@ namespace kv {
 namespace cg = cooperative_groups;
 
 constexpr int BINS = 256, COPIES = 4;
+constexpr int SHORT = 4096;         // slots of a row for which a CTA has 128 threads
 constexpr int FEW = 128;            // pairs that are compared with one another
 constexpr int BLOCK = 256;          // slots of a prefix sum's block
 constexpr int KEYS = 16384;         // most keys of a CTA that stay in shared memory; more are made again from the pages
 constexpr int MAX_CLUSTER = 8;
-constexpr int UNROLL = 4;           // 16-byte words of a lane in flight while rows move
-constexpr int AHEAD = 2;            // groups of four slots of a thread in flight while keys are read
 constexpr uint32_t PROTECTED = 0xffffffffu;
 
 // Blocks that `words` words of marks have, rounded up to a multiple of 4.
@@ -42,16 +41,22 @@ __host__ __device__ constexpr int blocks_of(int words) { return (words / (BLOCK 
 
 struct Unit {
     const int32_t *trow;
-    int32_t len, keep, since;
-    uint16_t *base;  // the layer's pages
-    int32_t head;
+    int32_t len, keep, head;
+    uint32_t open;    // positions first .. first + open - 1 are not protected
+    uint16_t *base;   // the layer's pages
+};
+
+// Slots divided by the page size, by a multiplication: exact below 2^22 for the sizes there are (up to 1024).
+struct PageSize {
+    uint32_t size, inverse;  // inverse: 2^32 / size rounded up
+    __device__ __forceinline__ int page(int slot) const { return (int)__umulhi((uint32_t)slot, inverse); }
+    __device__ __forceinline__ int within(int slot) const { return slot - page(slot) * (int)size; }
 };
 
 // Larger for a larger sum; 0 for NaN.
 __device__ __forceinline__ uint32_t order_of(float w) {
-    if (isnan(w)) return 0;
     const uint32_t b = __float_as_uint(w + 0.f);  // -0 is 0
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    return isnan(w) ? 0 : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 // Keys of slots j .. j + 3 (j a multiple of 4: one page has them, as pages are multiples of 16) of page p; 0 behind the end.
@@ -60,8 +65,8 @@ struct Four {
     int4 pos;
     int32_t shared;
 };
-__device__ __forceinline__ Four read_four(const KvEvictArgs &a, const Unit &u, int j, int32_t p) {
-    const uint16_t *st = u.base + p * a.c.page_stride + stats_at(a.c, u.head) + 2 * (j % a.c.page_size);
+__device__ __forceinline__ Four read_four(const KvEvictArgs &a, const Unit &u, PageSize ps, int j, int32_t p) {
+    const uint16_t *st = u.base + p * a.c.page_stride + stats_at(a.c, u.head) + 2 * ps.within(j);
     Four f;
     f.w = *reinterpret_cast<const float4 *>(st);
     f.pos = *reinterpret_cast<const int4 *>(st + 2 * a.c.page_size);
@@ -69,11 +74,21 @@ __device__ __forceinline__ Four read_four(const KvEvictArgs &a, const Unit &u, i
     return f;
 }
 __device__ __forceinline__ uint4 keys_of(const KvEvictArgs &a, const Unit &u, int j, const Four &f) {
-    auto key = [&](int k, float x, int32_t at) {
-        if (j + k >= u.len) return 0u;  // as a pair with its slot less than all that exist, and so never kept
-        return f.shared > 1 || at < a.first || at >= u.since ? PROTECTED : order_of(x);
-    };
-    return make_uint4(key(0, f.w.x, f.pos.x), key(1, f.w.y, f.pos.y), key(2, f.w.z, f.pos.z), key(3, f.w.w, f.pos.w));
+    // (below `first` the difference wraps around to 2^31 - first and more, which no `open` is above)
+    const uint32_t open = f.shared > 1 ? 0u : u.open;
+    auto key = [&](float x, int32_t at) { return (uint32_t)at - (uint32_t)a.first >= open ? PROTECTED : order_of(x); };
+    uint4 k = make_uint4(key(f.w.x, f.pos.x), key(f.w.y, f.pos.y), key(f.w.z, f.pos.z), key(f.w.w, f.pos.w));
+    if (j + 3 >= u.len) {  // as a pair with its slot less than all that exist, and so never kept
+        k.w = 0;
+        if (j + 2 >= u.len) k.z = 0;
+        if (j + 1 >= u.len) k.y = 0;
+    }
+    return k;
+}
+
+// The same again, for rows whose keys shared memory does not hold: out of line, so that it is in the program once.
+__device__ __noinline__ uint4 keys_again(const KvEvictArgs &a, const Unit &u, PageSize ps, int j) {
+    return keys_of(a, u, j, read_four(a, u, ps, j, u.trow[ps.page(j)]));
 }
 
 // The last of the keep-th largest: pairs of key and inverted slot whose bytes under the masks are as large stay.
@@ -82,30 +97,38 @@ struct Border {
 };
 
 // keys_max: keys of a CTA that there is room for.
-template <int ET>
-__global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(const KvEvictArgs a, int words_max, int keys_max) {
+template <int ET, bool CLUSTER>
+__global__ void __launch_bounds__(ET, 1024 / ET) kda_kv_evict_kernel(const KvEvictArgs a, const PageSize ps, int words_max, int keys_max) {
     constexpr int EW = ET / 32;
+    constexpr int UNROLL = 4;  // 16-byte words of a lane in flight while rows move
+    constexpr int AHEAD = 2;   // groups of four slots of a thread in flight while keys are read
     // [words_max] marks, holes and sources before each block of them, keys; each a multiple of 16 bytes
     extern __shared__ __align__(16) uint32_t smem[];
-    __shared__ __align__(16) int32_t hist[2][BINS * COPIES];  // of passes in turn
-    __shared__ int32_t sums[BINS];
+    __shared__ __align__(16) int32_t hist[CLUSTER ? 2 : 1][BINS * COPIES];  // of passes in turn
+    __shared__ int32_t sums[CLUSTER ? BINS : 1];
     __shared__ uint64_t few[FEW];
     __shared__ int found[3];   // bin, count above it, its own count
     __shared__ int listed;     // pairs in few (of the cluster's first CTA)
     __shared__ int spoiled;    // this CTA's slots have a bad page
     __shared__ uint64_t part[EW];
     const cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int C = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
     const int blocks_max = blocks_of(words_max);
     uint32_t *marks = smem;
     int32_t *holes = reinterpret_cast<int32_t *>(marks + words_max), *sources = holes + blocks_max;
     uint32_t *kept = reinterpret_cast<uint32_t *>(sources + blocks_max);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto sync_all = [&] {
-        if (C > 1)
+        if constexpr (CLUSTER)
             cluster.sync();
         else
             __syncthreads();
+    };
+    auto of_rank = [&](auto *p, int r) {
+        if constexpr (CLUSTER)
+            return cluster.map_shared_rank(p, r);
+        else
+            return p;
     };
     if (tid == 0) listed = spoiled = 0;
 
@@ -127,10 +150,9 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
     }
     u.len = a.t.lens[row];
     u.keep = a.keep[i];
-    u.since = a.since ? a.since[i] : INT32_MAX;
+    u.open = a.since ? (uint32_t)max(a.since[i], a.first) - a.first : 0x80000000u - a.first;
     u.trow = a.t.table + (int64_t)row * a.t.max_pages;
-    const int ps = a.c.page_size;
-    const bool bad_len = u.len < 0 || u.len > (int64_t)a.t.max_pages * ps;
+    const bool bad_len = u.len < 0 || u.len > (int64_t)a.t.max_pages * a.c.page_size;
     if (bad_len || u.keep < 0 || u.len <= u.keep || u.len > KDA_KV_EVICT_MAX_LEN) {
         if (tells) {
             a.new_lens[i] = bad_len ? 0 : u.len;
@@ -144,43 +166,18 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
     const int s0 = min(u.len, rank * per), s1 = min(u.len, s0 + per);
     const bool stay = s1 - s0 <= keys_max;
     bool bad = false;
-    // f(j, keys of slots j .. j + 3) for this thread's slots, from the pages or from shared memory
-    auto from_pages = [&](auto f) {
-        for (int j0 = s0 + 4 * tid; j0 < s1; j0 += 4 * ET * AHEAD) {
-            int32_t p[AHEAD];
-            Four x[AHEAD];
-#pragma unroll
-            for (int e = 0; e < AHEAD; ++e) {
-                const int j = j0 + e * 4 * ET;
-                p[e] = j < s1 ? u.trow[j / ps] : 0;
-            }
-#pragma unroll
-            for (int e = 0; e < AHEAD; ++e) {
-                const int j = j0 + e * 4 * ET;
-                if (!page_ok(a.t, p[e])) {
-                    bad = true;
-                    p[e] = 0;
-                }
-                if (j < s1) x[e] = read_four(a, u, j, p[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < AHEAD; ++e) {
-                const int j = j0 + e * 4 * ET;
-                if (j < s1) f(j, keys_of(a, u, j, x[e]));
-            }
-        }
-    };
+    // f(j, keys of slots j .. j + 3) for this thread's slots; again from the pages where shared memory does not hold them
     auto each = [&](auto f) {
-        if (!stay) return from_pages(f);
-        for (int j = s0 + 4 * tid; j < s1; j += 4 * ET) f(j, *reinterpret_cast<const uint4 *>(kept + j - s0));
+        for (int j = s0 + 4 * tid; j < s1; j += 4 * ET)
+            f(j, stay ? *reinterpret_cast<const uint4 *>(kept + j - s0) : keys_again(a, u, ps, j));
     };
 
     // `need` of the pairs that begin as the bytes found so far are among those that stay
     Border t = {0, 0, 0, 0};
     int need = max(u.keep, 1);  // (a row that keeps nothing has its pages looked at, too)
     for (int pass = 0; pass < 7; ++pass) {
-        int32_t *h = hist[pass & 1];
-        if (tid < BINS) reinterpret_cast<int4 *>(h)[tid] = make_int4(0, 0, 0, 0);
+        int32_t *h = hist[CLUSTER ? pass & 1 : 0];
+        for (int b = tid; b < BINS; b += ET) reinterpret_cast<int4 *>(h)[b] = make_int4(0, 0, 0, 0);
         __syncthreads();
         const int shift = pass < 4 ? 24 - 8 * pass : 16 - 8 * (pass - 4);
         int32_t *h_lane = h + (lane & (COPIES - 1));
@@ -199,10 +196,33 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
             }
         };
         if (pass == 0) {
-            from_pages([&](int j, uint4 k) {
-                if (stay) *reinterpret_cast<uint4 *>(kept + j - s0) = k;
-                count(j, k);
-            });
+            for (int j0 = s0 + 4 * tid; j0 < s1; j0 += 4 * ET * AHEAD) {
+                int32_t p[AHEAD];
+                Four x[AHEAD];
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e) {
+                    const int j = j0 + e * 4 * ET;
+                    p[e] = j < s1 ? u.trow[ps.page(j)] : 0;
+                }
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e) {
+                    const int j = j0 + e * 4 * ET;
+                    if (!page_ok(a.t, p[e])) {
+                        bad = true;
+                        p[e] = 0;
+                    }
+                    if (j < s1) x[e] = read_four(a, u, ps, j, p[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e) {
+                    const int j = j0 + e * 4 * ET;
+                    if (j < s1) {
+                        const uint4 k = keys_of(a, u, j, x[e]);
+                        if (stay) *reinterpret_cast<uint4 *>(kept + j - s0) = k;
+                        count(j, k);
+                    }
+                }
+            }
             if (bad) spoiled = 1;
         } else if (pass < 4) {
             each(count);
@@ -210,16 +230,16 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
             each(count_slots);
         }
         sync_all();
-        if (C > 1) {
-            if (tid < BINS) {
+        if constexpr (CLUSTER) {
+            for (int b = tid; b < BINS; b += ET) {
                 int c = 0;
 #pragma unroll
                 for (int r = 0; r < MAX_CLUSTER; ++r)
                     if (r < C) {
-                        const int4 x = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(h + tid * COPIES, r));
+                        const int4 x = *reinterpret_cast<const int4 *>(of_rank(h + b * COPIES, r));
                         c += x.x + x.y + x.z + x.w;
                     }
-                sums[tid] = c;
+                sums[b] = c;
             }
             __syncthreads();
         }
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
 #pragma unroll
             for (int e = 0; e < BINS / 32; ++e) {
                 const int bin = BINS - 1 - (lane * (BINS / 32) + e);
-                if (C > 1) {
+                if constexpr (CLUSTER) {
                     c[e] = sums[bin];
                 } else {
                     const int4 x = reinterpret_cast<const int4 *>(h)[bin];
@@ -256,7 +276,7 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
         }
         __syncthreads();
         if (pass == 0) {
-            const bool wrong = lane < C && *cluster.map_shared_rank(&spoiled, lane);
+            const bool wrong = lane < C && *of_rank(&spoiled, lane);
             if (__any_sync(FULL, wrong)) {  // the same in all CTAs of the row: it stays as it is, in every layer and head
                 sync_all();
                 if (tells) {
@@ -283,20 +303,51 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t slot = 0xffffffu - (j + e);
                     if ((x[e] & t.key_mask) == t.key && (slot & t.slot_mask) == t.slot) {
-                        const int at = atomicAdd(cluster.map_shared_rank(&listed, 0), 1);
-                        for (int r = 0; r < C; ++r) cluster.map_shared_rank(few, r)[at] = (uint64_t)x[e] << 32 | slot;
+                        const int at = atomicAdd(of_rank(&listed, 0), 1);
+                        for (int r = 0; r < C; ++r) of_rank(few, r)[at] = (uint64_t)x[e] << 32 | slot;
                     }
                 }
             });
             sync_all();
-            if (tid < size) {
-                const uint64_t mine = few[tid];
-                int larger = 0;
-                for (int k = 0; k < size; ++k) larger += few[k] > mine;
-                if (larger == need - 1) {
-                    found[0] = (int)(uint32_t)(mine >> 32);
-                    found[1] = (int)(uint32_t)mine;
+            if (warp == 0) {
+                // bit by bit from the highest in which they differ, by votes of one warp, FEW / 32 pairs a lane
+                constexpr int N = FEW / 32;
+                uint32_t hi[N], lo[N], in = 0, all[2] = {~0u, ~0u}, any[2] = {0, 0};
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const uint64_t x = lane + 32 * n < size ? few[lane + 32 * n] : few[0];
+                    in |= (uint32_t)(lane + 32 * n < size) << n;
+                    hi[n] = (uint32_t)(x >> 32);
+                    lo[n] = (uint32_t)x;
+                    all[0] &= hi[n], any[0] |= hi[n];
+                    all[1] &= lo[n], any[1] |= lo[n];
                 }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t differ = __reduce_or_sync(FULL, any[half]) & ~__reduce_and_sync(FULL, all[half]);
+                    for (; differ; differ &= ~(0x80000000u >> __clz(differ))) {
+                        const int bit = 31 - __clz(differ);
+                        uint32_t set = 0;
+                        int above = 0;
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            set |= ((half ? lo[n] : hi[n]) >> bit & 1) << n;
+                            above += __popc(__ballot_sync(FULL, (set & in) >> n & 1));
+                        }
+                        if (above >= need) {
+                            in &= set;
+                        } else {
+                            need -= above;
+                            in &= ~set;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    if (in >> n & 1) {
+                        found[0] = (int)hi[n];
+                        found[1] = (int)lo[n];
+                    }
             }
             __syncthreads();
             t = Border{(uint32_t)found[0], 0xffffffffu, (uint32_t)found[1], 0xffffffu};
@@ -309,23 +360,17 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
         return;
     }
 
-    // marks: larger pairs, and those that begin as the last one does
+    // marks: pairs as large as the border's, whose bytes that were not looked at are 0
     for (int j0 = s0; j0 < s1; j0 += 4 * ET) {
         const int j = j0 + 4 * tid;
         uint32_t word = 0;
-        auto mark = [&](int, uint4 k) {
+        if (j < s1) {
+            const uint4 k = stay ? *reinterpret_cast<const uint4 *>(kept + j - s0) : keys_again(a, u, ps, j);
             const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t key = x[e] & t.key_mask, slot = (0xffffffu - (j + e)) & t.slot_mask;
-                word |= (uint32_t)(key > t.key || (key == t.key && slot >= t.slot)) << e;
+                word |= (uint32_t)(x[e] > t.key || (x[e] == t.key && 0xffffffu - (j + e) >= t.slot)) << e;
             }
-        };
-        if (j < s1) {
-            if (stay)
-                mark(j, *reinterpret_cast<const uint4 *>(kept + j - s0));
-            else
-                mark(j, keys_of(a, u, j, read_four(a, u, j, u.trow[j / ps])));
         }
         // eight threads' bits are a word, which every CTA of the cluster gets
         word <<= 4 * (lane & 7);
@@ -333,7 +378,7 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
         word |= __shfl_xor_sync(FULL, word, 2);
         word |= __shfl_xor_sync(FULL, word, 4);
         if ((j & ~31) < s1)
-            for (int r = lane & 7; r < C; r += 8) *cluster.map_shared_rank(marks + j / 32, r) = word;
+            for (int r = lane & 7; r < C; r += 8) *of_rank(marks + j / 32, r) = word;
     }
     sync_all();  // all marks are there, all sums have been read, nobody reads another CTA's memory any more
 
@@ -427,15 +472,15 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
             int64_t from = 0, to = 0;  // words before the rows
             if (lane < cnt) {
                 const int src = list[m - r0 + lane], dst = list[room + m - r0 + lane];
-                from = u.trow[src / ps] * a.c.page_stride;
-                to = u.trow[dst / ps] * a.c.page_stride;
-                const int32_t *f = reinterpret_cast<const int32_t *>(u.base + from + stats_at(a.c, u.head)) + src % ps;
-                int32_t *g = reinterpret_cast<int32_t *>(u.base + to + stats_at(a.c, u.head)) + dst % ps;
-                const int32_t x = f[0], y = f[ps];
+                from = u.trow[ps.page(src)] * a.c.page_stride;
+                to = u.trow[ps.page(dst)] * a.c.page_stride;
+                const int32_t *f = reinterpret_cast<const int32_t *>(u.base + from + stats_at(a.c, u.head)) + ps.within(src);
+                int32_t *g = reinterpret_cast<int32_t *>(u.base + to + stats_at(a.c, u.head)) + ps.within(dst);
+                const int32_t x = f[0], y = f[ps.size];
                 g[0] = x;
-                g[ps] = y;
-                from += (int64_t)(src % ps) * a.c.d;
-                to += (int64_t)(dst % ps) * a.c.d;
+                g[ps.size] = y;
+                from += ps.within(src) * a.c.d;
+                to += ps.within(dst) * a.c.d;
             }
             for (int k = lane & (width - 1); k - (lane & (width - 1)) < both; k += 32) {
                 const int64_t in = k < nv ? k * 8 : values + (k - nv) * 8;
@@ -460,6 +505,22 @@ __global__ void __launch_bounds__(ET, ET == 256 ? 4 : 1) kda_kv_evict_kernel(con
     }
 }
 
+struct Variant {
+    void (*kernel)(KvEvictArgs, PageSize, int, int);
+    int index;
+    unsigned threads;
+};
+// Clusters: 1,024 threads a CTA where a multiprocessor has one CTA at most.  Single CTAs: the steps of a unit are bound by
+// barriers and latencies, so that more and smaller CTAs are better where rows are short: 64 rows of 2,112 tokens in 4 layers
+// and 8 heads took 39 us with 128 threads, 48 with 256 (and 57 with one warp); 6 of 2,000 to 8,192 in 8 layers 76 us with 256
+// and 99 with 128.
+inline Variant variant(int64_t units, int C, int64_t cap) {
+    if (C > 1 && units * C <= current_device_sms()) return {kda_kv_evict_kernel<1024, true>, 0, 1024};
+    if (C > 1) return {kda_kv_evict_kernel<256, true>, 1, 256};
+    if (cap <= SHORT) return {kda_kv_evict_kernel<128, false>, 2, 128};
+    return {kda_kv_evict_kernel<256, false>, 3, 256};
+}
+
 }  // namespace kv
 
 int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {
@@ -467,20 +528,19 @@ int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {
     const int64_t units = (int64_t)a.n * a.c.layers * a.c.heads;
     const int64_t cap = std::min<int64_t>((int64_t)a.t.max_pages * a.t.page_size, KDA_KV_EVICT_MAX_LEN);
     const int words = (int)((cap + BLOCK - 1) / BLOCK * (BLOCK / 32));
-    // CTAs of a unit: more where there are few units, while each has 1,024 slots or more
+    // CTAs of a unit: more where there are few units, while each has 1,024 slots or more (384 units of 2,000 to 8,192 tokens, of
+    // which 1,024 stay: 76 us with one CTA each, 87 with two)
     int C = 1;
-    while (C < MAX_CLUSTER && units * C < (int64_t)current_device_sms() * 4 && cap > (int64_t)C * 1024) C *= 2;
+    while (C < MAX_CLUSTER && units * C < (int64_t)current_device_sms() * 2 && cap > (int64_t)C * 1024) C *= 2;
     const int other = 4 * (words + 2 * blocks_of(words)), room = (kSmemMax - 12288 - other) / 4 / BLOCK * BLOCK;
     const int keys = (int)std::min<int64_t>({KEYS, room, ((cap + C - 1) / C + BLOCK - 1) / BLOCK * BLOCK});
     const size_t smem = (size_t)other + 4 * keys;
-    // where a multiprocessor has one CTA at most, larger ones
-    const bool wide = units * C <= current_device_sms();
-    static std::atomic<uint64_t> prepared[2];
-    auto k = wide ? kda_kv_evict_kernel<1024> : kda_kv_evict_kernel<256>;
-    if (allow_smem(k, prepared[wide]) == cudaSuccess) {
+    const Variant v = variant(units, C, cap);
+    static std::atomic<uint64_t> prepared[4];
+    if (allow_smem(v.kernel, prepared[v.index]) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(units * C));
-        cfg.blockDim = dim3(wide ? 1024 : 256);
+        cfg.blockDim = dim3(v.threads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
         cudaLaunchAttribute attr[2];
@@ -489,8 +549,9 @@ int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim = {(unsigned)C, 1, 1};
         cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        cudaLaunchKernelEx(&cfg, k, a, words, keys);
+        cfg.numAttrs = C > 1 ? 2 : 1;
+        const PageSize ps{(uint32_t)a.t.page_size, (uint32_t)(((uint64_t)1 << 32) / a.t.page_size + 1)};
+        cudaLaunchKernelEx(&cfg, v.kernel, a, ps, words, keys);
     }
     return launch_result("kda_kv_evict_kernel launch");
 }

@@ -15,7 +15,7 @@
 namespace kda {
 namespace kv {
 
-constexpr int NT = 256;
+constexpr int NT = 128;
 
 // 16 bytes, or one element where offset or dim let pairs begin inside a 16-byte word.
 template <int VEC>
@@ -192,7 +192,13 @@ __global__ void __launch_bounds__(NT) kda_kv_append_kernel(const KvAppendArgs a,
     // the rows first: they do not depend on where they go
     const int n = items.count(), nv = (d / 8 + 1) / 2, gq = (a.H + HPT - 1) / HPT, gk = (kv + HPT - 1) / HPT;
     typename Word<VEC>::T r[HPT][2];
-    uint4 w[HPT][2];
+    uint4 single[VEC == 8 ? 1 : HPT][2];  // values are copied in 16-byte words in either case
+    auto &w = [&]() -> uint4(&)[HPT][2] {
+        if constexpr (VEC == 8)
+            return r;
+        else
+            return single;
+    }();
     int kind = 3, h0 = 0, i = 0, e0 = 0, e1 = -1;  // 0: queries, 1: keys, 2: values, 3: stats
     if (mine) {
         if (u < (gq + gk) * n) {
@@ -216,9 +222,17 @@ __global__ void __launch_bounds__(NT) kda_kv_append_kernel(const KvAppendArgs a,
         }
     }
 
-    for (int j = warp; j < per_cta && tok0 + j < a.num_tokens; j += NT / 32) {
+    if (kind < 2 && i < items.rot) {  // (those of threads without a token are not used)
+        const Turn<VEC> t = turn_of<VEC>(a.r, i, a.positions[tok], false);
+#pragma unroll
+        for (int k = 0; k < HPT; ++k) rotate<FP16>(r[k][0], r[k][1], t, a.r.interleaved);
+    }
+
+    for (int j = warp; j < per_cta && tok0 + j < a.num_tokens; j += blockDim.x / 32) {
         const int64_t t = tok0 + j;
-        const int b = sequence_of(a.cu, a.n, t, lane);
+        // in a decode step sequence t has token t: looked at first, as a search is two loads more that wait for one another
+        const int g = (int)min(t, (int64_t)a.n - 1);
+        const int b = a.cu[g] == t && a.cu[g + 1] == t + 1 ? g : sequence_of(a.cu, a.n, t, lane);
         Place p = {-1, 0, 0};
         if (b >= 0 && b < a.n) {
             const int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
@@ -255,11 +269,6 @@ __global__ void __launch_bounds__(NT) kda_kv_append_kernel(const KvAppendArgs a,
     if (kind == 0 ? !p.live : p.page < 0) return;
     uint16_t *page = c.pages + p.page;
     if (kind < 2) {
-        if (i < items.rot) {
-            const Turn<VEC> t = turn_of<VEC>(a.r, i, a.positions[tok], false);
-#pragma unroll
-            for (int k = 0; k < HPT; ++k) rotate<FP16>(r[k][0], r[k][1], t, a.r.interleaved);
-        }
         if (kind)
             put<VEC, HPT>(r, page + (int64_t)p.slot * d, (int64_t)c.page_size * d, h0, kv, e0, e1);
         else
@@ -279,11 +288,13 @@ inline bool wide(const RopeArgs &r) { return r.offset % 8 == 0 && r.dim % 16 == 
 
 struct Grid {
     dim3 grid;
+    unsigned threads;
     int per_cta;
 };
 inline Grid grid_of(int64_t tokens, int64_t units) {
     Grid g;
     g.per_cta = units > NT ? 1 : (int)(NT / units);
+    g.threads = units > NT ? NT : (unsigned)(g.per_cta * units + 31) / 32 * 32;
     g.grid = dim3((unsigned)((tokens + g.per_cta - 1) / g.per_cta), (unsigned)(units > NT ? (units + NT - 1) / NT : 1));
     return g;
 }
@@ -294,7 +305,7 @@ int launch_rotate_as(const RotateArgs &a, cudaStream_t st) {
     const int64_t units = (int64_t)((a.H + HPT - 1) / HPT) * items.count();
     const Grid g = grid_of(a.num_tokens, units);
     auto k = a.fp16 ? kda_rope_kernel<true, VEC, HPT> : kda_rope_kernel<false, VEC, HPT>;
-    dependent_launch(k, g.grid, NT, 0, st, a, (int)units, g.per_cta);
+    dependent_launch(k, g.grid, g.threads, 0, st, a, (int)units, g.per_cta);
     return launch_result("kda_rope_kernel launch");
 }
 
@@ -305,7 +316,7 @@ int launch_append_as(const KvAppendArgs &a, cudaStream_t st) {
     const int64_t units = (gq + gk) * items.count() + gk * ((a.c.d / 8 + 1) / 2) + (a.c.stats ? a.c.heads : 0);
     const Grid g = grid_of(a.num_tokens, units);
     auto k = a.c.fp16 ? kda_kv_append_kernel<true, VEC, HPT> : kda_kv_append_kernel<false, VEC, HPT>;
-    dependent_launch(k, g.grid, NT, 0, st, a, (int)units, g.per_cta);
+    dependent_launch(k, g.grid, g.threads, 0, st, a, (int)units, g.per_cta);
     return launch_result("kda_kv_append_kernel launch");
 }
 
