@@ -1,0 +1,12 @@
+// kda_kv_decode_bf16.cu -- the attention kernels of kda_kv_decode.cuh for bf16.
+#include "kda_kv_decode.cuh"
+
+namespace kda {
+namespace kv {
+
+int launch_decode_bf16(const DecodeP &p, const CUtensorMap &map, cudaStream_t st) {
+    return launch_decode_of<false>(p, map, st);
+}
+
+}  // namespace kv
+}  // namespace kda

@@ -555,9 +555,8 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  * do not matter to it, whatever they hold (NaN too).  A seen key whose score is +infinity or NaN makes the query's outputs
  * and lse NaN (-infinity: weight 0); a seen value that is not finite makes its channel NaN or infinite, and where it is one
  * of several drafted tokens (nq above 1, or a tree_mask) all outputs and lse of the queries that see it NaN.
- * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 relative to
- * themselves down to 2^-28 of the largest of their part of the row, by up to 2^-39 of it below), outputs at the end.  Results
- * do not depend on the other sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all
+ * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 as for
+ * kda_latent_decode), outputs at the end.  Results do not depend on the other sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all
  * lengths of the call and on the GPU's number of multiprocessors.  The workspace need not be initialised and keeps nothing
  * between calls; calls that overlap on the GPU need one each.
  * max_tokens <= KDA_KV_MAX_TOKENS, H <= KDA_KV_MAX_HEADS, n <= 65535.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs
