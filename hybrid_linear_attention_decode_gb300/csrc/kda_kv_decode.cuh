@@ -35,23 +35,20 @@
 namespace kda {
 namespace kv {
 
-constexpr int CW = 8;                  // consuming warps
-constexpr int NT = (CW + 1) * 32;      // and the producer
-constexpr int STAGE = 16384;           // bytes of a tile: keys and values
 // Barriers of the ring, more than it has stages: a multiple of the groups of warps that take tiles in turn, so that a barrier
 // is always the same group's.  (A group that skipped uses of a barrier could take an earlier phase for its own: phases are
 // told apart by their parity alone.)
 constexpr int BARS = 16;
-constexpr int MERGE = CW * 64 * 8 * 4; // bytes where warps' outputs meet: 64 channels of 8 rows each
 // A unit counts for this many tiles more where the list is split: beginning and ending one costs about as much.
-constexpr int START = 4;
+constexpr int START = 8;
 
 using latent::exp2_;
 using latent::kBias;
 using latent::kRaise;
 
-template <int DP>
-constexpr int kTile = STAGE / (DP * 4);  // tokens
+// CW: consuming warps of a CTA, 8 / CW CTAs on a multiprocessor.
+template <int DP, int CW>
+constexpr int kTile = DP == 256 ? 16 : (CW >= 4 ? 4096 : 2048) / DP;  // tokens
 
 struct Cut {  // where a CTA's part of the list begins: place `off` of unit u of sequence b; places of a whole part
     int32_t b, u, off, pad;
@@ -60,13 +57,15 @@ struct Cut {  // where a CTA's part of the list begins: place `off` of unit u of
 
 struct DecodeP {
     KvDecodeArgs a;
-    int32_t groups, G, block;  // CTAs, rows of a group of heads, rows of a unit: 8, 16, 32 or 64
+    int32_t groups, G, block;  // CTAs, heads of a group, rows of a unit: 8, 16, 32 or 64
+    uint32_t inverse_g;        // 2^32 / G rounded up: row / G is the upper half of row * inverse_g (rows are below 2^15); 0: G is 1
     int32_t box_rows, whole;   // tokens of a box; whether it has all channels (else a box for each 64)
     Cut *cut;         // [groups]
     float *part;      // [groups * 2][block][DP] normalised parts: those that begin a unit second
     float *part_l;    // [groups * 2][block] log2 of their sums
     float *lse2;      // [n max_tokens][H] log2 of the rows' sums (add_weights)
-    int64_t *base;    // [n + 1] tiles of 64 tokens before each sequence (add_weights); INT64_MAX behind those that take part
+    int64_t *base;    // [n + 1] tiles of 64 tokens before each sequence (add_weights), INT64_MAX behind those that take part;
+                      // then the number of tiles
     float *scores;    // see score_at()
 };
 
@@ -77,12 +76,15 @@ struct Range {  // a CTA's part of the list
 };
 
 struct Scratch {
-    int64_t scan[3][CW + 1];
+    int64_t scan[3][12];
     int64_t b, u, off, tiles, slots;
 };
 
 __device__ __forceinline__ int units_of(const DecodeP &p, const Seq &s) {
     return p.a.c.heads * ((s.nq * p.G + p.block - 1) / p.block);
+}
+__device__ __forceinline__ int over_g(const DecodeP &p, int row) {
+    return p.inverse_g ? (int)__umulhi((uint32_t)row, p.inverse_g) : row;
 }
 template <int TILE>
 __device__ __forceinline__ int tiles_of(const Seq &s) {
@@ -97,7 +99,7 @@ __device__ __forceinline__ int64_t score_at(const DecodeP &p, const Seq &s, int6
 
 // Prefix sums of the sequences' places, each thread a run of sequences.  Called by all NT threads; also writes zeros for the
 // queries of empty (or bad) sequences.
-template <int TILE>
+template <int TILE, int NT>
 __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
     const KvDecodeArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x;
@@ -132,7 +134,7 @@ __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
         sh->u = sh->off = sh->tiles = sh->slots = 0;
     }
     __syncthreads();
-    for (int w = 0; w <= CW; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
 #pragma unroll
         for (int k = 0; k < 3; ++k)
             if (w < warp && (k == 0 || a.add_weights)) before[k] += sh->scan[k][w];
@@ -162,9 +164,14 @@ __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
                 slots += s.len;
             }
             if (a.add_weights && g == 0) {
-                // sequences that pass the bound come last in what the third launch goes over, and are left out of it
+                // sequences that pass the bound are the last ones with tokens, and the third launch ends before them
                 p.base[b + 1] = slots <= a.max_slots ? tiles : INT64_MAX;
-                if (t && slots > a.max_slots) set_status(a.status, KDA_DEV_BAD_SEQLENS);
+                if (slots > a.max_slots) {
+                    if (t) set_status(a.status, KDA_DEV_BAD_SEQLENS);
+                    if (t && slots - s.len <= a.max_slots) p.base[a.n + 1] = tiles - tiles64(s);
+                } else if (b == a.n - 1) {
+                    p.base[a.n + 1] = tiles;
+                }
             }
         }
     }
@@ -236,12 +243,26 @@ __device__ __forceinline__ bool sync_threads_or(int id, int n, bool x) {
                  : "memory");
     return r != 0;
 }
+// Loads that are the first to leave L2 again: what they read is read once, and scores and parts should stay.
+__device__ __forceinline__ uint64_t evict_first() {
+    uint64_t r;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
+    return r;
+}
 __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t *bar) {
+                                            uint64_t *bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-        "[%7];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, "
+        "%5, %6}], [%7], %8;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+        "%4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 
@@ -253,34 +274,43 @@ struct Part {
     int32_t keep_scores;
 };
 
-template <int DP, int RW, int RG>
+template <int DP, int RW, int RG, int CW>
 struct Config {
-    static constexpr int TILE = kTile<DP>, CH = DP / 64, MT = TILE / 16;
+    static constexpr int TILE = kTile<DP, CW>, CH = DP / 64, MT = TILE / 16;
+    static constexpr int STAGE = TILE * DP * 4;            // bytes of a tile: keys and values
+    static constexpr int MERGE = CW * 64 * 8 * 4;          // bytes where warps' outputs meet, one of two: 64 channels of 8 rows
+    // Threads: the consumers, the producer, and with eight consumers three idle warps that make the producer's warpgroup whole
+    // (registers come in warpgroups): launched with 168 registers a thread (64,512 of 65,536), of which the consumers
+    // take 216 and the others give down to 72: 256 * 216 + 128 * 72 = 64,512, what the launch holds.
+    static constexpr int NT = CW == 8 ? 384 : (CW + 1) * 32;
+    static constexpr int ROOM = (CW == 8 ? kSmemMax : kSmemMax / (8 / CW) - 1024) - 4096;  // (1 KB of each CTA is the system's)
     static constexpr int ROWS = 8 * RW * RG;               // rows of a unit
     static constexpr int QROW = DP * 2 + 16;               // bytes of a query in shared memory: no bank conflicts
     static constexpr int QBYTES = ROWS * QROW;
-    static constexpr int STAGES = (kSmemMax - 4096 - MERGE - 2 * QBYTES) / STAGE < 12 ? (kSmemMax - 4096 - MERGE - 2 * QBYTES) / STAGE
-                                                                                      : 12;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + MERGE + 2 * QBYTES;
+    static constexpr int FIT = (ROOM - 2 * MERGE - 2 * QBYTES) / STAGE, STAGES = FIT < 12 ? FIT : 12;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 2 * MERGE + 2 * QBYTES;
     static constexpr int GROUPS = CW / RG;
-    static_assert(BARS % GROUPS == 0 && STAGES <= BARS && STAGES > GROUPS, "");
-    static constexpr bool Q_REGS = DP * RW <= 128;         // queries stay in registers
+    static_assert(RG <= CW && BARS % GROUPS == 0 && STAGES <= BARS && STAGES >= 4, "");
+    static constexpr bool Q_REGS = DP * RW <= 256;         // queries stay in registers
 };
 
 // RW: 8 rows each of a warp (1 or 2); RG: warps that share a tile, with rows of their own.
-template <bool FP16, int DP, int RW, int RG>
-__global__ void __launch_bounds__(NT, 1)
+template <bool FP16, int DP, int RW, int RG, int CW>
+__global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
     kda_kv_decode_kernel(const DecodeP p, const __grid_constant__ CUtensorMap map) {
-    using C = Config<DP, RW, RG>;
-    constexpr int TILE = C::TILE, CH = C::CH, MT = C::MT, ROWS = C::ROWS, QROW = C::QROW, STAGES = C::STAGES;
+    using C = Config<DP, RW, RG, CW>;
+    constexpr int TILE = C::TILE, CH = C::CH, MT = C::MT, ROWS = C::ROWS, QROW = C::QROW, STAGES = C::STAGES, NT = C::NT;
+    constexpr int STAGE = C::STAGE, MERGE = C::MERGE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *merge = reinterpret_cast<float *>(sm + STAGES * STAGE);  // [CW][64 channels][8 rows]
-    uint8_t *qs = sm + STAGES * STAGE + MERGE;                      // [2][ROWS][QROW]
+    float *merge = reinterpret_cast<float *>(sm + STAGES * STAGE);  // [2][CW][64 channels][8 rows]
+    uint8_t *qs = sm + STAGES * STAGE + 2 * MERGE;                   // [2][ROWS][QROW]
     __shared__ uint64_t full[BARS], empty[BARS], q_full[2], q_empty[2];
     __shared__ Scratch scratch;
     __shared__ Part parts[2];
     __shared__ float sm_m[CW][8 * RW], sm_l[CW][8 * RW];
+    __shared__ float row_m[ROWS], row_inv[ROWS];  // of the unit's rows: maximum, 1 / sum
+    __shared__ int32_t row_out[ROWS];             // and words from the sequence's outputs to theirs
     const KvDecodeArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int kv = a.c.heads, G = p.G, d = a.c.d;
@@ -301,16 +331,19 @@ __global__ void __launch_bounds__(NT, 1)
     for (int i = tid; i < 2 * C::QBYTES / 16; i += NT) reinterpret_cast<uint4 *>(qs)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     wait_for_previous();
-    const Range R = range_of<TILE>(p, &scratch);  // its barriers show the initialised ones to all
+    const Range R = range_of<TILE, NT>(p, &scratch);  // its barriers show the initialised ones to all
     allow_dependent_launch();
     bool ok = true;
 
-    if (warp == CW) {
+    if (warp >= CW) {
+        if constexpr (CW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp > CW) return;
         // ---------------------------------------------------------------- producer
         // lanes of a box, which begins with token `box` of a tile: keys and values
         const int ps = a.c.page_size, rows = p.box_rows, box = (lane >> 1) * rows, value = lane & 1;
         const int small = ps < TILE ? TILE / ps : 0, box_page = ps < TILE ? box / ps : 0;
         const uint32_t num_pages = (uint32_t)a.c.num_pages;
+        const uint64_t policy = evict_first();
         int it = 0, st = 0, n = 0;
         int64_t at = R.lo, tiles64_before = R.tiles, slots_before = R.slots;
         int off = R.off, u = R.u, b0 = R.b, left = 0;
@@ -348,7 +381,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 __syncwarp();
                 for (int r = lane; r < live; r += 32) {
-                    const int t = (r0 + r) / G;
+                    const int t = over_g(p, r0 + r);
                     bulk_g2s(qs + slot * C::QBYTES + r * QROW,
                              a.q + (s.c0 + t) * a.q_ts + (int64_t)(hk * G + r0 + r - t * G) * a.q_hs, d * 2, q_full + slot);
                 }
@@ -383,10 +416,10 @@ __global__ void __launch_bounds__(NT, 1)
                     if (box < TILE) {
                         uint8_t *to = sm + st * STAGE + value * (STAGE / 2) + box * (DP * 2);
                         if (p.whole)
-                            tma_load_5d(to, &map, 0, 0, 0, (at_row + in_box) / 8, (int)page, bar);
+                            tma_load_5d(to, &map, 0, 0, 0, (at_row + in_box) / 8, (int)page, bar, policy);
                         else
                             for (int ch = 0; ch < CH; ++ch)
-                                latent::tma_load_3d(to + ch * rows * 128, &map, ch * 64, at_row + in_box, (int)page, bar);
+                                tma_load_3d(to + ch * rows * 128, &map, ch * 64, at_row + in_box, (int)page, bar, policy);
                     }
                     if (++st == STAGES) st = 0;
                 }
@@ -405,6 +438,7 @@ __global__ void __launch_bounds__(NT, 1)
         for (int i = max(0, it - STAGES); i < it; ++i)
             if (!latent::warp_wait(full + i % BARS, (i / BARS) & 1)) ok = false;
     } else {
+        if constexpr (CW == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---------------------------------------------------------------- consumers
         const int grp = warp / RG, rg = warp % RG;  // rows rg * 8 RW of the unit's
         const int quad = lane & 3, top = lane >> 2;
@@ -457,10 +491,12 @@ __global__ void __launch_bounds__(NT, 1)
             const bool drafts = s.nq > 1 || a.tree;
             const int draft0 = drafts ? s.len - s.nq : s.len;  // first token that not all rows see
 
-            for (int j = 0; j < w.nt; ++j, ++it) {
-                if (it % C::GROUPS != grp) continue;
-                if (ok) ok = latent::warp_wait(full + (it & (BARS - 1)), (it / BARS) & 1);
-                uint8_t *tile = sm + it % STAGES * STAGE;
+            const int it0 = it;
+            it += w.nt;
+            for (int j = (grp - it0) & (C::GROUPS - 1); j < w.nt; j += C::GROUPS) {
+                const int i = it0 + j;
+                if (ok) ok = latent::warp_wait(full + (i & (BARS - 1)), (i / BARS) & 1);
+                uint8_t *tile = sm + i % STAGES * STAGE;
                 const int key0 = (w.first + j) * TILE;
                 const bool edge = key0 + TILE > draft0;
                 // 16 bytes `c` (8 channels each) of the value row of token r
@@ -477,8 +513,10 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                     if (RG > 1) sync_threads(2 + grp, RG * 32);  // every warp has looked
                     __syncwarp();
-                    for (int r = 0; r < TILE; ++r)
-                        if ((key0 + r >= s.len || ((poison >> r) & 1)) && lane < DP / 8) *value_word(r, lane) = make_uint4(0, 0, 0, 0);
+                    for (int k = max(0, s.len - key0) * (DP / 8) + lane; k < TILE * (DP / 8); k += 32)
+                        *value_word(k / (DP / 8), k % (DP / 8)) = make_uint4(0, 0, 0, 0);
+                    for (uint64_t x = poison; x; x &= x - 1)
+                        if (lane < DP / 8) *value_word(__ffsll(x) - 1, lane) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -520,13 +558,13 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                         for (int f = 0; f < 2; ++f) {
                             const int r = w.r0 + rg * 8 * RW + h * 8 + 2 * quad + f;
-                            const uint64_t seen = drafts && r < total ? drafts_seen(a, s, r / G) : ~0ull;
+                            const uint64_t seen = drafts && r < total ? drafts_seen(a, s, over_g(p, r)) : ~0ull;
 #pragma unroll
                             for (int t = 0; t < MT; ++t)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const int row = t * 16 + top + 8 * e, i = key0 + row - draft0;
-                                    if (key0 + row >= s.len || (i >= 0 && !((seen >> i) & 1)))
+                                    const int row = t * 16 + top + 8 * e, draft = key0 + row - draft0;
+                                    if (key0 + row >= s.len || (draft >= 0 && !((seen >> draft) & 1)))
                                         c[t][h][2 * e + f] = -INFINITY;
                                     else if ((poison >> row) & 1)
                                         c[t][h][2 * e + f] = NAN;
@@ -610,7 +648,7 @@ __global__ void __launch_bounds__(NT, 1)
                         for (int h = 0; h < RW; ++h) mma<FP16>(o[k][h], y, b[t][h][0], b[t][h][1]);
                     }
                 __syncwarp();
-                if (lane == 0) latent::mbar_arrive(empty + (it & (BARS - 1)));
+                if (lane == 0) latent::mbar_arrive(empty + (i & (BARS - 1)));
             }
             if constexpr (!C::Q_REGS) {
                 __syncwarp();
@@ -632,66 +670,71 @@ __global__ void __launch_bounds__(NT, 1)
             sync_threads(1, CW * 32);
             const bool whole = w.nt == w.tiles;
             const int64_t part = (int64_t)blockIdx.x * 2 + (w.first == 0);
-            float scale[RW][2];
+            if (tid < ROWS) {  // a row a thread (with 64 rows there are four warps at least)
+                const int g = tid / (8 * RW), i = tid % (8 * RW), r = w.r0 + tid;
+                float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int h = 0; h < RW; ++h)
+                for (int v = 0; v < CW / RG; ++v) M = fmaxf(M, sm_m[v * RG + g][i]);
+                const float mm = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int v = 0; v < CW / RG; ++v) L += sm_l[v * RG + g][i] * exp2_(sm_m[v * RG + g][i] - mm);
+                row_m[tid] = mm;
+                row_inv[tid] = L == 0.f ? 0.f : 1.f / L;
+                if (r < total) {
+                    const float l2 = L == 0.f ? -INFINITY : mm + log2f(L) - kBias<FP16>;
+                    const int t = over_g(p, r), head = w.hk * G + r - t * G;
+                    row_out[tid] = (t * a.H + head) * d;
+                    if (!whole) {
+                        p.part_l[part * ROWS + tid] = l2;
+                    } else {
+                        if (a.lse) a.lse[(s.c0 + t) * a.H + head] = l2 * latent::kLn2;
+                        if (a.add_weights) p.lse2[((int64_t)w.b * a.max_tokens + t) * a.H + head] = l2;
+                    }
+                }
+            }
+            sync_threads(1, CW * 32);
+            uint16_t *out = a.out + s.c0 * a.H * d;
+            int turn = 0;
+#pragma unroll
+            for (int h = 0; h < RW; ++h) {
+                float scale[2];
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    const int i = h * 8 + 2 * quad + f;
-                    float M = -INFINITY, L = 0.f;
-#pragma unroll
-                    for (int v = rg; v < CW; v += RG) M = fmaxf(M, sm_m[v][i]);
-                    const float mm = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                    for (int v = rg; v < CW; v += RG) L += sm_l[v][i] * exp2_(sm_m[v][i] - mm);
-                    scale[h][f] = L == 0.f ? 0.f : exp2_(m[h][f] - mm) / L;
-                    const int row = rg * 8 * RW + i, r = w.r0 + row;
-                    if (warp < RG && top == 0 && r < total) {
-                        const float l2 = L == 0.f ? -INFINITY : mm + log2f(L) - kBias<FP16>;
-                        const int t = r / G, head = w.hk * G + r - t * G;
-                        if (!whole) {
-                            p.part_l[part * ROWS + row] = l2;
-                        } else {
-                            if (a.lse) a.lse[(s.c0 + t) * a.H + head] = l2 * latent::kLn2;
-                            if (a.add_weights) p.lse2[((int64_t)w.b * a.max_tokens + t) * a.H + head] = l2;
-                        }
-                    }
+                    const int row = rg * 8 * RW + h * 8 + 2 * quad + f;
+                    scale[f] = exp2_(m[h][f] - row_m[row]) * row_inv[row];
                 }
 #pragma unroll
-            for (int h = 0; h < RW; ++h)
+                for (int ch = 0; ch < CH; ++ch)
+                    if (ch * 64 < d) {
+                        float *half = merge + turn * (MERGE / 4);
+                        turn ^= 1;
 #pragma unroll
-                for (int ch = 0; ch < CH; ++ch) {
-                    if (ch * 64 >= d) break;
+                        for (int k = 0; k < 4; ++k) {
+                            float *to = half + ((warp * 64 + k * 16 + top) * 8 + 2 * quad);
+                            const float(&y)[4] = o[ch * 4 + k][h];
+                            *reinterpret_cast<float2 *>(to) = make_float2(y[0] * scale[0], y[1] * scale[1]);
+                            *reinterpret_cast<float2 *>(to + 64) = make_float2(y[2] * scale[0], y[3] * scale[1]);
+                        }
+                        sync_threads(1, CW * 32);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float *to = merge + ((warp * 64 + k * 16 + top) * 8 + 2 * quad);
-                        const float(&y)[4] = o[ch * 4 + k][h];
-                        *reinterpret_cast<float2 *>(to) = make_float2(y[0] * scale[h][0], y[1] * scale[h][1]);
-                        *reinterpret_cast<float2 *>(to + 64) = make_float2(y[2] * scale[h][0], y[3] * scale[h][1]);
-                    }
-                    sync_threads(1, CW * 32);
+                        for (int k = tid; k < RG * 256; k += CW * 32) {  // a thread has two channels of a row
+                            const int g = k >> 8, pair = (k >> 3) & 31, row = g * 8 * RW + h * 8 + (k & 7), chn = ch * 64 + pair * 2;
+                            if (w.r0 + row < total && chn < d) {
+                                float x = 0.f, y = 0.f;
 #pragma unroll
-                    for (int i = tid; i < RG * 256; i += CW * 32) {  // (group of rows, two channels, row)
-                        const int g = i >> 8, pair = (i >> 3) & 31, row = g * 8 * RW + h * 8 + (i & 7), r = w.r0 + row;
-                        const int chn = ch * 64 + pair * 2;
-                        if (r < total && chn < d) {
-                            float x = 0.f, y = 0.f;
-#pragma unroll
-                            for (int v = 0; v < CW / RG; ++v) {
-                                const float *from = merge + ((v * RG + g) * 64 + pair * 2) * 8 + (i & 7);
-                                x += from[0];
-                                y += from[8];
-                            }
-                            if (whole) {
-                                const int t = r / G, head = w.hk * G + r - t * G;
-                                *reinterpret_cast<uint32_t *>(a.out + ((s.c0 + t) * a.H + head) * d + chn) = latent::pack2<FP16>(x, y);
-                            } else {
-                                *reinterpret_cast<float2 *>(p.part + (part * ROWS + row) * DP + chn) = make_float2(x, y);
+                                for (int v = 0; v < CW / RG; ++v) {
+                                    const float *from = half + ((v * RG + g) * 64 + pair * 2) * 8 + (k & 7);
+                                    x += from[0];
+                                    y += from[8];
+                                }
+                                if (whole)
+                                    *reinterpret_cast<uint32_t *>(out + row_out[row] + chn) = latent::pack2<FP16>(x, y);
+                                else
+                                    *reinterpret_cast<float2 *>(p.part + (part * ROWS + row) * DP + chn) = make_float2(x, y);
                             }
                         }
                     }
-                    sync_threads(1, CW * 32);
-                }
+            }
         }
     }
     if (!ok && lane == 0) set_status(a.status, KDA_DEV_TIMEOUT);
@@ -702,9 +745,9 @@ constexpr int JW = 16;  // warps of a joining CTA
 // Joins the parts of the unit that the beginning of part blockIdx.x + 1 of the list cuts, if no earlier beginning does.  A
 // row's parts are divided among as many warps as there are for it, a lane has channels 4 lane .. 4 lane + 3 and those 128
 // further on.
-template <bool FP16, int DP>
+template <bool FP16, int DP, int TILE>
 __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
-    constexpr int TILE = kTile<DP>, V = (DP + 127) / 128;
+    constexpr int V = (DP + 127) / 128;
     __shared__ float4 sm_o[JW][V][32];
     __shared__ float sm_m[JW], sm_w[JW];
     wait_for_previous();
@@ -799,44 +842,67 @@ __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
     }
 }
 
-template <bool FP16, int DP, int RW, int RG>
-int launch_as(const DecodeP &p, const CUtensorMap &map, cudaStream_t st) {
+// Keys' and then values' rows of a page, [pages][heads, keys then values, x tokens / 8][chunks of 64 channels][8 tokens][64], in
+// boxes of `rows` tokens with all their channels, so that the copy reads 8 whole rows of the cache at a time and 64 channels of 8
+// tokens are one swizzled block of shared memory.  Where head_dim is no multiple of 64, [pages][...x tokens][head_dim] in boxes of
+// `rows` tokens x 64 channels, of which those behind the last read as zeros.
+inline bool cache_map(const KvCacheArgs &c, int rows, bool whole, int padded, CUtensorMap *map) {
+    const latent::EncodeTiledFn enc = latent::encoder();
+    if (!enc) return false;
+    const int64_t tokens = (int64_t)2 * c.heads * c.page_size, d = c.d;
+    if (whole) {
+        const int64_t dims[5] = {64, 8, d / 64, tokens / 8, c.num_pages}, strides[4] = {d, 64, 8 * d, c.page_stride};
+        const int box[5] = {64, 8, padded / 64, rows / 8, 1};
+        return latent::tensor_map(enc, map, c.fp16, c.pages, 5, dims, strides, box);
+    }
+    const int64_t dims[3] = {d, tokens, c.num_pages}, strides[2] = {d, c.page_stride};
+    const int box[3] = {64, rows, 1};
+    return latent::tensor_map(enc, map, c.fp16, c.pages, 3, dims, strides, box);
+}
+
+template <bool FP16, int DP, int RW, int RG, int CW>
+int launch_as(DecodeP p, cudaStream_t st) {
+    using C = Config<DP, RW, RG, CW>;
+    p.groups = current_device_sms() * (8 / CW);
+    p.box_rows = std::min(p.a.c.page_size, C::TILE);
+    CUtensorMap map;
+    if (!cache_map(p.a.c, p.box_rows, p.whole, DP, &map))
+        return fail(KDA_ERR_CUDA, "kv decode: the cache's tensor map was refused");
     static std::atomic<uint64_t> prepared{0};
-    auto k = kda_kv_decode_kernel<FP16, DP, RW, RG>;
-    if (allow_smem(k, prepared) == cudaSuccess)
-        dependent_launch(k, dim3((unsigned)p.groups), NT, Config<DP, RW, RG>::SMEM, st, p, map);
+    auto k = kda_kv_decode_kernel<FP16, DP, RW, RG, CW>;
+    if (allow_smem(k, prepared) == cudaSuccess) dependent_launch(k, dim3((unsigned)p.groups), C::NT, C::SMEM, st, p, map);
     int rc = launch_result("kda_kv_decode_kernel launch");
     if (rc == KDA_OK && p.groups > 1) {
-        dependent_launch(kda_kv_join_kernel<FP16, DP>, dim3((unsigned)p.groups - 1), JW * 32, 0, st, p);
+        dependent_launch(kda_kv_join_kernel<FP16, DP, C::TILE>, dim3((unsigned)p.groups - 1), JW * 32, 0, st, p);
         rc = launch_result("kda_kv_join_kernel launch");
     }
     return rc;
 }
 
-template <bool FP16, int DP>
-int launch_rows(const DecodeP &p, const CUtensorMap &map, cudaStream_t st) {
+template <bool FP16, int DP, int CW>
+int launch_rows(const DecodeP &p, cudaStream_t st) {
     switch (p.block) {
-        case 8: return launch_as<FP16, DP, 1, 1>(p, map, st);
-        case 16: return launch_as<FP16, DP, 2, 1>(p, map, st);
-        case 32: return launch_as<FP16, DP, 2, 2>(p, map, st);
-        default: return launch_as<FP16, DP, 2, 4>(p, map, st);
+        case 8: return launch_as<FP16, DP, 1, 1, CW>(p, st);
+        case 16: return launch_as<FP16, DP, 2, 1, CW>(p, st);
+        case 32: return launch_as<FP16, DP, 2, 2, CW < 4 ? 4 : CW>(p, st);
+        default: return launch_as<FP16, DP, 2, 4, 8>(p, st);
     }
 }
 
 inline int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 template <bool FP16>
-int launch_decode_of(const DecodeP &p, const CUtensorMap &map, cudaStream_t st) {
+int launch_decode_of(const DecodeP &p, cudaStream_t st) {
     switch (padded(p.a.c.d)) {
-        case 64: return launch_rows<FP16, 64>(p, map, st);
-        case 128: return launch_rows<FP16, 128>(p, map, st);
-        default: return launch_rows<FP16, 256>(p, map, st);
+        case 64: return launch_rows<FP16, 64, 4>(p, st);
+        case 128: return launch_rows<FP16, 128, 4>(p, st);
+        default: return launch_rows<FP16, 256, 8>(p, st);
     }
 }
 
 // Each in a file of its own, so that they compile side by side.
-int launch_decode_bf16(const DecodeP &p, const CUtensorMap &map, cudaStream_t st);
-int launch_decode_fp16(const DecodeP &p, const CUtensorMap &map, cudaStream_t st);
+int launch_decode_bf16(const DecodeP &p, cudaStream_t st);
+int launch_decode_fp16(const DecodeP &p, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace kda

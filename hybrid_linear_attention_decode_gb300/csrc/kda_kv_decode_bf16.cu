@@ -4,8 +4,8 @@
 namespace kda {
 namespace kv {
 
-int launch_decode_bf16(const DecodeP &p, const CUtensorMap &map, cudaStream_t st) {
-    return launch_decode_of<false>(p, map, st);
+int launch_decode_bf16(const DecodeP &p, cudaStream_t st) {
+    return launch_decode_of<false>(p, st);
 }
 
 }  // namespace kv

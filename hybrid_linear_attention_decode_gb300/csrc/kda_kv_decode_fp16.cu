@@ -4,8 +4,8 @@
 namespace kda {
 namespace kv {
 
-int launch_decode_fp16(const DecodeP &p, const CUtensorMap &map, cudaStream_t st) {
-    return launch_decode_of<true>(p, map, st);
+int launch_decode_fp16(const DecodeP &p, cudaStream_t st) {
+    return launch_decode_of<true>(p, st);
 }
 
 }  // namespace kv
