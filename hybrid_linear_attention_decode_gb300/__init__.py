@@ -156,7 +156,7 @@ def load_library(path: str | None = None):
     lib.kda_kv_decode_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_kv_decode.argtypes = [pkv, i32, ptable, i32, vp, vp, i64, i32, i32, vp, i64, i64, vp, f32, vp, vp, i32, f32,
                                   i64, vp, ctypes.c_size_t, vp, vp]
-    lib.kda_kv_evict.argtypes = [pkv, ptable, i32, vp, vp, i32, vp, vp, vp, vp]
+    lib.kda_kv_evict.argtypes = [pkv, ptable, i32, vp, vp, i32, vp, i32, vp, vp, vp]
     for name in ("kda_kv_cache_pages", "kda_rope_turns", "kda_rope_turns_of", "kda_rope_apply", "kda_kv_append",
                  "kda_kv_decode", "kda_kv_evict"):
         getattr(lib, name).restype = ctypes.c_int
@@ -897,17 +897,18 @@ def kda_kv_decode(cache: KvCache, layer: int, pt: PageTable, rows, cu_tokens, ma
 
 
 def kda_kv_evict(cache: KvCache, pt: PageTable, rows, keep, new_lens, dev_status, first: int = 0, since=None,
-                 stream=None) -> None:
+                 max_len: int = 0, stream=None) -> None:
     """Each layer and head keeps keep[i] tokens of row rows[i], those with the largest sums, in the row's first slots; see
-    include/kda.h.  rows, keep, new_lens, since int32 [n] (rows and since may be None); kda_pages_truncate(pt, rows,
-    new_lens, ...) then gives the pages behind back."""
+    include/kda.h.  rows, keep, new_lens, since int32 [n] (rows and since may be None), max_len a bound on the rows' lens (0:
+    what the table has room for; a close one is faster); kda_pages_truncate(pt, rows, new_lens, ...) then gives the pages
+    behind back."""
     name = "kda_kv_evict"
     dev = _device_of(name, (cache.data, pt.table, pt.lens, pt.refcount, rows, keep, new_lens, since, dev_status))
     n, pc = keep.shape[0], pt.c()
     if rows is None and n > pc.max_seqs:
         _raise(f"{name}: more sequences than table rows")
     _launch(load_library().kda_kv_evict, name, dev, stream, cache.kv(), pc, n, _int32(rows, "rows", n),
-            _int32(keep, "keep"), first, _int32(since, "since", n), _int32(new_lens, "new_lens", n),
+            _int32(keep, "keep"), first, _int32(since, "since", n), max_len, _int32(new_lens, "new_lens", n),
             _int32(dev_status, "dev_status", 1))
 
 

@@ -205,7 +205,7 @@ int launch_kv_decode(const KvDecodeArgs &a, cudaStream_t st);
 struct KvEvictArgs {
     KvCacheArgs c;
     PageTableArgs t;
-    int32_t n, first;
+    int32_t n, first, max_len;
     const int32_t *rows, *keep, *since;
     int32_t *new_lens;
     int32_t *status;

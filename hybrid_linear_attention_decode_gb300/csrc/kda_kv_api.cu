@@ -296,7 +296,8 @@ int kda_kv_decode(const kda_kv_cache *cache, int32_t layer, const kda_page_table
 }
 
 int kda_kv_evict(const kda_kv_cache *cache, const kda_page_table *pt, int32_t n, const int32_t *rows, const int32_t *keep,
-                 int32_t first, const int32_t *since, int32_t *new_lens, int32_t *dev_status, kda_stream_t stream) {
+                 int32_t first, const int32_t *since, int32_t max_len, int32_t *new_lens, int32_t *dev_status,
+                 kda_stream_t stream) {
     clear_error();
     KvEvictArgs a;
     const int rc = check_both(cache, pt, true, &a.c, &a.t);
@@ -305,6 +306,8 @@ int kda_kv_evict(const kda_kv_cache *cache, const kda_page_table *pt, int32_t n,
     if (n < 0 || n > 65535 || (int64_t)n * a.c.layers * a.c.heads > (int64_t)1 << 26)
         return fail(KDA_ERR_INVALID_ARG, "kv evict: n must be at most 65535 and n * layers * heads 2^26");
     if (first < 0) return fail(KDA_ERR_INVALID_ARG, "kv evict: first must not be negative");
+    if (max_len < 0 || max_len > KDA_KV_EVICT_MAX_LEN)
+        return fail(KDA_ERR_INVALID_ARG, "kv evict: max_len must be from 0 to KDA_KV_EVICT_MAX_LEN");
     if (n == 0) return KDA_OK;
     if (!keep || !new_lens) return fail(KDA_ERR_INVALID_ARG, "kv evict: keep or new_lens is NULL");
     if (!al(keep, 4) || !al(new_lens, 4) || (rows && !al(rows, 4)) || (since && !al(since, 4)) ||
@@ -312,6 +315,10 @@ int kda_kv_evict(const kda_kv_cache *cache, const kda_page_table *pt, int32_t n,
         return fail(KDA_ERR_INVALID_ARG, "kv evict: tables or status misaligned");
     a.n = n;
     a.first = first;
+    a.max_len = KDA_KV_EVICT_MAX_LEN;
+    const int64_t room = (int64_t)a.t.max_pages * a.t.page_size;
+    if (room < a.max_len) a.max_len = (int32_t)room;
+    if (max_len > 0 && max_len < a.max_len) a.max_len = max_len;
     a.rows = rows;
     a.keep = keep;
     a.since = since;

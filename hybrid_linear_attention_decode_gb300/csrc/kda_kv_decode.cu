@@ -13,8 +13,9 @@ __global__ void __launch_bounds__(WW * 32) kda_kv_weights_kernel(const DecodeP p
     allow_dependent_launch();
     const KvDecodeArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = a.c.heads, ps = a.c.page_size;
-    const int64_t items = p.base[a.n + 1] * kv, per = (items + gridDim.x - 1) / gridDim.x;
-    const int64_t i0 = min(items, blockIdx.x * per), tile0 = i0 / kv;
+    const int64_t tiles = p.base[a.n + 1], items = tiles * kv;
+    const int64_t per = items >> 31 ? (items + gridDim.x - 1) / gridDim.x : ((uint32_t)items + gridDim.x - 1) / gridDim.x;
+    const int64_t i0 = min(items, blockIdx.x * per), tile0 = i0 >> 31 ? i0 / kv : (uint32_t)i0 / kv;
     const int head0 = (int)(i0 - tile0 * kv), count = (int)(min(items, i0 + per) - i0);
     if (warp >= count) return;
     int b = 0, hi = a.n + 1;  // the last sequence that does not begin behind the tile, 32 ways a step
@@ -24,30 +25,38 @@ __global__ void __launch_bounds__(WW * 32) kda_kv_weights_kernel(const DecodeP p
         b += (31 - __clz(m)) * step;
         hi = min(hi, b + step);
     }
+    int64_t begin = p.base[b], end = p.base[b + 1];
+    int4 s = p.seqs[b];  // row, tokens, queries
     for (int i = warp; i < count; i += WW) {
         const int t0 = (head0 + i) / kv, hk = head0 + i - t0 * kv;
         const int64_t tile = tile0 + t0;
-        while (p.base[b + 1] <= tile) ++b;
-        const Seq s = seq_of(a, b);
-        const int key = (int)(tile - p.base[b]) * 64 + 2 * lane;
-        if (key >= s.len) continue;
-        const int32_t page = a.t.table[(int64_t)s.row * a.t.max_pages + key / ps];
-        const float *x = p.scores + score_at(p, s, tile, hk) + 2 * lane;
+        while (end <= tile) {
+            begin = end;
+            end = p.base[++b + 1];
+            s = p.seqs[b];
+        }
+        const int key = (int)(tile - begin) * 64 + 2 * lane, rows = s.z * p.G;
+        if (key >= s.y) continue;
+        const int32_t page = a.t.table[(int64_t)s.x * a.t.max_pages + key / ps];
+        const bool good = page_ok(a.t, page);
+        float *w = reinterpret_cast<float *>(a.c.pages + (good ? page * a.c.page_stride : 0) + stats_at(a.c, hk)) + key % ps;
+        const bool mine = good && a.t.refcount[good ? page : 0] <= 1;
+        const float2 sum = *reinterpret_cast<const float2 *>(w);
+        const float *x = p.scores + (tile * a.max_tokens * a.H + hk * rows) * 64 + 2 * lane;  // see score_at()
         const float *lse = p.lse2 + (int64_t)b * a.max_tokens * a.H + hk * p.G;
         float2 add = make_float2(0.f, 0.f);
-        for (int t = 0; t < s.nq; ++t)
+        for (int t = 0; t < s.z; ++t, lse += a.H)
 #pragma unroll 8
-            for (int g = 0; g < p.G; ++g) {
-                const float l2 = lse[t * a.H + g];
-                const float2 v = __ldcs(reinterpret_cast<const float2 *>(x + (t * p.G + g) * 64));
+            for (int g = 0; g < p.G; ++g, x += 64) {
+                const float l2 = lse[g];
+                const float2 v = __ldcs(reinterpret_cast<const float2 *>(x));
                 const bool some = l2 > -INFINITY;  // (not NaN)
                 add.x += some ? exp2_(v.x - l2) : 0.f;
                 add.y += some ? exp2_(v.y - l2) : 0.f;
             }
-        if (!page_ok(a.t, page) || a.t.refcount[page] > 1) continue;
-        float *w = reinterpret_cast<float *>(a.c.pages + page * a.c.page_stride + stats_at(a.c, hk)) + key % ps;
-        w[0] = a.decay * w[0] + add.x;
-        if (key + 1 < s.len) w[1] = a.decay * w[1] + add.y;
+        if (!mine) continue;
+        w[0] = a.decay * sum.x + add.x;
+        if (key + 1 < s.y) w[1] = a.decay * sum.y + add.y;
     }
 }
 
@@ -58,19 +67,21 @@ inline int block_rows(int G, int max_tokens) {
 }
 
 struct Layout {
-    size_t cut, part, part_l, lse2, base, scores, bytes;
+    size_t cut, part, part_l, lse2, base, seqs, scores, bytes;
 };
 inline Layout layout(const KvCacheArgs &c, int sms, int H, int n, int max_tokens, int64_t max_slots) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Layout L;
-    // for the most rows that parts of units may have together, so that what is enough for some max_tokens is enough for fewer
-    const size_t rows = (size_t)sms * 2 * 128;
+    // rows of two parts for each CTA, 64 on one CTA a multiprocessor or 32 on two: whatever max_tokens is, so that what is enough
+    // for some is enough for fewer
+    const size_t rows = (size_t)sms * 2 * 64;
     L.cut = 0;
-    L.part = up(sizeof(Cut) * sms * 4);
+    L.part = up(sizeof(Cut) * sms * 2);
     L.part_l = L.part + up(rows * padded(c.d) * 4);
     L.lse2 = L.part_l + up(rows * 4);
     L.base = L.lse2 + (max_slots ? up((size_t)n * max_tokens * H * 4) : 0);
-    L.scores = L.base + (max_slots ? up(((size_t)n + 2) * 8) : 0);
+    L.seqs = L.base + (max_slots ? up(((size_t)n + 2) * 8) : 0);
+    L.scores = L.seqs + (max_slots ? up((size_t)n * 16) : 0);
     L.bytes = L.scores + (max_slots ? up(((size_t)max_slots / 64 + n) * 64 * max_tokens * H * 4) : 0);
     return L;
 }
@@ -97,6 +108,7 @@ int launch_kv_decode(const KvDecodeArgs &a, cudaStream_t st) {
     p.part_l = reinterpret_cast<float *>(ws + L.part_l);
     p.lse2 = reinterpret_cast<float *>(ws + L.lse2);
     p.base = reinterpret_cast<int64_t *>(ws + L.base);
+    p.seqs = reinterpret_cast<int4 *>(ws + L.seqs);
     p.scores = reinterpret_cast<float *>(ws + L.scores);
     int rc = a.c.fp16 ? launch_decode_fp16(p, st) : launch_decode_bf16(p, st);
     if (rc == KDA_OK && a.add_weights) {

@@ -66,6 +66,7 @@ struct DecodeP {
     float *lse2;      // [n max_tokens][H] log2 of the rows' sums (add_weights)
     int64_t *base;    // [n + 1] tiles of 64 tokens before each sequence (add_weights), INT64_MAX behind those that take part;
                       // then the number of tiles
+    int4 *seqs;       // [n] table row, tokens and queries (add_weights)
     float *scores;    // see score_at()
 };
 
@@ -166,6 +167,7 @@ __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
             if (a.add_weights && g == 0) {
                 // sequences that pass the bound are the last ones with tokens, and the third launch ends before them
                 p.base[b + 1] = slots <= a.max_slots ? tiles : INT64_MAX;
+                p.seqs[b] = make_int4(s.row, s.len, s.nq, 0);
                 if (slots > a.max_slots) {
                     if (t) set_status(a.status, KDA_DEV_BAD_SEQLENS);
                     if (t && slots - s.len <= a.max_slots) p.base[a.n + 1] = tiles - tiles64(s);

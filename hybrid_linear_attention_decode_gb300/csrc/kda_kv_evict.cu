@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) kda_kv_evict_kernel(const KvEvi
     u.open = a.since ? (uint32_t)max(a.since[i], a.first) - a.first : 0x80000000u - a.first;
     u.trow = a.t.table + (int64_t)row * a.t.max_pages;
     const bool bad_len = u.len < 0 || u.len > (int64_t)a.t.max_pages * a.c.page_size;
-    if (bad_len || u.keep < 0 || u.len <= u.keep || u.len > KDA_KV_EVICT_MAX_LEN) {
+    if (bad_len || u.keep < 0 || u.len <= u.keep || u.len > a.max_len) {
         if (tells) {
             a.new_lens[i] = bad_len ? 0 : u.len;
             if (bad_len || u.keep < 0 || u.len > u.keep) set_status(a.status, KDA_DEV_BAD_SEQLENS);
@@ -322,10 +322,11 @@ __global__ void __launch_bounds__(ET, 1024 / ET) kda_kv_evict_kernel(const KvEvi
                     all[0] &= hi[n], any[0] |= hi[n];
                     all[1] &= lo[n], any[1] |= lo[n];
                 }
+                int left = size;  // pairs that may still be it
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t differ = __reduce_or_sync(FULL, any[half]) & ~__reduce_and_sync(FULL, all[half]);
-                    for (; differ; differ &= ~(0x80000000u >> __clz(differ))) {
+                    for (; differ && left > 1; differ &= ~(0x80000000u >> __clz(differ))) {
                         const int bit = 31 - __clz(differ);
                         uint32_t set = 0;
                         int above = 0;
@@ -336,8 +337,10 @@ __global__ void __launch_bounds__(ET, 1024 / ET) kda_kv_evict_kernel(const KvEvi
                         }
                         if (above >= need) {
                             in &= set;
+                            left = above;
                         } else {
                             need -= above;
+                            left -= above;
                             in &= ~set;
                         }
                     }
@@ -526,7 +529,7 @@ inline Variant variant(int64_t units, int C, int64_t cap) {
 int launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {
     using namespace kv;
     const int64_t units = (int64_t)a.n * a.c.layers * a.c.heads;
-    const int64_t cap = std::min<int64_t>((int64_t)a.t.max_pages * a.t.page_size, KDA_KV_EVICT_MAX_LEN);
+    const int64_t cap = a.max_len;
     const int words = (int)((cap + BLOCK - 1) / BLOCK * (BLOCK / 32));
     // CTAs of a unit: more where there are few units, while each has 1,024 slots or more (384 units of 2,000 to 8,192 tokens, of
     // which 1,024 stay: 76 us with one CTA each, 87 with two)

@@ -542,9 +542,9 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  *   q          device [num_tokens][H][head_dim], the cache's type, at the given token and head strides (elements,
  *              multiples of 8), 16-byte aligned; H a multiple of the cache's heads
  *   out        device [num_tokens][H][head_dim] contiguous, the cache's type, 16-byte aligned
- *   add_weights  1 (a cache with stats): each cached token's sum becomes weight_decay * sum + the weights that the
- *              sequence's queries give it in this call, summed over the query tokens and over the query heads that share
- *              its key-value head.  weight_decay from 0 to 1; max_slots as the workspace was asked for.  Shared pages
+ *   add_weights  1 (a cache with stats): the sum of each cached token of a sequence with queries becomes weight_decay * sum
+ *              + the weights that these give it in this call, summed over the query tokens and over the query heads that
+ *              share its key-value head.  weight_decay from 0 to 1; max_slots as the workspace was asked for.  Shared pages
  *              (refcount above 1) are never written, so their tokens' sums stay; refcount may not be NULL then.  No table
  *              row may appear twice in such a call.  Sequences whose slots pass max_slots, added up in order, are
  *              flagged (KDA_DEV_BAD_SEQLENS) and leave their sums as they were, their outputs are as always.  A query
@@ -556,9 +556,9 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  * and lse NaN (-infinity: weight 0); a seen value that is not finite makes its channel NaN or infinite, and where it is one
  * of several drafted tokens (nq above 1, or a tree_mask) all outputs and lse of the queries that see it NaN.
  * fp32 scores, sums and outputs; weights are rounded to the cache's type for the second product (in fp16 as for
- * kda_latent_decode), outputs at the end.  Results do not depend on the other sequences' contents, but a sequence's split over CTAs (and so its last bits) depends on all
- * lengths of the call and on the GPU's number of multiprocessors.  The workspace need not be initialised and keeps nothing
- * between calls; calls that overlap on the GPU need one each.
+ * kda_latent_decode), outputs at the end.  Results do not depend on the other sequences' contents, but a sequence's split
+ * over CTAs (and so its last bits) depends on all lengths of the call and on the GPU's number of multiprocessors.  The
+ * workspace need not be initialised and keeps nothing between calls; calls that overlap on the GPU need one each.
  * max_tokens <= KDA_KV_MAX_TOKENS, H <= KDA_KV_MAX_HEADS, n <= 65535.  A wait that gives up sets KDA_DEV_TIMEOUT (outputs
  * then are undefined).
  */
@@ -569,7 +569,7 @@ KDA_API int kda_kv_decode(const kda_kv_cache *cache, int32_t layer, const kda_pa
                           float weight_decay, int64_t max_slots, void *workspace, size_t workspace_bytes,
                           int32_t *dev_status, kda_stream_t stream);
 
-/* Most tokens of a row that kda_kv_evict takes. */
+/* Most tokens of a row that kda_kv_evict shortens. */
 #define KDA_KV_EVICT_MAX_LEN (1 << 20)
 
 /*
@@ -586,13 +586,16 @@ KDA_API int kda_kv_decode(const kda_kv_cache *cache, int32_t layer, const kda_pa
  *   rows      device [n] int32 or NULL (row i); -1 = a padding entry
  *   keep      device [n] int32, not negative; a row of at most keep[i] tokens stays as it is
  *   since     device [n] int32, or NULL (nothing is newest)
+ *   max_len   bound on the rows' lens, 0: what the table has room for; KDA_KV_EVICT_MAX_LEN at most.  It decides how much
+ *             shared memory a row takes: 64 rows of 2,112 tokens in 4 layers and 8 heads take 39 us with a bound of
+ *             2,240 and 77 us with one of 131,072
  *   new_lens  device [n] int32: min(len, keep[i]); 0 for padding entries; len for rows that are flagged and left as they
- *             are: a bad length or page, a row longer than KDA_KV_EVICT_MAX_LEN (0 for a bad row or length)
+ *             are: a bad page, more than keep[i] and max_len tokens, a negative keep[i] (0 for a bad row or length)
  * Flags: KDA_DEV_BAD_SLOT, _SEQLENS, _PAGE.  No row may appear twice in a call.  n <= 65535.
  */
 KDA_API int kda_kv_evict(const kda_kv_cache *cache, const kda_page_table *pt, int32_t n, const int32_t *rows,
-                         const int32_t *keep, int32_t first, const int32_t *since, int32_t *new_lens, int32_t *dev_status,
-                         kda_stream_t stream);
+                         const int32_t *keep, int32_t first, const int32_t *since, int32_t max_len, int32_t *new_lens,
+                         int32_t *dev_status, kda_stream_t stream);
 
 /*
  * Host-side prefix index and retention policies ("A Preview of Production-Scale Kimi K3 Support on vLLM",

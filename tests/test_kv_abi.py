@@ -48,8 +48,8 @@ def apply(lib, r=None, dtype=0, T=3, H=4, D=192, pos=P, inv=0, x=P, xs=(768, 192
     return lib.kda_rope_apply(ref(r or rope(dim=64, offset=128)), dtype, T, H, D, pos, inv, x, *xs, out, *os, None)
 
 
-def evict(lib, c=None, t=None, n=2, rows=None, keep=P, first=0, since=None, new=P, st=P):
-    return lib.kda_kv_evict(ref(c or cache()), ref(t or table()), n, rows, keep, first, since, new, st, None)
+def evict(lib, c=None, t=None, n=2, rows=None, keep=P, first=0, since=None, most=0, new=P, st=P):
+    return lib.kda_kv_evict(ref(c or cache()), ref(t or table()), n, rows, keep, first, since, most, new, st, None)
 
 
 BAD_CACHE = [(dict(pages=None), 1), (dict(dtype=2), 1), (dict(stats=2), 1), (dict(head_dim=8), 2), (dict(head_dim=264), 2),
@@ -115,7 +115,7 @@ def test_rope_refuses(lib, kw, rc):
 
 
 @pytest.mark.parametrize("kw", [dict(c=cache(stats=0, page_stride=64 * 8 * 256, layer_stride=100 * 64 * 8 * 256)), dict(n=-1),
-                                dict(n=65536), dict(first=-1), dict(keep=None), dict(new=None), dict(keep=P + 2),
+                                dict(n=65536), dict(first=-1), dict(most=-1), dict(most=(1 << 20) + 1), dict(keep=None), dict(new=None), dict(keep=P + 2),
                                 dict(since=P + 1), dict(rows=P + 2), dict(t=table(refcount=None)), dict(st=P + 3),
                                 dict(n=60000, c=cache(layers=200))])
 def test_evict_refuses(lib, kw):

@@ -96,6 +96,19 @@ def test_drafted_chains_and_trees(dtype, kv, G, d, page, tokens):
     assert int(st) == 0 and int(st2) == 0
 
 
+@pytest.mark.parametrize("kv,G,d,page,tokens", [(2, 32, 128, 64, 5), (1, 128, 64, 16, 3), (1, 9, 200, 32, 10), (4, 16, 96, 128, 1)])
+def test_more_rows_than_a_unit(kv, G, d, page, tokens):
+    """More than 64 rows of a sequence on a key-value head, and calls that mix few and many of them."""
+    lens = [700, 64, 33, 2000, 5]
+    nq = [tokens, 1, tokens, 1, min(tokens, 5)]
+    p = Pages(lens, kv, d, page, seed=G)
+    p.poison()
+    q = queries(sum(nq), kv * G, d, torch.bfloat16)
+    out, lse, st = decode(p, q, nq)
+    compare(p, q, nq, out, lse)
+    assert int(st) == 0
+
+
 @pytest.mark.parametrize("kv,G,d,page,lens", [
     (2, 4, 128, 64, [50000]), (1, 1, 64, 16, [100001]), (4, 8, 128, 128, [9000, 1, 20000, 333]), (1, 16, 256, 64, [30000, 5]),
     (8, 4, 128, 32, [int(x) for x in np.random.default_rng(1).integers(1, 900, 90)]),
@@ -295,7 +308,7 @@ def test_sums_skip_bad_pages():
 
 
 # ------------------------------------------------------------------------------------------------- eviction
-def evict_and_compare(p, keep, rows=None, first=0, since=None, expect=0, skip=()):
+def evict_and_compare(p, keep, rows=None, first=0, since=None, expect=0, skip=(), max_len=0):
     """The call against the rules, every word of the cache; skip: entries that are left as they are."""
     cache, L, kv = p.cache, p.cache.data.shape[0], p.heads
     want = cache.data.clone()
@@ -328,7 +341,7 @@ def evict_and_compare(p, keep, rows=None, first=0, since=None, expect=0, skip=()
                     x[l, pb, h, sb] = x[l, pa, h, sa].clone()
     new, st = torch.full((len(keep),), -9, dtype=torch.int32, device=DEV), status()
     kda.kda_kv_evict(cache, p.pt, None if rows is None else i32(rows), i32(keep), new, st, first=first,
-                     since=None if since is None else i32(since))
+                     since=None if since is None else i32(since), max_len=max_len)
     assert int(st) == expect
     for got, n in zip(new.tolist(), expect_lens):
         assert n is None or got == n
@@ -364,6 +377,22 @@ def test_evict_long_rows(lens, keep, ties):
     p = Pages(lens, 2 if lens[0] < 200000 else 1, 16, 64, stats=True)
     heavy(p, ties=ties)
     evict_and_compare(p, keep, first=100, since=[99000] * len(lens))
+
+
+def test_evict_bound_of_lengths():
+    """Rows up to the bound are shortened; longer ones are flagged unless they stay as they are anyway."""
+    p = Pages([300, 200, 201, 199], 2, 32, 16, stats=True)
+    heavy(p)
+    new = evict_and_compare(p, [300, 50, 60, 70], max_len=200, expect=kda.KDA_DEV_BAD_SEQLENS, skip=(2,))
+    assert new == [300, 50, 201, 70]
+
+
+@pytest.mark.parametrize("room", [70, 300, 9000, 20000])
+def test_evict_of_short_rows_in_wide_tables(room):
+    p = Pages([100, 2000, 513, 64] * 40, 2, 16, 16, stats=True)
+    p.pt.table = torch.nn.functional.pad(p.pt.table, (0, max(0, room - p.pt.table.shape[1])), value=-1).contiguous()
+    heavy(p, ties=0.5)
+    evict_and_compare(p, [50, 1500, 512, 3] * 40, first=7)
 
 
 def test_evict_many_units():
