@@ -289,8 +289,9 @@ struct Config {
     static constexpr int ROWS = 8 * RW * RG;               // rows of a unit
     static constexpr int QROW = DP * 2 + 16;               // bytes of a query in shared memory: no bank conflicts
     static constexpr int QBYTES = ROWS * QROW;
-    static constexpr int FIT = (ROOM - 2 * MERGE - 2 * QBYTES) / STAGE, STAGES = FIT < 12 ? FIT : 12;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + 2 * MERGE + 2 * QBYTES;
+    static constexpr int TURNS = CW == 4 && RG == 2 ? 1 : 2;  // buffers for outputs (one where a fifth stage needs the room)
+    static constexpr int FIT = (ROOM - TURNS * MERGE - 2 * QBYTES) / STAGE, STAGES = FIT < 12 ? FIT : 12;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + TURNS * MERGE + 2 * QBYTES;
     static constexpr int GROUPS = CW / RG;
     static_assert(RG <= CW && BARS % GROUPS == 0 && STAGES <= BARS && STAGES >= 4, "");
     static constexpr bool Q_REGS = DP * RW <= 256;         // queries stay in registers
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *merge = reinterpret_cast<float *>(sm + STAGES * STAGE);  // [2][CW][64 channels][8 rows]
-    uint8_t *qs = sm + STAGES * STAGE + 2 * MERGE;                   // [2][ROWS][QROW]
+    uint8_t *qs = sm + STAGES * STAGE + C::TURNS * MERGE;                   // [2][ROWS][QROW]
     __shared__ uint64_t full[BARS], empty[BARS], q_full[2], q_empty[2];
     __shared__ Scratch scratch;
     __shared__ Part parts[2];
@@ -709,7 +710,10 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                 for (int ch = 0; ch < CH; ++ch)
                     if (ch * 64 < d) {
                         float *half = merge + turn * (MERGE / 4);
-                        turn ^= 1;
+                        if (C::TURNS == 2)
+                            turn ^= 1;
+                        else if (h + ch > 0)
+                            sync_threads(1, CW * 32);  // all have read what is there
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float *to = half + ((warp * 64 + k * 16 + top) * 8 + 2 * quad);
