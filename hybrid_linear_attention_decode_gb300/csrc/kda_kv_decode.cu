@@ -6,9 +6,14 @@ namespace kv {
 
 constexpr int WW = 8;  // warps of a CTA of the third launch
 
-// sum = decay * sum + sum over rows of 2^(x - lse2): a warp for 64 tokens of one key-value head (an item), two tokens a lane.
-// A CTA has a contiguous part of the items, so that it looks for a sequence once.
-__global__ void __launch_bounds__(WW * 32) kda_kv_weights_kernel(const DecodeP p) {
+// sum = decay * sum + sum over rows of 2^(x - lse2): a warp for 64 tokens of one key-value head (an item), two tokens a lane, or
+// (MANY rows) several that divide the rows where there are few items.  A CTA has a contiguous part of the items, so that it
+// looks for a sequence once; all CTAs are on the GPU at once.
+template <bool MANY>
+constexpr int kWeightCtas = MANY ? 5 : 8;  // on a multiprocessor
+template <bool MANY>
+__global__ void __launch_bounds__(WW * 32, kWeightCtas<MANY>) kda_kv_weights_kernel(const DecodeP p) {
+    __shared__ float2 sums[MANY ? WW : 1][32];
     wait_for_previous();
     allow_dependent_launch();
     const KvDecodeArgs &a = p.a;
@@ -17,7 +22,10 @@ __global__ void __launch_bounds__(WW * 32) kda_kv_weights_kernel(const DecodeP p
     const int64_t per = items >> 31 ? (items + gridDim.x - 1) / gridDim.x : ((uint32_t)items + gridDim.x - 1) / gridDim.x;
     const int64_t i0 = min(items, blockIdx.x * per), tile0 = i0 >> 31 ? i0 / kv : (uint32_t)i0 / kv;
     const int head0 = (int)(i0 - tile0 * kv), count = (int)(min(items, i0 + per) - i0);
-    if (warp >= count) return;
+    int split = 1;  // warps of an item, with eight rows each or more
+    while (MANY && split < WW && split * 16 <= p.G * a.max_tokens && items * split * 2 <= gridDim.x * WW) split *= 2;
+    const int at_once = WW / split, mine = warp / split, slice = warp % split;
+    if (count == 0) return;
     int b = 0, hi = a.n + 1;  // the last sequence that does not begin behind the tile, 32 ways a step
     while (hi - b > 1) {
         const int step = (hi - b + 31) / 32, at = b + lane * step;
@@ -27,36 +35,63 @@ __global__ void __launch_bounds__(WW * 32) kda_kv_weights_kernel(const DecodeP p
     }
     int64_t begin = p.base[b], end = p.base[b + 1];
     int4 s = p.seqs[b];  // row, tokens, queries
-    for (int i = warp; i < count; i += WW) {
-        const int t0 = (head0 + i) / kv, hk = head0 + i - t0 * kv;
-        const int64_t tile = tile0 + t0;
-        while (end <= tile) {
-            begin = end;
-            end = p.base[++b + 1];
-            s = p.seqs[b];
-        }
-        const int key = (int)(tile - begin) * 64 + 2 * lane, rows = s.z * p.G;
-        if (key >= s.y) continue;
-        const int32_t page = a.t.table[(int64_t)s.x * a.t.max_pages + key / ps];
-        const bool good = page_ok(a.t, page);
-        float *w = reinterpret_cast<float *>(a.c.pages + (good ? page * a.c.page_stride : 0) + stats_at(a.c, hk)) + key % ps;
-        const bool mine = good && a.t.refcount[good ? page : 0] <= 1;
-        const float2 sum = *reinterpret_cast<const float2 *>(w);
-        const float *x = p.scores + (tile * a.max_tokens * a.H + hk * rows) * 64 + 2 * lane;  // see score_at()
-        const float *lse = p.lse2 + (int64_t)b * a.max_tokens * a.H + hk * p.G;
-        float2 add = make_float2(0.f, 0.f);
-        for (int t = 0; t < s.z; ++t, lse += a.H)
-#pragma unroll 8
-            for (int g = 0; g < p.G; ++g, x += 64) {
-                const float l2 = lse[g];
-                const float2 v = __ldcs(reinterpret_cast<const float2 *>(x));
-                const bool some = l2 > -INFINITY;  // (not NaN)
-                add.x += some ? exp2_(v.x - l2) : 0.f;
-                add.y += some ? exp2_(v.y - l2) : 0.f;
+    for (int j = 0; j < count; j += at_once) {
+        const int i = j + mine;
+        float2 add = make_float2(0.f, 0.f), sum = add;
+        float *w = nullptr;
+        int key = 0;
+        bool stays = true;
+        if (i < count) {
+            const int t0 = (head0 + i) / kv, hk = head0 + i - t0 * kv;
+            const int64_t tile = tile0 + t0;
+            while (end <= tile) {
+                begin = end;
+                end = p.base[++b + 1];
+                s = p.seqs[b];
             }
-        if (!mine) continue;
-        w[0] = a.decay * sum.x + add.x;
-        if (key + 1 < s.y) w[1] = a.decay * sum.y + add.y;
+            key = (int)(tile - begin) * 64 + 2 * lane;
+            const int rows = s.z * p.G;
+            if (key < s.y) {
+                // read without waiting for one another: a bad page's place is page 0
+                const int32_t page = a.t.table[(int64_t)s.x * a.t.max_pages + key / ps];
+                const bool good = page_ok(a.t, page);
+                const int32_t place = good ? page : 0;
+                w = reinterpret_cast<float *>(a.c.pages + place * a.c.page_stride + stats_at(a.c, hk)) + key % ps;
+                sum = *reinterpret_cast<const float2 *>(w);
+                stays = !good || slice != 0 || a.t.refcount[place] > 1;
+                const float *x = p.scores + (tile * a.max_tokens * a.H + (int64_t)hk * rows) * 64 + 2 * lane;  // see score_at()
+                const float *lse = p.lse2 + (int64_t)b * a.max_tokens * a.H + hk * p.G;
+                auto row = [&](const float *l, const float *y) {
+                    const float l2 = *l;
+                    const float2 v = __ldcs(reinterpret_cast<const float2 *>(y));
+                    const bool some = l2 > -INFINITY;  // (not NaN)
+                    add.x += some ? exp2_(v.x - l2) : 0.f;
+                    add.y += some ? exp2_(v.y - l2) : 0.f;
+                };
+                if (!MANY || split == 1) {
+                    for (int t = 0; t < s.z; ++t, lse += a.H)
+#pragma unroll 8
+                        for (int g = 0; g < p.G; ++g, x += 64) row(lse + g, x);
+                } else {
+#pragma unroll 8
+                    for (int r = slice; r < rows; r += split) row(lse + r + over_g(p, r) * (a.H - p.G), x + r * 64);
+                }
+            }
+        }
+        if (MANY && split > 1) {
+            sums[warp][lane] = add;
+            __syncthreads();
+            if (slice == 0)
+                for (int k = 1; k < split; ++k) {
+                    add.x += sums[warp + k][lane].x;
+                    add.y += sums[warp + k][lane].y;
+                }
+            __syncthreads();
+        }
+        if (!stays) {
+            w[0] = a.decay * sum.x + add.x;
+            if (key + 1 < s.y) w[1] = a.decay * sum.y + add.y;
+        }
     }
 }
 
@@ -112,7 +147,10 @@ int launch_kv_decode(const KvDecodeArgs &a, cudaStream_t st) {
     p.scores = reinterpret_cast<float *>(ws + L.scores);
     int rc = a.c.fp16 ? launch_decode_fp16(p, st) : launch_decode_bf16(p, st);
     if (rc == KDA_OK && a.add_weights) {
-        dependent_launch(kda_kv_weights_kernel, dim3((unsigned)sms * 8), WW * 32, 0, st, p);
+        if (p.G * a.max_tokens < 16)
+            dependent_launch(kda_kv_weights_kernel<false>, dim3((unsigned)sms * kWeightCtas<false>), WW * 32, 0, st, p);
+        else
+            dependent_launch(kda_kv_weights_kernel<true>, dim3((unsigned)sms * kWeightCtas<true>), WW * 32, 0, st, p);
         rc = launch_result("kda_kv_weights_kernel launch");
     }
     return rc;

@@ -50,9 +50,10 @@ using latent::kRaise;
 template <int DP, int CW>
 constexpr int kTile = DP == 256 ? 16 : (CW >= 4 ? 4096 : 2048) / DP;  // tokens
 
-struct Cut {  // where a CTA's part of the list begins: place `off` of unit u of sequence b; places of a whole part
-    int32_t b, u, off, pad;
-    int64_t per;
+struct Cut {  // where a CTA's part of the list begins: place `off` of unit u of sequence b, which has nq queries from c0 on and
+              // units of `tiles` tiles; places of a whole part
+    int64_t c0, per;
+    int32_t b, u, off, nq, tiles, pad;
 };
 
 struct DecodeP {
@@ -78,7 +79,8 @@ struct Range {  // a CTA's part of the list
 
 struct Scratch {
     int64_t scan[3][12];
-    int64_t b, u, off, tiles, slots;
+    int64_t b, u, off, tiles, slots, c0;
+    int32_t nq, unit_tiles;
 };
 
 __device__ __forceinline__ int units_of(const DecodeP &p, const Seq &s) {
@@ -132,7 +134,8 @@ __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
     }
     if (tid == 0) {
         sh->b = a.n;
-        sh->u = sh->off = sh->tiles = sh->slots = 0;
+        sh->u = sh->off = sh->tiles = sh->slots = sh->c0 = 0;
+        sh->nq = sh->unit_tiles = 0;
     }
     __syncthreads();
     for (int w = 0; w < NT / 32; ++w) {
@@ -157,6 +160,9 @@ __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
                 sh->off = (R.lo - at) % (t + START);
                 sh->tiles = tiles;
                 sh->slots = slots;
+                sh->c0 = s.c0;
+                sh->nq = s.nq;
+                sh->unit_tiles = t;
                 if (!(a.add_weights && g == 0)) break;
             }
             at += places;
@@ -193,7 +199,7 @@ __device__ __forceinline__ Range range_of(const DecodeP &p, Scratch *sh) {
     R.off = (int32_t)sh->off;
     R.tiles = sh->tiles;
     R.slots = sh->slots;
-    if (tid == 0) p.cut[g] = Cut{R.b, R.u, R.off, 0, R.per};
+    if (tid == 0) p.cut[g] = Cut{sh->c0, R.per, R.b, R.u, R.off, sh->nq, sh->unit_tiles, 0};
     return R;
 }
 
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                 ++n;
                 // the table's entries by 32 at a time, the next ones on their way while these are used
                 int page0 = first * TILE / ps, in_page = first * TILE - page0 * ps;
-                const int pages = (s.len + ps - 1) / ps;
+                const int pages = (s.len - 1) / ps + 1;
                 auto entries = [&](int from) { return from + lane < pages ? trow[from + lane] : (int32_t)num_pages; };
                 int32_t now = entries(page0), next = entries(page0 + 32);
                 int in_now = 0;  // the tile's first page among these
@@ -748,10 +754,9 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
 
 constexpr int JW = 16;  // warps of a joining CTA
 
-// Joins the parts of the unit that the beginning of part blockIdx.x + 1 of the list cuts, if no earlier beginning does.  A
-// row's parts are divided among as many warps as there are for it, a lane has channels 4 lane .. 4 lane + 3 and those 128
-// further on.
-template <bool FP16, int DP, int TILE>
+// Joins the parts of a cut unit: the CTAs of all beginnings of parts that lie within it share its rows.  A row's parts are divided
+// among as many warps as there are for it; a lane has channels 4 lane .. 4 lane + 3 and those 128 further on.
+template <bool FP16, int DP>
 __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
     constexpr int V = (DP + 127) / 128;
     __shared__ float4 sm_o[JW][V][32];
@@ -761,27 +766,25 @@ __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
     const KvDecodeArgs &a = p.a;
     const int g = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cut c = p.cut[g];
-    if (c.b >= a.n || c.off <= START || c.off - c.per > START) return;
-    const Seq s = seq_of(a, c.b);
-    const int rem = tiles_of<TILE>(s) + START - c.off;
-    const int parts = 1 + (int)((rem + c.per - 1) / c.per);
-    const int nrb = units_of(p, s) / a.c.heads, hk = c.u / nrb, block = p.block, r0 = (c.u - hk * nrb) * block;
-    const int rows = min(block, s.nq * p.G - r0);
+    if (c.b >= a.n || c.off <= START) return;  // nothing of the unit lies before
+    const int nth = (int)((c.off - START - 1) / c.per);  // this is the unit's nth beginning, from 0, with tiles before it
+    const int64_t rem = c.tiles + START - (c.off - nth * c.per);
+    const int parts = 1 + (int)((rem + c.per - 1) / c.per), g0 = g - nth - 1;  // the first part is CTA g0's
+    const int total = c.nq * p.G, nrb = (total + p.block - 1) / p.block, hk = c.u / nrb, r0 = (c.u - hk * nrb) * p.block;
+    const int rows = min(p.block, total - r0), share = parts - 1;  // rows nth, nth + share, ... are this CTA's
+    const int mine = rows > nth ? (rows - nth + share - 1) / share : 0;
     int per_row = 1;  // warps of a row
-    while (per_row * 2 * rows <= JW && per_row * 2 <= parts) per_row *= 2;
-    for (int first = 0; first < rows; first += JW / per_row) {
-        const int row = first + warp / per_row, k = warp % per_row;
-        const bool mine = row < rows;
-        auto at = [&](int i) { return ((int64_t)(g - 1 + i) * 2 + (i == 0)) * block + row; };
+    while (per_row * 2 * mine <= JW && per_row * 2 <= parts) per_row *= 2;
+    for (int first = 0; first < mine; first += JW / per_row) {
+        const int row = nth + (first + warp / per_row) * share, k = warp % per_row;
+        const bool here = row < rows;
+        auto at = [&](int i) { return ((int64_t)(g0 + i) * 2 + (i == 0)) * p.block + row; };
         float m = -INFINITY, sum = 0.f;
         float4 o[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mine) {
-            for (int i = k + lane * per_row; i < parts; i += 32 * per_row) {
-                const float x = p.part_l[at(i)];
-                m = fmaxf(m, x);
-            }
+        if (here) {
+            for (int i = k + lane * per_row; i < parts; i += 32 * per_row) m = fmaxf(m, p.part_l[at(i)]);
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, w));
             const float mm = m == -INFINITY ? 0.f : m;
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
             sm_w[warp] = sum;
         }
         __syncthreads();
-        if (mine && k == 0) {
+        if (here && k == 0) {
             float M = m;
             for (int w = 1; w < per_row; ++w) M = fmaxf(M, sm_m[warp + w]);
             const float mm = M == -INFINITY ? 0.f : M;
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
             for (int v = 0; v < V; ++v) x[v] = make_float4(0.f, 0.f, 0.f, 0.f);
             float L = 0.f;
             for (int w = 0; w < per_row; ++w) {
-                const float f = exp2_(sm_m[warp + w] == -INFINITY ? -INFINITY : sm_m[warp + w] - mm);
+                const float f = exp2_(sm_m[warp + w] - mm);  // (of warps whose parts have no weight: 0)
                 L += f * sm_w[warp + w];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -830,17 +833,17 @@ __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
                 }
             }
             const float inv = L == 0.f ? 0.f : 1.f / L;
-            const int r = r0 + row, t = r / p.G, h = hk * p.G + r - t * p.G;
+            const int r = r0 + row, t = over_g(p, r), h = hk * p.G + r - t * p.G;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int ch = v * 128 + 4 * lane;
                 if (ch < a.c.d)
-                    *reinterpret_cast<uint2 *>(a.out + ((s.c0 + t) * a.H + h) * a.c.d + ch) =
+                    *reinterpret_cast<uint2 *>(a.out + ((c.c0 + t) * a.H + h) * a.c.d + ch) =
                         make_uint2(latent::pack2<FP16>(x[v].x * inv, x[v].y * inv), latent::pack2<FP16>(x[v].z * inv, x[v].w * inv));
             }
             if (lane == 0) {
                 const float l2 = L == 0.f ? -INFINITY : mm + log2f(L);
-                if (a.lse) a.lse[(s.c0 + t) * a.H + h] = l2 * latent::kLn2;
+                if (a.lse) a.lse[(c.c0 + t) * a.H + h] = l2 * latent::kLn2;
                 if (a.add_weights) p.lse2[((int64_t)c.b * a.max_tokens + t) * a.H + h] = l2;
             }
         }
@@ -879,7 +882,7 @@ int launch_as(DecodeP p, cudaStream_t st) {
     if (allow_smem(k, prepared) == cudaSuccess) dependent_launch(k, dim3((unsigned)p.groups), C::NT, C::SMEM, st, p, map);
     int rc = launch_result("kda_kv_decode_kernel launch");
     if (rc == KDA_OK && p.groups > 1) {
-        dependent_launch(kda_kv_join_kernel<FP16, DP, C::TILE>, dim3((unsigned)p.groups - 1), JW * 32, 0, st, p);
+        dependent_launch(kda_kv_join_kernel<FP16, DP>, dim3((unsigned)p.groups - 1), JW * 32, 0, st, p);
         rc = launch_result("kda_kv_join_kernel launch");
     }
     return rc;
