@@ -379,6 +379,12 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                 const int first = max(off - START, 0), nt = max(off + take - START, 0) - first;
                 at += take;
                 if (nt == 0) continue;
+                // the table's entries by 32 at a time, the next ones on their way while these are used
+                int page0 = first * TILE / ps, in_page = first * TILE - page0 * ps;
+                const int pages = (s.len - 1) / ps + 1;
+                auto entries = [&](int from) { return from + lane < pages ? trow[from + lane] : (int32_t)num_pages; };
+                int32_t now = entries(page0), next = entries(page0 + 32);
+                int in_now = 0;  // the tile's first page among these
                 const int hk = u / nrb, r0 = (u - hk * nrb) * ROWS, live = min(ROWS, total - r0);
                 const int slot = n & 1;
                 if (n >= 2) ok = latent::warp_wait(q_empty + slot, (n / 2 - 1) & 1);
@@ -395,12 +401,6 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                              a.q + (s.c0 + t) * a.q_ts + (int64_t)(hk * G + r0 + r - t * G) * a.q_hs, d * 2, q_full + slot);
                 }
                 ++n;
-                // the table's entries by 32 at a time, the next ones on their way while these are used
-                int page0 = first * TILE / ps, in_page = first * TILE - page0 * ps;
-                const int pages = (s.len - 1) / ps + 1;
-                auto entries = [&](int from) { return from + lane < pages ? trow[from + lane] : (int32_t)num_pages; };
-                int32_t now = entries(page0), next = entries(page0 + 32);
-                int in_now = 0;  // the tile's first page among these
                 const int at_row = (value * kv + hk) * ps;
                 for (int j = 0, rest = s.len - first * TILE - box; j < nt; ++j, ++it, rest -= TILE) {
                     uint32_t page = (uint32_t)__shfl_sync(FULL, now, (in_now + box_page) & 31);

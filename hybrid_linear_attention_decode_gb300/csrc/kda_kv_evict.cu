@@ -6,8 +6,8 @@
 //
 //   select  the keep-th largest pair of key and slot (lower slots count as larger) byte by byte: a histogram of 256 bins in
 //           shared memory (four copies, so that lanes with equal bytes meet less; atomics on counts: their order does not
-//           matter), summed over the cluster.  It ends when a bin is taken whole, or when a bin has so few pairs that each
-//           can be compared with all others
+//           matter), summed over the cluster.  It ends when a bin is taken whole, or when a bin has so few pairs that
+//           votes of one warp find the last one
 //   mark    one bit a slot, kept or not, in every CTA of the cluster; prefix sums over blocks of 256 slots of the holes (dropped,
 //           below keep) and of the sources (kept, at or behind keep), of which there are as many; both listed in order, where
 //           the keys were
@@ -30,7 +30,7 @@ namespace cg = cooperative_groups;
 
 constexpr int BINS = 256, COPIES = 4;
 constexpr int SHORT = 4096;         // slots of a row for which a CTA has 128 threads
-constexpr int FEW = 128;            // pairs that are compared with one another
+constexpr int FEW = 128;            // pairs among which one warp finds the last
 constexpr int BLOCK = 256;          // slots of a prefix sum's block
 constexpr int KEYS = 16384;         // most keys of a CTA that stay in shared memory; more are made again from the pages
 constexpr int MAX_CLUSTER = 8;
@@ -98,7 +98,8 @@ struct Border {
 
 // keys_max: keys of a CTA that there is room for.
 template <int ET, bool CLUSTER>
-__global__ void __launch_bounds__(ET, 1024 / ET) kda_kv_evict_kernel(const KvEvictArgs a, const PageSize ps, int words_max, int keys_max) {
+__global__ void __launch_bounds__(ET, 1024 / ET)
+    kda_kv_evict_kernel(const KvEvictArgs a, const PageSize ps, int words_max, int keys_max) {
     constexpr int EW = ET / 32;
     constexpr int UNROLL = 4;  // 16-byte words of a lane in flight while rows move
     constexpr int AHEAD = 2;   // groups of four slots of a thread in flight while keys are read
@@ -371,9 +372,8 @@ __global__ void __launch_bounds__(ET, 1024 / ET) kda_kv_evict_kernel(const KvEvi
             const uint4 k = stay ? *reinterpret_cast<const uint4 *>(kept + j - s0) : keys_again(a, u, ps, j);
             const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 word |= (uint32_t)(x[e] > t.key || (x[e] == t.key && 0xffffffu - (j + e) >= t.slot)) << e;
-            }
         }
         // eight threads' bits are a word, which every CTA of the cluster gets
         word <<= 4 * (lane & 7);

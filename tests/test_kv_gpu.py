@@ -128,6 +128,25 @@ def test_long_and_many(kv, G, d, page, lens):
     assert bool(torch.isfinite(out).all())
 
 
+def test_thousands_of_entries_with_repeats_and_padding():
+    """65535 entries, most of them padding; table rows repeat; the others' outputs are those of a small call."""
+    p = Pages([100, 0, 333, 17], 2, 64, 16)
+    n = 65535
+    rows = torch.full((n,), -1, dtype=torch.int32)
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(1))[:1500]
+    rows[at] = torch.randint(0, 4, (1500,), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    q = queries(n, 4, 64, torch.bfloat16)
+    out, lse, st = decode(p, q, [1] * n, rows=rows.cuda(), cu=None)
+    assert int(st) == 0
+    pad = rows.cuda() < 0
+    assert bool((out[pad] == 0).all()) and bool((lse[pad] == -math.inf).all())
+    for b in at[:12].tolist():
+        row = int(rows[b])
+        o, l, _ = attention(p, 0, row, q[b:b + 1], 1 / 8)
+        check(out[b:b + 1], *o)
+        check(lse[b:b + 1], *l)
+
+
 def test_padding_bad_entries_and_rows_behind():
     lens = [100, 70, 5, 200]
     p = Pages(lens, 2, 64, 16, max_seqs=5)
@@ -432,6 +451,17 @@ def test_evict_odd_sums():
         evict_and_compare(p, [keep])
 
 
+def test_evict_thousands_of_padding_entries():
+    p = Pages([100, 80], 2, 64, 16, stats=True)
+    heavy(p)
+    n = 5000
+    rows = [-1] * n
+    rows[1234], rows[4999] = 1, 0
+    keep = [5] * n
+    new = evict_and_compare(p, keep, rows=rows)
+    assert [x for x in new if x] == [5, 5] and new[1234] == 5 and new[4999] == 5
+
+
 def test_evict_refused_rows_stay():
     p = Pages([100, 80, 90, 60, 70], 2, 64, 16, stats=True, max_seqs=6)
     heavy(p)
@@ -580,6 +610,21 @@ def test_captured_step_follows_its_inputs():
         torch.cuda.synchronize()
         for s, w in zip(states, want):
             assert all(torch.equal(a, b) for a, b in zip(fields(s), w)) and int(s["st"]) == 0
+
+
+def test_calls_of_other_sizes_share_one_workspace():
+    """What is enough for the largest is enough for all; nothing is kept in it between calls."""
+    p = Pages([700, 64, 33, 1500], 2, 64, 16, stats=True)
+    nbytes = kda.kda_kv_decode_workspace_bytes(p.cache, 64, 4, 8, 4000)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    for H, nq, decay in ((64, [8, 8, 8, 8], 1.0), (2, [1, 1, 1, 1], None), (64, [1, 2, 0, 3], 0.5), (8, [5, 1, 1, 1], None),
+                         (32, [1, 1, 1, 1], 1.0)):
+        assert kda.kda_kv_decode_workspace_bytes(p.cache, H, 4, max(nq), 4000 if decay else 0) <= nbytes
+        sums = p.cache.weights.clone()
+        q = queries(sum(nq), H, 64, torch.bfloat16, seed=H)
+        out, lse, st = decode(p, q, nq, decay=decay, max_slots=4000 if decay else None, ws=ws)
+        compare(p, q, nq, out, lse, sums=sums if decay else None, decay=decay)
+        assert int(st) == 0 and (decay or torch.equal(sums, p.cache.weights))
 
 
 def test_calls_on_a_given_stream_and_repeats_are_the_same():
