@@ -134,7 +134,6 @@ int launch_kv_decode(const KvDecodeArgs &a, cudaStream_t st) {
     p.G = a.H / a.c.heads;
     p.inverse_g = p.G == 1 ? 0 : (uint32_t)(((uint64_t)1 << 32) / p.G + 1);
     p.block = block_rows(p.G, a.max_tokens);
-    p.whole = a.c.d % 64 == 0;
     const int sms = current_device_sms();
     const Layout L = layout(a.c, sms, a.H, a.n, a.max_tokens, a.max_slots);
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
@@ -145,7 +144,8 @@ int launch_kv_decode(const KvDecodeArgs &a, cudaStream_t st) {
     p.base = reinterpret_cast<int64_t *>(ws + L.base);
     p.seqs = reinterpret_cast<int4 *>(ws + L.seqs);
     p.scores = reinterpret_cast<float *>(ws + L.scores);
-    int rc = a.c.fp16 ? launch_decode_fp16(p, st) : launch_decode_bf16(p, st);
+    int rc = a.c.d % 64 == 0 ? (a.c.fp16 ? launch_decode_fp16(p, st) : launch_decode_bf16(p, st))
+                             : (a.c.fp16 ? launch_decode_fp16_odd(p, st) : launch_decode_bf16_odd(p, st));
     if (rc == KDA_OK && a.add_weights) {
         if (p.G * a.max_tokens < 16)
             dependent_launch(kda_kv_weights_kernel<false>, dim3((unsigned)sms * kWeightCtas<false>), WW * 32, 0, st, p);
