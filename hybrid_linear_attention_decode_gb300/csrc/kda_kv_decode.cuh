@@ -461,7 +461,9 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
         auto token_at = [&](int r) {  // a token's first 64 channels within a tile's keys or values, r a multiple of 8
             return WHOLE ? r * (DP * 2) : (r & ~(rows - 1)) * (DP * 2) + (r & (rows - 1)) * 128;
         };
-        const float sl = a.scale * latent::kLog2e;
+        // scores stay as the products are until the exponential, whose argument is one operation then
+        const float sl = a.scale * latent::kLog2e, raise_by = kRaise<FP16> / sl;
+        const uint64_t sl2 = latent::pair(sl, sl);
         int it = 0;
         for (int n = 0;; ++n) {
             const int slot = n & 1;
@@ -557,12 +559,6 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                         for (int h = 0; h < RW; ++h) mma<FP16>(c[t][h], x, qk[h][0], qk[h][1]);
                     }
                 }
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int h = 0; h < RW; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) c[t][h][e] *= sl;
                 if (edge) {
 #pragma unroll
                     for (int h = 0; h < RW; ++h)
@@ -592,8 +588,8 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                             if (r < total) {
 #pragma unroll
                                 for (int t = 0; t < MT; ++t) {
-                                    out[t * 16] = c[t][h][f];
-                                    out[t * 16 + 8] = c[t][h][2 + f];
+                                    out[t * 16] = c[t][h][f] * sl;
+                                    out[t * 16 + 8] = c[t][h][2 + f] * sl;
                                 }
                             }
                         }
@@ -607,7 +603,7 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                         x[h][f] = fmaxf(c[0][h][f], c[0][h][2 + f]);
 #pragma unroll
                         for (int t = 1; t < MT; ++t) x[h][f] = fmaxf(x[h][f], fmaxf(c[t][h][f], c[t][h][2 + f]));
-                        raise |= x[h][f] > m[h][f] + kRaise<FP16>;
+                        raise |= x[h][f] > m[h][f] + raise_by;
                     }
                 if (__any_sync(FULL, raise)) {
 #pragma unroll
@@ -619,8 +615,8 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                             y = fmaxf(y, __shfl_xor_sync(FULL, y, 8));
                             y = fmaxf(y, __shfl_xor_sync(FULL, y, 16));
                             y = fmaxf(y, m[h][f]);
-                            const float z = y == -INFINITY ? 1.f : exp2_(m[h][f] - y);
-                            m[h][f] = y;
+                            const float z = y == -INFINITY ? 1.f : exp2_((m[h][f] - y) * sl);
+                            m[h][f] = y * sl == INFINITY ? NAN : y;  // a score past fp32 makes all weights NaN
                             l[h][f] *= z;
 #pragma unroll
                             for (int k = 0; k < DP / 16; ++k) {
@@ -633,19 +629,24 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                 uint32_t b[MT][RW][2];
 #pragma unroll
                 for (int h = 0; h < RW; ++h) {
-                    float less[2];
+                    float up[2];
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) less[f] = (m[h][f] == -INFINITY ? 0.f : m[h][f]) - kBias<FP16>;
+                    for (int f = 0; f < 2; ++f) up[f] = m[h][f] == -INFINITY ? kBias<FP16> : fmaf(-m[h][f], sl, kBias<FP16>);
+                    const uint64_t up2 = latent::pair(up[0], up[1]);
+                    uint64_t sum = latent::pair(l[h][0], l[h][1]);
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            c[t][h][e] = exp2_(c[t][h][e] - less[e & 1]);
-                            l[h][e & 1] += c[t][h][e];
+                        for (int e = 0; e < 4; e += 2) {
+                            latent::unpair(latent::fma2(latent::pair(c[t][h][e], c[t][h][e + 1]), sl2, up2), c[t][h][e], c[t][h][e + 1]);
+                            c[t][h][e] = exp2_(c[t][h][e]);
+                            c[t][h][e + 1] = exp2_(c[t][h][e + 1]);
+                            sum = latent::add2(sum, latent::pair(c[t][h][e], c[t][h][e + 1]));
                         }
                         b[t][h][0] = transposed(latent::pack_weights<FP16>(c[t][h][0], c[t][h][1]));
                         b[t][h][1] = transposed(latent::pack_weights<FP16>(c[t][h][2], c[t][h][3]));
                     }
+                    latent::unpair(sum, l[h][0], l[h][1]);
                 }
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
@@ -671,6 +672,7 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
             for (int h = 0; h < RW; ++h)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
+                    m[h][f] *= sl;  // in units of log2 from here on
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) l[h][f] += __shfl_xor_sync(FULL, l[h][f], x);
                     if (top == 0) {
