@@ -758,8 +758,10 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
 
 constexpr int JW = 16;  // warps of a joining CTA
 
-// Joins the parts of a cut unit: the CTAs of all beginnings of parts that lie within it share its rows.  A row's parts are divided
-// among as many warps as there are for it; a lane has channels 4 lane .. 4 lane + 3 and those 128 further on.
+// Joins the parts of a cut unit: the CTAs of all beginnings of parts that lie within it share its rows; a unit of 64 rows with few of
+// them has up to four CTAs for each, 16 rows a CTA (16 sequences of 64 tokens: this launch 13 -> 7 us; with up to 32 rows the CTAs
+// without work cost as much as it gives).  A row's parts are divided among as many warps as there are
+// for it; a lane has channels 4 lane .. 4 lane + 3 and those 128 further on.
 template <bool FP16, int DP>
 __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
     constexpr int V = (DP + 127) / 128;
@@ -775,12 +777,15 @@ __global__ void __launch_bounds__(JW * 32) kda_kv_join_kernel(const DecodeP p) {
     const int64_t rem = c.tiles + START - (c.off - nth * c.per);
     const int parts = 1 + (int)((rem + c.per - 1) / c.per), g0 = g - nth - 1;  // the first part is CTA g0's
     const int total = c.nq * p.G, nrb = (total + p.block - 1) / p.block, hk = c.u / nrb, r0 = (c.u - hk * nrb) * p.block;
-    const int rows = min(p.block, total - r0), share = parts - 1;  // rows nth, nth + share, ... are this CTA's
-    const int mine = rows > nth ? (rows - nth + share - 1) / share : 0;
+    const int rows = min(p.block, total - r0);
+    const int ways = min((int)gridDim.y, (rows + JW * (parts - 1) - 1) / (JW * (parts - 1)));  // CTAs for each beginning
+    if (blockIdx.y >= ways) return;
+    const int share = (parts - 1) * ways, turn = nth * ways + blockIdx.y;
+    const int mine = rows > turn ? (rows - turn + share - 1) / share : 0;  // rows turn, turn + share, ... are this CTA's
     int per_row = 1;  // warps of a row
     while (per_row * 2 * mine <= JW && per_row * 2 <= parts) per_row *= 2;
     for (int first = 0; first < mine; first += JW / per_row) {
-        const int row = nth + (first + warp / per_row) * share, k = warp % per_row;
+        const int row = turn + (first + warp / per_row) * share, k = warp % per_row;
         const bool here = row < rows;
         auto at = [&](int i) { return ((int64_t)(g0 + i) * 2 + (i == 0)) * p.block + row; };
         float m = -INFINITY, sum = 0.f;
@@ -886,7 +891,7 @@ int launch_as(DecodeP p, cudaStream_t st) {
     if (allow_smem(k, prepared) == cudaSuccess) dependent_launch(k, dim3((unsigned)p.groups), C::NT, C::SMEM, st, p, map);
     int rc = launch_result("kda_kv_decode_kernel launch");
     if (rc == KDA_OK && p.groups > 1) {
-        dependent_launch(kda_kv_join_kernel<FP16, DP>, dim3((unsigned)p.groups - 1), JW * 32, 0, st, p);
+        dependent_launch(kda_kv_join_kernel<FP16, DP>, dim3((unsigned)p.groups - 1, p.block > 32 ? p.block / JW : 1), JW * 32, 0, st, p);
         rc = launch_result("kda_kv_join_kernel launch");
     }
     return rc;
