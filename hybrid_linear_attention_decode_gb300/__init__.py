@@ -802,7 +802,7 @@ class Rope:
     def c(self) -> _Rope:
         """The C struct of the tensor as it is now (made again when anything that goes into it has changed)."""
         t = self.turns
-        key = (t.data_ptr(), t.shape, t.dtype, self.offset, self.interleaved, self.scale)
+        key = (t.data_ptr(), t.shape, t.stride(), t.dtype, self.offset, self.interleaved, self.scale)
         kept = self.__dict__.get("_kept")
         if kept is not None and kept[0] == key:
             return kept[1]

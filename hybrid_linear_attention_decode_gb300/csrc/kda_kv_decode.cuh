@@ -11,15 +11,17 @@
 // so that a captured launch follows its lengths.  A unit that one CTA holds whole is written at once; one that is cut leaves
 // normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
-// A CTA (one on each multiprocessor) has a ring of tiles in shared memory, 192 KB at most:
-//   warp 8     walks the list: what a unit is and its queries into a ring of two, its tiles by TMA.  A box is one head's
+// A CTA has a producing and four consuming warps, two CTAs a multiprocessor; with 64 rows or 256 channels eight consuming warps, one
+// CTA.  It has a ring of tiles in shared memory:
+//   producer   walks the list: what a unit is and its queries into a ring of two, its tiles by TMA.  A box is one head's
 //              keys and values of a page (or of a tile's tokens), all channels: 4 to 16 KB.  (Boxes of 16 tokens x 64 channels,
 //              2 KB, reached 4.4 TB/s of 6.7.)
-//   warps 0-7  take tiles in turn, each the whole tile and 8 or 16 rows of queries (two or four warps share a tile where there
+//   consumers  take tiles in turn, each the whole tile and 8 or 16 rows of queries (two or four warps share a tile where there
 //              are more).  S^T = K Q^T and O^T += V^T P^T by m16n8k16 products: tokens and channels fill the 16 rows of
 //              the operand that comes from shared memory, query rows the 8 columns, so that groups of 4 to 8 heads waste
 //              little; S^T becomes P^T by a register transposition.  The tensor work is a small part of the time that
-//              the bytes take (16 KB in 715 cycles; 64 products of 2 cycles), and a tcgen05 tile has 64 rows at least.
+//              the bytes take (16 KB in 715 cycles; 64 products of 2 cycles), and a tcgen05 tile has 64 rows at least.  Units
+//              of 64 rows are bound by it: 64 % of the copy's rate, where units of up to 32 rows reach 98 (64 sequences of 9000).
 // Each warp keeps its own maximum and sums; they meet when the unit's part ends, in shared memory.  The maximum is raised only by
 // more than kRaise, by a vote; until then nothing is exchanged or rescaled.
 //
@@ -46,9 +48,8 @@ using latent::exp2_;
 using latent::kBias;
 using latent::kRaise;
 
-// CW: consuming warps of a CTA, 8 / CW CTAs on a multiprocessor.
-template <int DP, int CW>
-constexpr int kTile = DP == 256 ? 16 : (CW >= 4 ? 4096 : 2048) / DP;  // tokens
+template <int DP>
+constexpr int kTile = 4096 / DP;  // tokens
 
 struct Cut {  // where a CTA's part of the list begins: place `off` of unit u of sequence b, which has nq queries from c0 on and
               // units of `tiles` tiles; places of a whole part
@@ -282,9 +283,10 @@ struct Part {
     int32_t keep_scores;
 };
 
+// CW: consuming warps of a CTA, 8 / CW CTAs on a multiprocessor.
 template <int DP, int RW, int RG, int CW>
 struct Config {
-    static constexpr int TILE = kTile<DP, CW>, CH = DP / 64, MT = TILE / 16;
+    static constexpr int TILE = kTile<DP>, CH = DP / 64, MT = TILE / 16;
     static constexpr int STAGE = TILE * DP * 4;            // bytes of a tile: keys and values
     static constexpr int MERGE = CW * 64 * 8 * 4;          // bytes where warps' outputs meet, one of two: 64 channels of 8 rows
     // Threads: the consumers, the producer, and with eight consumers three idle warps that make the producer's warpgroup whole
@@ -615,8 +617,10 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                             y = fmaxf(y, __shfl_xor_sync(FULL, y, 8));
                             y = fmaxf(y, __shfl_xor_sync(FULL, y, 16));
                             y = fmaxf(y, m[h][f]);
+                            // a score past what fp32 holds: all weights NaN, or none yet
+                            if (fabsf(y * sl) == INFINITY) y = y > 0.f ? NAN : -INFINITY;
                             const float z = y == -INFINITY ? 1.f : exp2_((m[h][f] - y) * sl);
-                            m[h][f] = y * sl == INFINITY ? NAN : y;  // a score past fp32 makes all weights NaN
+                            m[h][f] = y;
                             l[h][f] *= z;
 #pragma unroll
                             for (int k = 0; k < DP / 16; ++k) {
@@ -902,7 +906,7 @@ int launch_rows(const DecodeP &p, cudaStream_t st) {
     switch (p.block) {
         case 8: return launch_as<FP16, DP, 1, 1, CW, WHOLE>(p, st);
         case 16: return launch_as<FP16, DP, 2, 1, CW, WHOLE>(p, st);
-        case 32: return launch_as<FP16, DP, 2, 2, CW < 4 ? 4 : CW, WHOLE>(p, st);
+        case 32: return launch_as<FP16, DP, 2, 2, CW, WHOLE>(p, st);
         default: return launch_as<FP16, DP, 2, 4, 8, WHOLE>(p, st);
     }
 }

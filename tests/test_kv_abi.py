@@ -219,3 +219,12 @@ def test_views_are_the_pages():
     assert key is c.kv() and (key.layers, key.num_pages) == (2, 3)
     c.data.transpose_(0, 1)
     assert (c.kv().layers, c.kv().num_pages) == (3, 2) and c.c().rank == 4 * 52
+
+
+def test_rope_notices_strides():
+    turns = torch.arange(64)
+    r = kda.Rope(turns[:16])
+    assert r.c().dim == 32 and r.c() is r.c()
+    r.turns = turns[::2][:16]  # the same address and shape
+    with pytest.raises(ValueError, match="contiguous"):
+        r.c()

@@ -232,6 +232,41 @@ def test_scales(dtype, scale):
     compare(p, q, [1] * 3, out, lse, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens", [1, 7, 16])
+def test_scores_past_fp32_by_the_scale(dtype, tokens):
+    """Products that fp32 holds, scores that it does not: +infinity makes a query NaN, -infinity weighs nothing."""
+    d, n = 64, 100
+    p = Pages([n, n, n, n], 1, d, 16, dtype=dtype)
+    for b, signs in enumerate(("-", "-0", "-+", "0")):  # of the keys, in turn; a key is 0 or +-(6e4, 0, ...)
+        pid, slot = p.places(b)
+        for j in range(n):
+            c = signs[j % len(signs)] if j < n - tokens else signs[-1]
+            p.cache.keys[0, pid[j], 0, slot[j]] = 0
+            p.cache.keys[0, pid[j], 0, slot[j], 0] = {"-": -6e4, "0": 0.0, "+": 6e4}[c]
+    q = torch.zeros(4 * tokens, 4, d, dtype=dtype, device=DEV)
+    q[:, :, 0] = 6e4
+    out, lse, st = decode(p, q, [tokens] * 4, scale=1e30)  # 3.6e9 * 1e30
+    assert int(st) == 0
+    out, lse = out.view(4, tokens, 4, d), lse.view(4, tokens, 4)
+    assert bool((out[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+    assert bool(out[2].isnan().all()) and bool(lse[2].isnan().all())
+    for b in (1, 3):  # weights of the zero scores are equal
+        pid, slot = p.places(b)
+        zero = p.cache.keys[0, pid, 0, slot, 0] == 0
+        for t in range(tokens):
+            seen = zero.clone()
+            seen[n - tokens + t + 1:] = False
+            v = p.cache.values[0, pid, 0, slot].to(F64)[seen]
+            k = int(seen.sum())
+            # weights rounded to the type and exponentials of 2^-22, a sum of k terms, one rounding
+            u = torch.finfo(dtype).eps / 2
+            tol = u * v.mean(0).abs() + (u + 2.0 ** -20 + k * 2.0 ** -24) * v.abs().mean(0) + torch.finfo(dtype).smallest_normal
+            for h in range(4):
+                check(out[b, t, h], v.mean(0), tol)
+                assert abs(float(lse[b, t, h]) - math.log(k)) <= 2.0 ** -20 + 4 * 2.0 ** -24 * math.log(k)
+
+
 def test_long_tail_of_small_weights():
     """One large weight whose value is near zero, and 30000 of e^-20 of it that make up the output."""
     for dtype in (torch.float16, torch.bfloat16):
