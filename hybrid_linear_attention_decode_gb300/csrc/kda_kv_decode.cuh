@@ -6,15 +6,15 @@
 // for the nq H / heads rows (query token, head of the group) that share a key-value head.  Keys and values are read once,
 // 4 head_dim bytes a token and head against 4 head_dim operations for each row: with up to 64 rows bound by the bytes.
 //
-// Split: a unit is one (sequence, key-value head, block of rows); its tiles of 16 KB (64, 32 or 16 tokens) stand in one list
+// Split: a unit is one (sequence, key-value head, block of rows); its tiles of 16 or 24 KB (64, 32 or 16 tokens) stand in one list
 // with those of all other units, and each CTA takes an equal, contiguous part of the list, found on the device from lens,
 // so that a captured launch follows its lengths.  A unit that one CTA holds whole is written at once; one that is cut leaves
 // normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
-// A CTA has a producing and four consuming warps, two CTAs a multiprocessor; with 64 rows or 256 channels eight consuming warps, one
+// A CTA has a producing and four consuming warps, two CTAs a multiprocessor; with 64 rows or more than 128 channels eight consuming warps, one
 // CTA.  It has a ring of tiles in shared memory:
 //   producer   walks the list: what a unit is and its queries into a ring of two, its tiles by TMA.  A box is one head's
-//              keys and values of a page (or of a tile's tokens), all channels: 4 to 16 KB.  (Boxes of 16 tokens x 64 channels,
+//              keys and values of a page (or of a tile's tokens), all channels: 4 to 24 KB.  (Boxes of 16 tokens x 64 channels,
 //              2 KB, reached 4.4 TB/s of 6.7.)
 //   consumers  take tiles in turn, each the whole tile and 8 or 16 rows of queries (two or four warps share a tile where there
 //              are more).  S^T = K Q^T and O^T += V^T P^T by m16n8k16 products: tokens and channels fill the 16 rows of
@@ -48,8 +48,10 @@ using latent::exp2_;
 using latent::kBias;
 using latent::kRaise;
 
+// Tokens of a tile: 16 KB (24 for 192 channels: one in 12 KB cost the producer as much as one in 16, 343 us instead of 276 for 64
+// sequences of 500 to 8192 tokens and 8 key-value heads; taken as 256 channels with 64 zeros 349).
 template <int DP>
-constexpr int kTile = 4096 / DP;  // tokens
+constexpr int kTile = DP == 192 ? 32 : 4096 / DP;
 
 struct Cut {  // where a CTA's part of the list begins: place `off` of unit u of sequence b, which has nq queries from c0 on and
               // units of `tiles` tiles; places of a whole part
@@ -911,13 +913,14 @@ int launch_rows(const DecodeP &p, cudaStream_t st) {
     }
 }
 
-inline int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+inline int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
 
 template <bool FP16, bool WHOLE>
 int launch_decode_of(const DecodeP &p, cudaStream_t st) {
     switch (padded(p.a.c.d)) {
         case 64: return launch_rows<FP16, 64, 4, WHOLE>(p, st);
         case 128: return launch_rows<FP16, 128, 4, WHOLE>(p, st);
+        case 192: return launch_rows<FP16, 192, 8, WHOLE>(p, st);
         default: return launch_rows<FP16, 256, 8, WHOLE>(p, st);
     }
 }

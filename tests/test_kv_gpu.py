@@ -73,6 +73,21 @@ def test_one_token(dtype, kv, G, d, page):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("d,page", [(136, 16), (160, 64), (184, 32), (192, 16), (192, 64), (200, 128)])
+@pytest.mark.parametrize("kv,G,tokens", [(8, 1, 1), (2, 4, 3), (1, 8, 4), (3, 12, 5)])
+def test_wide_heads(d, page, kv, G, tokens):
+    """Heads between 128 and 256 channels, each number of rows of a unit, sums of weights."""
+    lens = [tokens, 31, 32, 33, 700, 0, 95, 5000]
+    nq = [tokens] * len(lens)
+    p = Pages(lens, kv, d, page, stats=True, seed=d)
+    p.poison()
+    sums = p.cache.weights.clone()
+    q = queries(sum(nq), kv * G, d, torch.bfloat16, strided=True)
+    out, lse, st = decode(p, q, nq, decay=0.5)
+    compare(p, q, nq, out, lse, sums=sums, decay=0.5)
+    assert int(st) == 0
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("kv,G,d,page,tokens", [(8, 4, 128, 16, 5), (2, 8, 64, 64, 3), (1, 16, 128, 32, 8), (1, 5, 96, 64, 64),
                                                 (2, 1, 256, 16, 7), (1, 33, 72, 64, 4), (4, 2, 128, 64, 20)])
