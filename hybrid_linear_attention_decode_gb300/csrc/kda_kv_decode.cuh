@@ -14,8 +14,8 @@
 // A CTA has a producing and four consuming warps, two CTAs a multiprocessor; with 64 rows or more than 128 channels eight consuming warps, one
 // CTA.  It has a ring of tiles in shared memory:
 //   producer   walks the list: what a unit is and its queries into a ring of two, its tiles by TMA.  A box is one head's
-//              keys and values of a page (or of a tile's tokens), all channels: 4 to 24 KB.  (Boxes of 16 tokens x 64 channels,
-//              2 KB, reached 4.4 TB/s of 6.7.)
+//              keys or values of a page (or of a tile's tokens), all channels.  (With boxes of 16 tokens x 64 channels heads of
+//              128 were read at 4.4 TB/s of 6.7.)
 //   consumers  take tiles in turn, each the whole tile and 8 or 16 rows of queries (two or four warps share a tile where there
 //              are more).  S^T = K Q^T and O^T += V^T P^T by m16n8k16 products: tokens and channels fill the 16 rows of
 //              the operand that comes from shared memory, query rows the 8 columns, so that groups of 4 to 8 heads waste
