@@ -855,7 +855,7 @@ def kda_kv_append(cache: KvCache, layer: int, pt: PageTable, rows, cu_tokens, k,
 
 def kda_kv_decode_workspace_bytes(cache: KvCache, H: int, n: int, max_tokens: int, max_slots: int = 0) -> int:
     """Bytes of workspace kda_kv_decode needs on the cache's device (0 for unsupported sizes); max_slots: a bound on the sum
-    of the call's lens where weights are added up."""
+    of the call's lens, 1 or more, where weights are added up, else 0."""
     with torch.cuda.device(cache.data.device if cache.data.is_cuda else -1):
         return int(load_library().kda_kv_decode_workspace_bytes(cache.kv(), int(H), int(n), int(max_tokens),
                                                                 int(max_slots)))

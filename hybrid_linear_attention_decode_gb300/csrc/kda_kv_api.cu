@@ -261,6 +261,8 @@ int kda_kv_decode(const kda_kv_cache *cache, int32_t layer, const kda_page_table
     if (add_weights && (!a.c.stats || !(weight_decay >= 0.f && weight_decay <= 1.f)))
         return fail(KDA_ERR_INVALID_ARG, "kv decode: add_weights needs a cache with stats and weight_decay from 0 to 1");
     if (n == 0 || num_tokens == 0) return KDA_OK;
+    if (add_weights && max_slots < 1)  // a workspace for a bound of 0 has no places for sums and scores
+        return fail(KDA_ERR_INVALID_ARG, "kv decode: add_weights needs max_slots of 1 or more, as the workspace was asked for");
     if (!q || !out) return fail(KDA_ERR_INVALID_ARG, "kv decode: q or out is NULL");
     if (!al(q, 16) || !al(out, 16) || (lse && !al(lse, 4)) || (rows && !al(rows, 4)) ||
         (cu_tokens && !al(cu_tokens, 4)) || (tree_mask && !al(tree_mask, 8)) || (dev_status && !al(dev_status, 4)))

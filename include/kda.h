@@ -530,8 +530,8 @@ KDA_API int kda_kv_append(const kda_kv_cache *cache, int32_t layer, const kda_pa
 #define KDA_KV_MAX_HEADS 256
 
 /* Bytes of device workspace kda_kv_decode needs on the current device for these sizes (0 for unsupported ones).  max_slots:
- * 0 when weights are not added up, else a bound on the sum of lens over the call's sequences.  What is enough for some n,
- * max_tokens and max_slots is enough for smaller ones, too. */
+ * 0 when weights are not added up, else a bound on the sum of lens over the call's sequences, 1 or more (also where all
+ * are empty).  What is enough for some n, max_tokens and max_slots is enough for smaller ones, too. */
 KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t H, int32_t n, int32_t max_tokens,
                                              int64_t max_slots);
 
@@ -544,11 +544,11 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  *   out        device [num_tokens][H][head_dim] contiguous, the cache's type, 16-byte aligned
  *   add_weights  1 (a cache with stats): the sum of each cached token of a sequence with queries becomes weight_decay * sum
  *              + the weights that these give it in this call, summed over the query tokens and over the query heads that
- *              share its key-value head.  weight_decay from 0 to 1; max_slots as the workspace was asked for.  Shared pages
- *              (refcount above 1) are never written, so their tokens' sums stay; refcount may not be NULL then.  No table
- *              row may appear twice in such a call.  Sequences whose slots pass max_slots, added up in order, are
- *              flagged (KDA_DEV_BAD_SEQLENS) and leave their sums as they were, their outputs are as always.  A query
- *              whose lse is NaN adds nothing.
+ *              share its key-value head.  weight_decay from 0 to 1; max_slots as the workspace was asked for, 1 or more (a
+ *              call with queries and a bound of 0 is refused).  Shared pages (refcount above 1) are never written, so their
+ *              tokens' sums stay; refcount may not be NULL then.  No table row may appear twice in such a call.  Sequences
+ *              whose slots pass max_slots, added up in order, are flagged (KDA_DEV_BAD_SEQLENS) and leave their sums as
+ *              they were, their outputs are as always.  A query whose lse is NaN adds nothing.
  * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so do the
  * queries of a sequence with a bad row or length (flagged); a bad page's tokens read as zero keys and values (flagged).
  * Sequences with bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Tokens that a query does not see
