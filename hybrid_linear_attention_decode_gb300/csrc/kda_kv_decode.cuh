@@ -502,9 +502,17 @@ __global__ void __launch_bounds__(Config<DP, RW, RG, CW>::NT, 8 / CW)
                 for (int h = 0; h < RW; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[k][h][e] = 0.f;
+            // Rows behind the unit's last hold queries of a unit before, perhaps another sequence's.  Nothing is above their
+            // maximum, so that they never have the others' raised; what they come to (0 or NaN) stays in their column of the products
+            // and is not written.
             float m[RW][2], l[RW][2];
 #pragma unroll
-            for (int h = 0; h < RW; ++h) m[h][0] = m[h][1] = -INFINITY, l[h][0] = l[h][1] = 0.f;
+            for (int h = 0; h < RW; ++h)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    m[h][f] = w.r0 + rg * 8 * RW + h * 8 + 2 * quad + f < total ? -INFINITY : INFINITY;
+                    l[h][f] = 0.f;
+                }
             const bool drafts = s.nq > 1 || a.tree;
             const int draft0 = drafts ? s.len - s.nq : s.len;  // first token that not all rows see
 
