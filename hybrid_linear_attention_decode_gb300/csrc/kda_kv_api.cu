@@ -70,12 +70,14 @@ int check_rope(const kda_rope *r, int32_t D, RopeArgs *o) {
     return KDA_OK;
 }
 
-// theta / 2 pi as a fraction of a turn times 2^64, to the nearest multiple that 53 bits hold.
+// theta / 2 pi as a fraction of a turn times 2^64, whole turns left out, rounded to a whole number.  The quotient's 53 bits reach
+// below 2^-64 of a turn only where it is below 2^-11; there rounding (and not cutting off) halves the error.  Above, y is a whole
+// number already, so that it never becomes 2^64.
 uint64_t turns_of(double theta) {
     double x = theta / 6.283185307179586476925286766559;
     x -= floor(x);                     // whole turns a position do nothing
     const double y = ldexp(x, 64);     // below 2^64: x is below 1
-    return (uint64_t)y;
+    return (uint64_t)round(y);
 }
 
 }  // namespace

@@ -465,7 +465,8 @@ KDA_API int kda_kv_cache_pages(const kda_kv_cache *cache, kda_latent_cache *out)
  * The pairs are the channels offset + i and offset + dim/2 + i (interleaved 0: halves), or offset + 2i and offset + 2i + 1
  * (interleaved 1); the other channels of a head stay as they are.  turns[i] is theta_i as a fraction of a full turn, times
  * 2^64: position * turns[i] modulo 2^64 is then the exact fraction of a turn at any int32 position, so far positions are
- * as precise as near ones (the error of theta_i itself, 2^-53 of it, is all that grows).
+ * as precise as near ones.  All that grows with the position is the error of turns[i] itself: theta_i / 2 pi in 64-bit floating
+ * point (two roundings, 2^-52 of it), then half a unit, 2^-65 of a turn (2^-34 of a turn at position 2^31).
  */
 typedef struct kda_rope {
     int32_t dim, offset;       /* dim even, 2 to 256 */
