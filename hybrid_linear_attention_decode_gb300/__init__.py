@@ -783,7 +783,8 @@ class Rope:
              factor: float = 1.0, original: float = 0.0, low: float = 1.0, high: float = 32.0, scale: float = 1.0,
              device="cuda") -> "Rope":
         """theta_i = base^(-2i / dim), changed for long contexts as enum kda_rope_scaling in kda.h says: "none", "linear",
-        "ntk" or "parts" (by `low` and `high` turns within the `original` length)."""
+        "ntk" or "parts" (by `low` and `high` turns within the `original` length; for a ramp over the pairs' indices
+        give the frequencies to :meth:`of`)."""
         if scaling not in _SCALING:
             _raise(f"scaling must be one of {', '.join(_SCALING)}")
         turns = torch.empty(max(dim // 2, 0), dtype=torch.int64)
@@ -867,7 +868,9 @@ def kda_kv_decode(cache: KvCache, layer: int, pt: PageTable, rows, cu_tokens, ma
     """Grouped-query attention of the newest tokens over the paged cache; see include/kda.h.  q [T, H, head_dim] (token and
     head axes may be strided), out [T, H, head_dim], lse fp32 [T, H] or None; rows, cu_tokens, tree_mask as for
     kda_latent_decode.  weight_decay: not None adds the call's weights to the cache's sums, after multiplying these
-    with it; max_slots then bounds the sum of the call's lens (None: the pool's pages full once).  workspace uint8,
+    with it; max_slots, 1 or more, then bounds the sum of the call's lens.  None stands for the pool's pages full once, which
+    lens pass where sequences share many pages: sequences past the bound are flagged and keep their old sums, so such a program
+    gives a bound of its own (and one with a large pool a closer one, as the workspace grows with it).  workspace uint8,
     kda_kv_decode_workspace_bytes() bytes for the same max_slots."""
     name = "kda_kv_decode"
     adds = weight_decay is not None

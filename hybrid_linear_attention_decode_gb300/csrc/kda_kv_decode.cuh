@@ -4,7 +4,7 @@
 //   s_j = scale q . k_j,   o = sum_j softmax(s)_j v_j
 //
 // for the nq H / heads rows (query token, head of the group) that share a key-value head.  Keys and values are read once,
-// 4 head_dim bytes a token and head against 4 head_dim operations for each row: with up to 64 rows bound by the bytes.
+// 4 head_dim bytes a token and head against 4 head_dim operations for each row: with up to 32 rows bound by the bytes.
 //
 // Split: a unit is one (sequence, key-value head, block of rows); its tiles of 16 or 24 KB (64, 32 or 16 tokens) stand in one list
 // with those of all other units, and each CTA takes an equal, contiguous part of the list, found on the device from lens,
@@ -12,7 +12,10 @@
 // normalised fp32 parts and the log2 of their sums in the workspace, which a second launch joins.
 //
 // A CTA has a producing and four consuming warps, two CTAs a multiprocessor; with 64 rows or more than 128 channels eight consuming warps, one
-// CTA.  It has a ring of tiles in shared memory:
+// CTA.  With heads of 128, 64 sequences of 500 to 8192 and 1000 of 10 to 200 tokens on 8 key-value heads, two CTAs against one of
+// eight: 8 rows 191 and 108 us against 189 and 187; 16 rows 194 and 202 against 202 and 327; 32 rows 207 and 253 against 227
+// and 371 (heads of 64: 100 and 95 against 102 and 165; 103 and 175 against 111 and 251; 110 and 195 against 126 and 278).
+// It has a ring of tiles in shared memory:
 //   producer   walks the list: what a unit is and its queries into a ring of two, its tiles by TMA.  A box is one head's
 //              keys or values of a page (or of a tile's tokens), all channels.  (With boxes of 16 tokens x 64 channels heads of
 //              128 were read at 4.4 TB/s of 6.7.)
@@ -24,6 +27,13 @@
 //              of 64 rows are bound by it: 64 % of the copy's rate, where units of up to 32 rows reach 98 (64 sequences of 9000).
 // Each warp keeps its own maximum and sums; they meet when the unit's part ends, in shared memory.  The maximum is raised only by
 // more than kRaise, by a vote; until then nothing is exchanged or rescaled.
+//
+// Weights are rounded to the cache's type for the second product, as both operands of a product have one type.  Each is off by
+// half a step at most, with either sign, so that an output is off by about as much as by its own rounding: 0.0023 of the outputs' size
+// in bf16 where rounding the outputs alone gives 0.0017 (fp16 0.00029, 0.00021).  Weights in two parts (a second product with what
+// the first rounding left) give 0.0017, at the same time where long sequences are bound by bytes, but 1000 sequences of 10 to 200
+// tokens take 117 instead of 108 us (230 instead of 203 with 16 rows), trees of 20 rows 131 instead of 122, 64 rows 205 instead of 157.
+// The sums of weights are of the fp32 scores.
 //
 // With add_weights the scores (fp32, in units of log2) also go to the workspace, and a third launch, when the rows' sums are
 // known, adds exp(s - lse) to the pages: 4 bytes written and read for each row and token, mostly in L2, where reading the keys

@@ -516,7 +516,9 @@ struct Variant {
 // Clusters: 1,024 threads a CTA where a multiprocessor has one CTA at most.  Single CTAs: the steps of a unit are bound by
 // barriers and latencies, so that more and smaller CTAs are better where rows are short: 64 rows of 2,112 tokens in 4 layers
 // and 8 heads took 39 us with 128 threads, 48 with 256 (and 57 with one warp); 6 of 2,000 to 8,192 in 8 layers 76 us with 256
-// and 99 with 128.
+// and 99 with 128.  On both sides of SHORT: 64 rows of 3,900 to 4,050 tokens 115 us with 128 threads, 122 with 256; 64 of 4,300 to
+// 4,500 138 and 133; 32 of 6,000 to 8,000 cut to 512 164 and 122.  Against the rule: 12 rows of 2,000 to 4,000 cut to 1,024, 90 and
+// 67, where there are too few units for the smaller CTAs to fill the GPU.
 inline Variant variant(int64_t units, int C, int64_t cap) {
     if (C > 1 && units * C <= current_device_sms()) return {kda_kv_evict_kernel<1024, true>, 0, 1024};
     if (C > 1) return {kda_kv_evict_kernel<256, true>, 1, 256};

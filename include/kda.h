@@ -481,7 +481,9 @@ enum kda_rope_scaling {
     KDA_ROPE_LINEAR = 1,       /* theta_i / factor */
     KDA_ROPE_NTK = 2,          /* base * factor^(dim / (dim - 2)) in the place of base */
     KDA_ROPE_PARTS = 3         /* with r = original theta_i / 2 pi (turns within the trained length) and
-                                * g = (r - low) / (high - low) clamped to 0..1:  theta_i (g + (1 - g) / factor) */
+                                * g = (r - low) / (high - low) clamped to 0..1:  theta_i (g + (1 - g) / factor).  The ramp is
+                                * linear in the turns; models whose ramp is linear in the pair's index i give their
+                                * frequencies to kda_rope_turns_of() one by one */
 };
 
 /* Host only: turns (host [dim / 2]) of a base and a scaling; factor at least 1, 0 < original and 0 <= low < high for
@@ -498,8 +500,9 @@ KDA_API int kda_rope_turns_of(int32_t count, const double *theta, uint64_t *turn
  *   positions  device [num_tokens] int32, any values
  *   x, out     device, of one type (dtype, enum kda_elem_type), with token and head strides in elements (multiples of 8),
  *              16-byte aligned.  out may be x itself (the same address and strides): then only the rotated channels are
- *              written; else out gets all D channels and may not overlap x.
- * The angle is exact to 2^-32 of a turn, sine, cosine and products fp32, rounded once to the type.
+ *              written; else out gets all D channels and may not overlap x.  Rows of out may not overlap one another.
+ * The angle's fraction of a turn is taken to 2^-32 and then rounded to fp32, which is off by up to 2^-26 of a turn near half a
+ * turn and by less near none; sine, cosine and products are fp32, rounded once to the type.
  * D a multiple of 8 up to 1024, H 1 to 1024, offset + dim <= D.
  */
 KDA_API int kda_rope_apply(const kda_rope *rope, int32_t dtype, int64_t num_tokens, int32_t H, int32_t D,
@@ -515,8 +518,9 @@ KDA_API int kda_rope_apply(const kda_rope *rope, int32_t dtype, int64_t num_toke
  *              head strides (elements, multiples of 8), 16-byte aligned: parts of one projection's output, for example
  *   positions  device [num_tokens] int32; NULL only without rope and stats
  *   q_out      device [num_tokens][H][head_dim] contiguous, 16-byte aligned; or q itself (its address, with contiguous
- *              strides).  Queries of all tokens before cu_tokens[n] are rotated, those of padding entries and of sequences
- *              with a bad row or page, too; rows behind cu_tokens[n] and those of flagged cu_tokens are left as they were.
+ *              strides).  The queries of all tokens from cu_tokens[0] to before cu_tokens[n] are rotated, those of padding
+ *              entries and of sequences with a bad row or page, too; rows before and behind them and those of flagged
+ *              cu_tokens are left as they were.
  * rope->offset + rope->dim <= head_dim; H 1 to 1024.  No two tokens of a call may go to the same place.
  */
 KDA_API int kda_kv_append(const kda_kv_cache *cache, int32_t layer, const kda_page_table *pt, int32_t n,
@@ -543,6 +547,7 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  *   q          device [num_tokens][H][head_dim], the cache's type, at the given token and head strides (elements,
  *              multiples of 8), 16-byte aligned; H a multiple of the cache's heads
  *   out        device [num_tokens][H][head_dim] contiguous, the cache's type, 16-byte aligned
+ * out, lse and the workspace overlap nothing else that the call reads or writes.
  *   add_weights  1 (a cache with stats): the sum of each cached token of a sequence with queries becomes weight_decay * sum
  *              + the weights that these give it in this call, summed over the query tokens and over the query heads that
  *              share its key-value head.  weight_decay from 0 to 1; max_slots as the workspace was asked for, 1 or more (a
@@ -550,6 +555,11 @@ KDA_API size_t kda_kv_decode_workspace_bytes(const kda_kv_cache *cache, int32_t 
  *              tokens' sums stay; refcount may not be NULL then.  No table row may appear twice in such a call.  Sequences
  *              whose slots pass max_slots, added up in order, are flagged (KDA_DEV_BAD_SEQLENS) and leave their sums as
  *              they were, their outputs are as always.  A query whose lse is NaN adds nothing.
+ * max_tokens decides for all sequences of a call how many query rows of a key-value head are worked on together: 8, 16, 32 or
+ * 64, as few as hold (H / heads) max_tokens rows, or 64.  Up to 32 that costs a sequence with fewer queries little; with 64 it
+ * pays for products of rows that it does not have.  64 sequences of 500 to 8192 tokens with one query each, 32 query and 8
+ * key-value heads of 128: 190 us with max_tokens 1, 192 with 8, 301 from 9 on.  With 16 queries for one of them: 309 us in one
+ * call, 213 in a call for the 63 and one for it; with 5 queries 193 and 206.
  * A query that sees nothing (an empty sequence, a padding entry, an empty mask) gets out 0 and lse -inf, and so do the
  * queries of a sequence with a bad row or length (flagged); a bad page's tokens read as zero keys and values (flagged).
  * Sequences with bad cu_tokens and rows of out behind cu_tokens[n] are left as they were.  Tokens that a query does not see
